@@ -30,7 +30,7 @@ inline bool per_token(const lbq_weights* w, int64_t M) {
 }
 
 inline bool fmt_known(int32_t fmt) {
-  return fmt == LBQ_TERN5 || fmt == LBQ_SIGN1 || fmt == LBQ_Q2RHT;
+  return fmt == LBQ_TERN5 || fmt == LBQ_SIGN1 || fmt == LBQ_Q2RHT || lbq::is_q4(fmt);
 }
 
 // Checks a weight descriptor; fills L on success.
@@ -42,6 +42,8 @@ lbq_status check_weights(const lbq_weights* w, Layout* L) {
   if (!w->codes) return LBQ_ERR_ARG;
   if (!aligned(w->codes, 16)) return LBQ_ERR_ALIGN;
   if (w->code_stride < L->code_stride || w->code_stride % 16) return LBQ_ERR_SHAPE;
+  // (4-bit: the kernels index rows and K with 32 bits, offsets with 64)
+  if (lbq::is_q4(w->fmt) && (w->N > (int64_t{1} << 28) || w->K > (int64_t{1} << 28))) return LBQ_ERR_SHAPE;
   if (w->fmt == LBQ_TERN5) {
     if (w->scales || w->scale_stride != 0) return LBQ_ERR_ARG;
   } else {
@@ -130,6 +132,24 @@ lbq_status check_batch(const lbq_product* ps, int32_t n) {
 
 namespace {
 thread_local int g_last_cuda_error = 0;
+
+// Limits of the expert calls: slots and rows are counted in 32 bits on the device.
+constexpr int64_t kMaxSlots = int64_t{1} << 30;
+constexpr int64_t kMaxWidth = int64_t{1} << 24;
+constexpr int32_t kMaxTopk = 1024;
+
+lbq_status check_routing(int64_t T, int32_t topk, int32_t E) {
+  if (T < 1 || topk < 1 || topk > kMaxTopk || E < 1 || E > LBQ_MAX_EXPERTS) return LBQ_ERR_SHAPE;
+  return T > kMaxSlots / topk ? LBQ_ERR_SHAPE : LBQ_OK;
+}
+
+// E matrices of one format and shape behind one another (4-bit formats).
+lbq_status check_expert_weights(const lbq_weights* w, int32_t E, Layout* L) {
+  const lbq_status st = check_weights(w, L);
+  if (st != LBQ_OK) return st;
+  if (!lbq::is_q4(w->fmt)) return LBQ_ERR_FORMAT;
+  return E < 1 || E > LBQ_MAX_EXPERTS ? LBQ_ERR_SHAPE : LBQ_OK;
+}
 }  // namespace
 
 lbq_status lbq_cuda_status(cudaError_t e) {
@@ -146,7 +166,7 @@ void for_each_batch_launch(const lbq_product* ps, int32_t n, F fn) {
   bool one_format = true;
   for (int32_t i = 1; i < n; ++i) one_format = one_format && ps[i].w.fmt == ps[0].w.fmt;
   std::vector<lbq_product> sub;
-  for (const int32_t fmt : {LBQ_TERN5, LBQ_SIGN1, LBQ_Q2RHT}) {
+  for (const int32_t fmt : {LBQ_TERN5, LBQ_SIGN1, LBQ_Q2RHT, LBQ_Q4G32, LBQ_Q4G128}) {
     const lbq_product* list = ps;
     int32_t count = n;
     if (!one_format) {
@@ -313,6 +333,7 @@ lbq_status lbq_gemv_batch_plan(const lbq_product* ps, int32_t n, int32_t ctas, i
   if (st != LBQ_OK) return st;
   for (int32_t i = 1; i < n; ++i)
     if (ps[i].w.fmt != ps[0].w.fmt) return LBQ_ERR_ARG;
+  if (lbq::is_q4(ps[0].w.fmt)) return LBQ_ERR_FORMAT;  // not scheduled in unit-slices
   *total = lbq_gemv_batch_plan_list(ps, n, ctas, pieces, bound);
   return LBQ_OK;
 }
@@ -333,6 +354,83 @@ lbq_status lbq_gemm(const lbq_weights* w, const uint16_t* X, int64_t M, const in
     return LBQ_OK;
   }
   return from_cuda(lbq_launch_gemm(w, X, M, D, Y, workspace, as_stream(stream)));
+}
+
+lbq_status lbq_expert_sort(const void* expert, int32_t id_bytes, int64_t T, int32_t topk, int32_t E,
+                           int32_t* offsets, int32_t* rows, int32_t* slots, void* stream) {
+  if (!expert || !offsets || !rows || !slots || (id_bytes != 4 && id_bytes != 8)) return LBQ_ERR_ARG;
+  lbq_status st = check_routing(T, topk, E);
+  if (st != LBQ_OK) return st;
+  if (!aligned(expert, static_cast<uintptr_t>(id_bytes)) || !aligned(offsets, 4) || !aligned(rows, 4) ||
+      !aligned(slots, 4))
+    return LBQ_ERR_ALIGN;
+  return from_cuda(lbq_launch_expert_sort(expert, id_bytes, T * topk, E, offsets, rows, slots, as_stream(stream)));
+}
+
+lbq_status lbq_expert_dispatch(const uint16_t* X, int64_t T, int64_t K, const int32_t* rows, int32_t topk,
+                               const float* weights, int64_t R, uint16_t* out, void* stream) {
+  if (!X || !rows || !out) return LBQ_ERR_ARG;
+  lbq_status st = check_routing(T, topk, 1);
+  if (st != LBQ_OK) return st;
+  if (R < 1 || R > kMaxSlots || K < 1 || K > kMaxWidth) return LBQ_ERR_SHAPE;
+  if (!aligned(X, 2) || !aligned(out, 2) || !aligned(rows, 4) || !aligned(weights, 4)) return LBQ_ERR_ALIGN;
+  if (overlap(X, 2 * T * K, out, 2 * R * K)) return LBQ_ERR_ARG;
+  return from_cuda(lbq_launch_expert_dispatch(X, rows, weights, T, topk, K, R, out, as_stream(stream)));
+}
+
+lbq_status lbq_expert_combine(const uint16_t* Y, int64_t R, int64_t N, const int32_t* rows, int64_t T,
+                              int32_t topk, const float* weights, uint16_t* out, void* stream) {
+  if (!Y || !rows || !out) return LBQ_ERR_ARG;
+  lbq_status st = check_routing(T, topk, 1);
+  if (st != LBQ_OK) return st;
+  if (R < 1 || R > kMaxSlots || N < 1 || N > kMaxWidth) return LBQ_ERR_SHAPE;
+  if (!aligned(Y, 2) || !aligned(out, 2) || !aligned(rows, 4) || !aligned(weights, 4)) return LBQ_ERR_ALIGN;
+  if (overlap(Y, 2 * R * N, out, 2 * T * N)) return LBQ_ERR_ARG;
+  return from_cuda(lbq_launch_expert_combine(Y, rows, weights, T, topk, N, R, out, as_stream(stream)));
+}
+
+lbq_status lbq_expert_combine_grad(const uint16_t* dout, const uint16_t* Y, int64_t R, int64_t N,
+                                   const int32_t* rows, int64_t T, int32_t topk, const float* weights,
+                                   uint16_t* dY, float* dweights, void* stream) {
+  if (!dout || !Y || !rows || !weights || !dY || !dweights) return LBQ_ERR_ARG;
+  lbq_status st = check_routing(T, topk, 1);
+  if (st != LBQ_OK) return st;
+  if (R < 1 || R > kMaxSlots || N < 1 || N > kMaxWidth) return LBQ_ERR_SHAPE;
+  if (!aligned(dout, 2) || !aligned(Y, 2) || !aligned(dY, 2) || !aligned(rows, 4) || !aligned(weights, 4) ||
+      !aligned(dweights, 4))
+    return LBQ_ERR_ALIGN;
+  const size_t nR = 2 * static_cast<size_t>(R) * N, nT = 2 * static_cast<size_t>(T) * N;
+  const size_t nw = 4 * static_cast<size_t>(T) * topk;
+  if (overlap(dY, nR, Y, nR) || overlap(dY, nR, dout, nT) || overlap(dweights, nw, weights, nw))
+    return LBQ_ERR_ARG;
+  return from_cuda(lbq_launch_expert_combine_grad(dout, Y, rows, weights, T, topk, N, R, dY, dweights,
+                                                  as_stream(stream)));
+}
+
+size_t lbq_expert_workspace_bytes(const lbq_weights* w, int32_t E, int64_t R) {
+  Layout L;
+  if (check_expert_weights(w, E, &L) != LBQ_OK || R < 1 || R > kMaxSlots) return 0;
+  return 0;
+}
+
+lbq_status lbq_expert_gemm(const lbq_weights* w, int32_t E, const uint16_t* X, int64_t T,
+                           const int32_t* offsets, const int32_t* slots, int32_t topk, int64_t R,
+                           uint16_t* Y, void* workspace, size_t workspace_bytes, void* stream) {
+  Layout L;
+  lbq_status st = check_expert_weights(w, E, &L);
+  if (st != LBQ_OK) return st;
+  if (!X || !offsets || !Y) return LBQ_ERR_ARG;
+  if (T < 1 || T > kMaxSlots || R < 1 || R > kMaxSlots || topk < 1 || topk > kMaxTopk) return LBQ_ERR_SHAPE;
+  if (!slots && T < R) return LBQ_ERR_SHAPE;
+  if (!aligned(X, 16) || !aligned(Y, 2) || !aligned(offsets, 4) || !aligned(slots, 4)) return LBQ_ERR_ALIGN;
+  if (overlap(X, 2 * static_cast<size_t>(T) * w->K, Y, 2 * static_cast<size_t>(R) * w->N)) return LBQ_ERR_ARG;
+  const size_t need = lbq_expert_workspace_bytes(w, E, R);
+  if (need) {
+    if (!workspace || workspace_bytes < need) return LBQ_ERR_WORKSPACE;
+    if (!aligned(workspace, 16)) return LBQ_ERR_ALIGN;
+  }
+  const lbq_expert_rows rows = {X, offsets, slots, Y, T, R, topk, E};
+  return from_cuda(lbq_launch_q4_expert_few(w, rows, as_stream(stream)));
 }
 
 }  // extern "C"

@@ -1,0 +1,354 @@
+// expert.cu -- token slots sorted by expert, rows copied to that order and added back.
+//
+// The sort is a stable counting sort in one launch: every warp counts the experts of its
+// own run of slots, the counts become first rows by prefix sums over warps, CTAs (a
+// cluster reads each other's counts through distributed shared memory) and experts, and
+// every warp walks its run again to hand out rows. Row order is slot order within an
+// expert, so the result does not depend on timing. The copies and sums are bound by the
+// bytes of the rows; one CTA a token, 16-byte accesses where the rows allow them.
+#include <cooperative_groups.h>
+
+#include "lbq_common.cuh"
+#include "sm100_async.cuh"
+
+namespace {
+
+using namespace lbq;
+namespace cg = cooperative_groups;
+
+constexpr int kSortThreads = 1024, kSortWarps = kSortThreads / 32;
+constexpr int kSortCluster = 8;
+
+template <typename Id>
+__device__ __forceinline__ int expert_of(const Id* ids, int64_t i, int64_t end, int E) {
+  if (i >= end) return E;
+  const Id v = ids[i];
+  return v >= 0 && v < static_cast<Id>(E) ? static_cast<int>(v) : E;
+}
+
+// Shared memory: hist [warps][E], tot [E], base [E].
+template <typename Id>
+__global__ void __launch_bounds__(kSortThreads, 1)
+    expert_sort_kernel(const Id* __restrict__ ids, int64_t R, int E, int64_t per_warp,
+                       int32_t* __restrict__ offsets, int32_t* __restrict__ rows,
+                       int32_t* __restrict__ slots) {
+  extern __shared__ int32_t sm[];
+  __shared__ int32_t wsum[kSortWarps];
+  int32_t* hist = sm;
+  int32_t* tot = hist + kSortWarps * E;
+  int32_t* base = tot + E;
+  cg::cluster_group cluster = cg::this_cluster();
+  const int C = static_cast<int>(cluster.num_blocks()), rank = static_cast<int>(cluster.block_rank());
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  for (int i = tid; i < kSortWarps * E; i += kSortThreads) hist[i] = 0;
+  __syncthreads();
+  const int64_t w0 = (static_cast<int64_t>(rank) * kSortWarps + warp) * per_warp;
+  const int64_t w1 = w0 + per_warp < R ? w0 + per_warp : R;
+  int32_t* mine = hist + warp * E;
+  for (int64_t i = w0; i < w1; i += 32) {
+    const int e = expert_of(ids, i + lane, w1, E);
+    const unsigned peers = __match_any_sync(0xffffffffu, e);
+    if (e < E && lane == __ffs(peers) - 1) mine[e] += __popc(peers);
+    __syncwarp();
+  }
+  __syncthreads();
+  // each expert's counts of the warps before, and the CTA's total
+  for (int e = tid; e < E; e += kSortThreads) {
+    int32_t run = 0;
+    for (int w = 0; w < kSortWarps; ++w) {
+      const int32_t c = hist[w * E + e];
+      hist[w * E + e] = run;
+      run += c;
+    }
+    tot[e] = run;
+  }
+  cluster.sync();
+  // thread e (E <= kSortThreads): totals of all CTAs, those of the CTAs before this one
+  int32_t all = 0, before = 0;
+  if (tid < E) {
+    for (int c = 0; c < C; ++c) {
+      const int32_t v = *cluster.map_shared_rank(tot + tid, c);
+      all += v;
+      if (c < rank) before += v;
+    }
+  }
+  cluster.sync();  // no CTA leaves while another still reads its totals
+  int32_t scan = all;  // inclusive over the warp, then over the CTA
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int32_t v = __shfl_up_sync(0xffffffffu, scan, o);
+    if (lane >= o) scan += v;
+  }
+  if (lane == 31) wsum[warp] = scan;
+  __syncthreads();
+  int32_t ahead = 0, total = 0;
+  for (int w = 0; w < kSortWarps; ++w) {
+    if (w < warp) ahead += wsum[w];
+    total += wsum[w];
+  }
+  if (tid < E) {
+    const int32_t first = ahead + scan - all;
+    base[tid] = first + before;
+    if (rank == 0) offsets[tid] = first;
+  }
+  if (rank == 0 && tid == 0) offsets[E] = total;
+  __syncthreads();
+  const unsigned below = (1u << lane) - 1u;
+  for (int64_t i = w0; i < w1; i += 32) {
+    const int e = expert_of(ids, i + lane, w1, E);
+    const unsigned peers = __match_any_sync(0xffffffffu, e);
+    int32_t row = -1;
+    if (e < E) row = base[e] + mine[e] + __popc(peers & below);
+    __syncwarp();
+    if (e < E && lane == __ffs(peers) - 1) mine[e] += __popc(peers);
+    __syncwarp();
+    if (i + lane < w1) {
+      rows[i + lane] = row;
+      if (row >= 0) slots[row] = static_cast<int32_t>(i + lane);
+    }
+  }
+  for (int64_t r = total + static_cast<int64_t>(rank) * kSortThreads + tid; r < R; r += static_cast<int64_t>(C) * kSortThreads)
+    slots[r] = -1;
+}
+
+// kVec bf16 values as one access, widened to fp32.
+template <int kVec>
+struct Vec;
+template <>
+struct Vec<8> {
+  uint4 v;
+  __device__ __forceinline__ void load(const uint16_t* p) { v = *reinterpret_cast<const uint4*>(p); }
+  __device__ __forceinline__ void store(uint16_t* p) const { *reinterpret_cast<uint4*>(p) = v; }
+  __device__ __forceinline__ void get(float (&f)[8]) const {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      f[2 * i] = __uint_as_float(w[i] << 16);
+      f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    }
+  }
+  __device__ __forceinline__ void set(const float (&f)[8]) {
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      w[i] = f32_to_bf16_bits(f[2 * i]) | (static_cast<uint32_t>(f32_to_bf16_bits(f[2 * i + 1])) << 16);
+    v = make_uint4(w[0], w[1], w[2], w[3]);
+  }
+};
+template <>
+struct Vec<1> {
+  uint16_t v;
+  __device__ __forceinline__ void load(const uint16_t* p) { v = *p; }
+  __device__ __forceinline__ void store(uint16_t* p) const { *p = v; }
+  __device__ __forceinline__ void get(float (&f)[1]) const { f[0] = bf16_bits_to_f32(v); }
+  __device__ __forceinline__ void set(const float (&f)[1]) { v = f32_to_bf16_bits(f[0]); }
+};
+
+constexpr int kRowThreads = 256;
+
+struct RouteArgs {
+  const int32_t* rows;
+  const float* weights;  // null: all 1
+  int64_t R, N;
+  int32_t topk;
+};
+
+// The row of slot i, or -1 when it names none.
+__device__ __forceinline__ int64_t row_of(const RouteArgs& a, int64_t i) {
+  const int32_t r = __ldg(a.rows + i);
+  return r >= 0 && r < a.R ? r : -1;
+}
+
+template <int kVec, bool kWeighted>
+__global__ void __launch_bounds__(kRowThreads)
+    dispatch_kernel(const uint16_t* __restrict__ X, const RouteArgs a, uint16_t* __restrict__ out) {
+  const int64_t t = blockIdx.x;
+  for (int64_t n = static_cast<int64_t>(threadIdx.x) * kVec; n < a.N; n += kRowThreads * kVec) {
+    Vec<kVec> v;
+    v.load(X + t * a.N + n);
+    float f[kVec];
+    if (kWeighted) v.get(f);
+    for (int j = 0; j < a.topk; ++j) {
+      const int64_t r = row_of(a, t * a.topk + j);
+      if (r < 0) continue;
+      if (kWeighted) {
+        const float w = __ldg(a.weights + t * a.topk + j);
+        float p[kVec];
+#pragma unroll
+        for (int i = 0; i < kVec; ++i) p[i] = w * f[i];
+        Vec<kVec> o;
+        o.set(p);
+        o.store(out + r * a.N + n);
+      } else {
+        v.store(out + r * a.N + n);
+      }
+    }
+  }
+}
+
+template <int kVec, bool kWeighted>
+__global__ void __launch_bounds__(kRowThreads)
+    combine_kernel(const uint16_t* __restrict__ Y, const RouteArgs a, uint16_t* __restrict__ out) {
+  const int64_t t = blockIdx.x;
+  for (int64_t n = static_cast<int64_t>(threadIdx.x) * kVec; n < a.N; n += kRowThreads * kVec) {
+    float acc[kVec] = {};
+#pragma unroll 4
+    for (int j = 0; j < a.topk; ++j) {
+      const int64_t r = row_of(a, t * a.topk + j);
+      if (r < 0) continue;
+      const float w = kWeighted ? __ldg(a.weights + t * a.topk + j) : 1.0f;
+      Vec<kVec> v;
+      v.load(Y + r * a.N + n);
+      float f[kVec];
+      v.get(f);
+#pragma unroll
+      for (int i = 0; i < kVec; ++i) acc[i] += kWeighted ? w * f[i] : f[i];
+    }
+    Vec<kVec> o;
+    o.set(acc);
+    o.store(out + t * a.N + n);
+  }
+}
+
+// Slots of a token taken together in one walk over its columns.
+constexpr int kSlotsAtOnce = 8;
+
+template <int kVec>
+__global__ void __launch_bounds__(kRowThreads)
+    combine_grad_kernel(const uint16_t* __restrict__ dout, const uint16_t* __restrict__ Y,
+                        const RouteArgs a, uint16_t* __restrict__ dY, float* __restrict__ dweights) {
+  __shared__ float red[kRowThreads / 32][kSlotsAtOnce];
+  const int64_t t = blockIdx.x;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  for (int j0 = 0; j0 < a.topk; j0 += kSlotsAtOnce) {
+    int64_t r[kSlotsAtOnce];
+    float w[kSlotsAtOnce], dot[kSlotsAtOnce] = {};
+#pragma unroll
+    for (int j = 0; j < kSlotsAtOnce; ++j) {
+      r[j] = j0 + j < a.topk ? row_of(a, t * a.topk + j0 + j) : -1;
+      w[j] = r[j] >= 0 ? __ldg(a.weights + t * a.topk + j0 + j) : 0.0f;
+    }
+    for (int64_t n = static_cast<int64_t>(threadIdx.x) * kVec; n < a.N; n += kRowThreads * kVec) {
+      Vec<kVec> v;
+      v.load(dout + t * a.N + n);
+      float g[kVec];
+      v.get(g);
+#pragma unroll
+      for (int j = 0; j < kSlotsAtOnce; ++j) {
+        if (r[j] < 0) continue;
+        Vec<kVec> y, d;
+        y.load(Y + r[j] * a.N + n);
+        float f[kVec], p[kVec];
+        y.get(f);
+#pragma unroll
+        for (int i = 0; i < kVec; ++i) {
+          dot[j] += g[i] * f[i];
+          p[i] = w[j] * g[i];
+        }
+        d.set(p);
+        d.store(dY + r[j] * a.N + n);
+      }
+    }
+    // lanes by a fixed tree, then warps in order
+#pragma unroll
+    for (int j = 0; j < kSlotsAtOnce; ++j) {
+      const float s = warp_sum(dot[j]);
+      if (lane == 0) red[warp][j] = s;
+    }
+    __syncthreads();
+    if (threadIdx.x < kSlotsAtOnce && j0 + static_cast<int>(threadIdx.x) < a.topk) {
+      float s = 0.0f;
+      for (int q = 0; q < kRowThreads / 32; ++q) s += red[q][threadIdx.x];
+      dweights[t * a.topk + j0 + threadIdx.x] = s;
+    }
+    __syncthreads();
+  }
+}
+
+bool vec8(int64_t N, const void* a, const void* b, const void* c = nullptr, const void* d = nullptr) {
+  const uintptr_t u = reinterpret_cast<uintptr_t>(a) | reinterpret_cast<uintptr_t>(b) |
+                      reinterpret_cast<uintptr_t>(c) | reinterpret_cast<uintptr_t>(d);
+  return N % 8 == 0 && (u & 15) == 0;
+}
+
+template <typename Id>
+cudaError_t launch_sort(const Id* ids, int64_t R, int32_t E, int32_t* offsets, int32_t* rows,
+                        int32_t* slots, cudaStream_t s) {
+  static PerDevice<bool> configured;
+  bool done = false;
+  cudaError_t e = configured.get(
+      [](int, bool* v) {
+        *v = true;
+        return cudaFuncSetAttribute(expert_sort_kernel<Id>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                    (kSortWarps + 2) * LBQ_MAX_EXPERTS * 4);
+      },
+      &done);
+  if (e != cudaSuccess) return e;
+  const int C = R <= 4 * kSortThreads ? 1 : kSortCluster;
+  const int64_t warps = static_cast<int64_t>(C) * kSortWarps;
+  const int64_t per_warp = ((R + warps - 1) / warps + 31) / 32 * 32;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(C));
+  cfg.blockDim = dim3(kSortThreads);
+  cfg.dynamicSmemBytes = static_cast<size_t>(kSortWarps + 2) * E * 4;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = static_cast<unsigned>(C);
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, expert_sort_kernel<Id>, ids, R, static_cast<int>(E), per_warp, offsets, rows, slots);
+}
+
+}  // namespace
+
+cudaError_t lbq_launch_expert_sort(const void* ids, int id_bytes, int64_t R, int32_t E,
+                                   int32_t* offsets, int32_t* rows, int32_t* slots, cudaStream_t s) {
+  return id_bytes == 8 ? launch_sort(static_cast<const long long*>(ids), R, E, offsets, rows, slots, s)
+                       : launch_sort(static_cast<const int*>(ids), R, E, offsets, rows, slots, s);
+}
+
+cudaError_t lbq_launch_expert_dispatch(const uint16_t* X, const int32_t* rows, const float* weights,
+                                       int64_t T, int32_t topk, int64_t K, int64_t R, uint16_t* out,
+                                       cudaStream_t s) {
+  const RouteArgs a = {rows, weights, R, K, topk};
+  const unsigned grid = static_cast<unsigned>(T);
+  if (vec8(K, X, out)) {
+    if (weights) dispatch_kernel<8, true><<<grid, kRowThreads, 0, s>>>(X, a, out);
+    else dispatch_kernel<8, false><<<grid, kRowThreads, 0, s>>>(X, a, out);
+  } else {
+    if (weights) dispatch_kernel<1, true><<<grid, kRowThreads, 0, s>>>(X, a, out);
+    else dispatch_kernel<1, false><<<grid, kRowThreads, 0, s>>>(X, a, out);
+  }
+  return cudaGetLastError();
+}
+
+cudaError_t lbq_launch_expert_combine(const uint16_t* Y, const int32_t* rows, const float* weights,
+                                      int64_t T, int32_t topk, int64_t N, int64_t R, uint16_t* out,
+                                      cudaStream_t s) {
+  const RouteArgs a = {rows, weights, R, N, topk};
+  const unsigned grid = static_cast<unsigned>(T);
+  if (vec8(N, Y, out)) {
+    if (weights) combine_kernel<8, true><<<grid, kRowThreads, 0, s>>>(Y, a, out);
+    else combine_kernel<8, false><<<grid, kRowThreads, 0, s>>>(Y, a, out);
+  } else {
+    if (weights) combine_kernel<1, true><<<grid, kRowThreads, 0, s>>>(Y, a, out);
+    else combine_kernel<1, false><<<grid, kRowThreads, 0, s>>>(Y, a, out);
+  }
+  return cudaGetLastError();
+}
+
+cudaError_t lbq_launch_expert_combine_grad(const uint16_t* dout, const uint16_t* Y,
+                                           const int32_t* rows, const float* weights, int64_t T,
+                                           int32_t topk, int64_t N, int64_t R, uint16_t* dY,
+                                           float* dweights, cudaStream_t s) {
+  const RouteArgs a = {rows, weights, R, N, topk};
+  const unsigned grid = static_cast<unsigned>(T);
+  if (vec8(N, dout, Y, dY))
+    combine_grad_kernel<8><<<grid, kRowThreads, 0, s>>>(dout, Y, a, dY, dweights);
+  else
+    combine_grad_kernel<1><<<grid, kRowThreads, 0, s>>>(dout, Y, a, dY, dweights);
+  return cudaGetLastError();
+}

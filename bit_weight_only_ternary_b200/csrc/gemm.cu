@@ -97,6 +97,7 @@ __global__ void __launch_bounds__(256) gemm_rowwarp(const uint8_t* __restrict__ 
 
 size_t lbq_gemm_workspace(const lbq_weights* w, int64_t M) {
   if (w->fmt == LBQ_TERN5) return lbq_gemm_tc_workspace(w, M);
+  if (is_q4(w->fmt)) return 0;
   return w->fmt == LBQ_Q2RHT
              ? kWsCounterBytes + static_cast<size_t>(w->K) * static_cast<size_t>(M) * sizeof(float)
              : 0;
@@ -110,6 +111,9 @@ cudaError_t lbq_launch_gemm(const lbq_weights* w, const uint16_t* X, int64_t M, 
   const uint8_t* codes = static_cast<const uint8_t*>(w->codes);
   const uint16_t* scales = static_cast<const uint16_t*>(w->scales);
   switch (w->fmt) {
+    case LBQ_Q4G32:
+    case LBQ_Q4G128:  // q4_gemv.cu
+      return lbq_launch_q4_few(w, X, M, Y, s);
     case LBQ_TERN5:  // tensor-core path (gemm_tc.cu)
       return lbq_launch_gemm_tc(w, X, M, Y, ws, s);
     case LBQ_SIGN1:

@@ -19,6 +19,7 @@ constexpr int kTernBlockBytes = 28;   // 26 code bytes + fp16 scale
 constexpr int kTernCodeBytes = 26;
 constexpr int kSignBlock = 128;       // weights per sign scale
 constexpr int kQ2Block = 32;          // weights per 2-bit scale
+constexpr int kQ4Chunk = 128;         // 4-bit formats: K comes in multiples of this
 constexpr int kRhtBlock = 512;        // Hadamard block size
 // Workspace layout shared by every product: [0, kWsCounterBytes) holds arrival
 // counters that must be zero when a call starts and are zero again when it ends;
@@ -47,6 +48,10 @@ struct Layout {
   int64_t block;         // weights per scale
 };
 
+// The 4-bit formats: 32 or 128 weights per fp16 scale.
+__host__ __device__ inline bool is_q4(int32_t fmt) { return fmt == LBQ_Q4G32 || fmt == LBQ_Q4G128; }
+__host__ __device__ inline int q4_group(int32_t fmt) { return fmt == LBQ_Q4G32 ? 32 : 128; }
+
 // Returns false on an unknown format or a K that violates the shape rules.
 inline bool layout_of(int32_t fmt, int64_t K, Layout* L) {
   if (K < 128 || K % 128) return false;
@@ -66,6 +71,12 @@ inline bool layout_of(int32_t fmt, int64_t K, Layout* L) {
       L->code_stride = K / 4;
       L->scale_stride = K / kQ2Block;
       L->block = kQ2Block;
+      return true;
+    case LBQ_Q4G32:
+    case LBQ_Q4G128:
+      L->code_stride = K / 2;
+      L->scale_stride = (K / q4_group(fmt) + 7) / 8 * 8;  // 16-byte rows of scales
+      L->block = q4_group(fmt);
       return true;
     default:
       return false;
@@ -178,3 +189,32 @@ cudaError_t lbq_launch_gemm_tc(const lbq_weights* w, const uint16_t* X, int64_t 
                                void* ws, cudaStream_t s);
 cudaError_t lbq_launch_gemm(const lbq_weights* w, const uint16_t* X, int64_t M, const int8_t* D,
                             uint16_t* Y, void* ws, cudaStream_t s);
+// The 4-bit products (q4_gemv.cu): a list of batch-1 products (y32: fp32 outputs, only
+// for a list of one), and one matrix times a few tokens.
+cudaError_t lbq_launch_q4_list(const lbq_product* ps, int32_t n, float* y32, cudaStream_t s);
+cudaError_t lbq_launch_q4_few(const lbq_weights* w, const uint16_t* X, int64_t M, uint16_t* Y,
+                              cudaStream_t s);
+// Rows of sorted order by their experts' matrices: row r in [offsets[e], offsets[e + 1])
+// reads X row slots[r] / topk (r itself when slots is null).
+struct lbq_expert_rows {
+  const uint16_t* X;
+  const int32_t* offsets;
+  const int32_t* slots;
+  uint16_t* Y;
+  int64_t T, R;
+  int32_t topk, E;
+};
+cudaError_t lbq_launch_q4_expert_few(const lbq_weights* w, const lbq_expert_rows& r, cudaStream_t s);
+// Slots sorted by expert and the rows' way there and back (expert.cu).
+cudaError_t lbq_launch_expert_sort(const void* ids, int id_bytes, int64_t R, int32_t E,
+                                   int32_t* offsets, int32_t* rows, int32_t* slots, cudaStream_t s);
+cudaError_t lbq_launch_expert_dispatch(const uint16_t* X, const int32_t* rows, const float* weights,
+                                       int64_t T, int32_t topk, int64_t K, int64_t R, uint16_t* out,
+                                       cudaStream_t s);
+cudaError_t lbq_launch_expert_combine(const uint16_t* Y, const int32_t* rows, const float* weights,
+                                      int64_t T, int32_t topk, int64_t N, int64_t R, uint16_t* out,
+                                      cudaStream_t s);
+cudaError_t lbq_launch_expert_combine_grad(const uint16_t* dout, const uint16_t* Y,
+                                           const int32_t* rows, const float* weights, int64_t T,
+                                           int32_t topk, int64_t N, int64_t R, uint16_t* dY,
+                                           float* dweights, cudaStream_t s);

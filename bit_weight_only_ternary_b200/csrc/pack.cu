@@ -151,6 +151,41 @@ __global__ void pack_q2_kernel(const float* __restrict__ W, int64_t K, int64_t N
       *reinterpret_cast<uint32_t*>(codes + g4_word_byte(n, q, cstride)) = 0u;
 }
 
+// 4-bit: s16 = fp16(max|w| / 7) per group of kG weights, q = nearest integer of w / s16
+// plus 8 (ties to even; the fp64 quotient of an fp32 by an fp16 value is a tie only when
+// the exact one is). One thread per (row, group).
+template <int kG>
+__global__ void pack_q4_kernel(const float* __restrict__ W, int64_t K, int64_t N,
+                               uint8_t* __restrict__ codes, int64_t cstride,
+                               uint16_t* __restrict__ scales, int64_t sstride) {
+  const int64_t nb = K / kG;
+  const int64_t gid = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x;
+  if (gid >= g4_rows(N) * nb) return;
+  const int64_t n = gid / nb, b = gid % nb;
+  const bool real = n < N;
+  const float* w = W + (real ? n : 0) * K + b * kG;
+  float mx = 0.0f;
+  if (real)
+    for (int i = 0; i < kG; ++i) mx = fmaxf(mx, fabsf(w[i]));
+  const uint16_t h = real ? scale_to_f16_bits(static_cast<double>(mx) / 7.0) : 0;
+  scales[g4_scale_elem(n, b, sstride)] = h;
+  if (b == nb - 1)  // zero the scale-row padding
+    for (int64_t p = nb; p < sstride; ++p) scales[g4_scale_elem(n, p, sstride)] = 0;
+  const double s = static_cast<double>(f16_bits_to_f32(h));
+  for (int q = 0; q < kG / 8; ++q) {
+    uint32_t word = 0;
+    if (real) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        double t = h ? rint(static_cast<double>(w[8 * q + i]) / s) : 0.0;
+        t = t < -8.0 ? -8.0 : (t > 7.0 ? 7.0 : t);
+        word |= static_cast<uint32_t>(static_cast<int>(t) + 8) << (4 * ((i >> 1) + 4 * (i & 1)));
+      }
+    }
+    *reinterpret_cast<uint32_t*>(codes + g4_word_byte(n, b * (kG / 8) + q, cstride)) = word;
+  }
+}
+
 __global__ void unpack_kernel(int32_t fmt, const uint8_t* __restrict__ codes, int64_t cstride,
                               const uint16_t* __restrict__ scales, int64_t sstride, int64_t K,
                               int64_t N, int64_t blk, int8_t* __restrict__ out,
@@ -181,11 +216,18 @@ __global__ void unpack_kernel(int32_t fmt, const uint8_t* __restrict__ codes, in
       const int64_t k = b * kSignBlock + i;
       o[i] = ((byte_at(k >> 3) >> (k & 7)) & 1) ? 1 : -1;
     }
-  } else {
+  } else if (fmt == LBQ_Q2RHT) {
     s = f16_bits_to_f32(scales[g4_scale_elem(n, b, sstride)]);
     for (int i = 0; i < kQ2Block; ++i) {
       const int64_t k = b * kQ2Block + i;
       o[i] = static_cast<int8_t>((byte_at(k >> 2) >> (2 * (k & 3))) & 3);
+    }
+  } else {  // 4-bit: q - 8
+    s = f16_bits_to_f32(scales[g4_scale_elem(n, b, sstride)]);
+    for (int i = 0; i < static_cast<int>(blk); ++i) {
+      const int64_t k = b * blk + i;
+      const int nib = static_cast<int>((k & 7) >> 1) + 4 * static_cast<int>(k & 1);
+      o[i] = static_cast<int8_t>(static_cast<int>((byte_at((k >> 3) * 4 + (nib >> 1)) >> (4 * (nib & 1))) & 15) - 8);
     }
   }
   if (sout) sout[n * nb + b] = s;
@@ -220,6 +262,14 @@ cudaError_t lbq_launch_pack(int32_t fmt, const float* W, int64_t K, int64_t N, u
     case LBQ_SIGN1:
       pack_sign_kernel<<<grid_for(units, T), T, 0, s>>>(W, K, N, codes, L.code_stride, scales,
                                                          L.scale_stride);
+      break;
+    case LBQ_Q4G32:
+      pack_q4_kernel<32><<<grid_for(units, T), T, 0, s>>>(W, K, N, codes, L.code_stride, scales,
+                                                           L.scale_stride);
+      break;
+    case LBQ_Q4G128:
+      pack_q4_kernel<128><<<grid_for(units, T), T, 0, s>>>(W, K, N, codes, L.code_stride, scales,
+                                                            L.scale_stride);
       break;
     default:
       pack_q2_kernel<<<grid_for(units, T), T, 0, s>>>(W, K, N, codes, L.code_stride, scales,

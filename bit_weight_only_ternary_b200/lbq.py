@@ -13,8 +13,9 @@ from dataclasses import dataclass
 
 import torch
 
-LBQ_TERN5, LBQ_SIGN1, LBQ_Q2RHT = 1, 2, 3
-FORMATS = {"tern": LBQ_TERN5, "sign": LBQ_SIGN1, "q2": LBQ_Q2RHT}
+LBQ_TERN5, LBQ_SIGN1, LBQ_Q2RHT, LBQ_Q4G32, LBQ_Q4G128 = 1, 2, 3, 5, 6
+FORMATS = {"tern": LBQ_TERN5, "sign": LBQ_SIGN1, "q2": LBQ_Q2RHT, "q4g32": LBQ_Q4G32,
+           "q4g128": LBQ_Q4G128}
 
 LBQ_OK, LBQ_ERR_ARG, LBQ_ERR_SHAPE, LBQ_ERR_ALIGN, LBQ_ERR_FORMAT, LBQ_ERR_CUDA, \
     LBQ_ERR_WORKSPACE, LBQ_ERR_DEVICE_WAIT = range(8)
@@ -23,7 +24,10 @@ LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "liblbq.so")
 EXPORTS = ("lbq_status_string", "lbq_packed_layout", "lbq_pack", "lbq_unpack", "lbq_rht_signs",
            "lbq_hadamard", "lbq_workspace_bytes", "lbq_gemv", "lbq_gemm", "lbq_gemv_noalloc", "lbq_device_fault",
            "lbq_selftest_wait", "lbq_read_probe", "lbq_gemv_batch_workspace_bytes", "lbq_gemv_batch",
-           "lbq_last_cuda_error", "lbq_last_cuda_error_string", "lbq_gemv_f32", "lbq_gemv_batch_plan")
+           "lbq_last_cuda_error", "lbq_last_cuda_error_string", "lbq_gemv_f32", "lbq_gemv_batch_plan",
+           "lbq_expert_sort", "lbq_expert_dispatch", "lbq_expert_combine", "lbq_expert_combine_grad",
+           "lbq_expert_workspace_bytes", "lbq_expert_gemm")
+LBQ_MAX_EXPERTS = 1024
 LBQ_BATCH_MAX = 256
 LBQ_BATCH_MAX_CTAS = 192
 LBQ_NOALLOC_SCRATCH_BYTES = 4 << 20
@@ -74,6 +78,12 @@ def _load():
         "lbq_gemv_batch_workspace_bytes": (sz, [ctypes.POINTER(lbq_product), i32]),
         "lbq_gemv_batch": (ctypes.c_int, [ctypes.POINTER(lbq_product), i32, p, sz, p]),
         "lbq_gemv_batch_plan": (ctypes.c_int, [ctypes.POINTER(lbq_product), i32, i32, p, p, p]),
+        "lbq_expert_sort": (ctypes.c_int, [p, i32, i64, i32, i32, p, p, p, p]),
+        "lbq_expert_dispatch": (ctypes.c_int, [p, i64, i64, p, i32, p, i64, p, p]),
+        "lbq_expert_combine": (ctypes.c_int, [p, i64, i64, p, i64, i32, p, p, p]),
+        "lbq_expert_combine_grad": (ctypes.c_int, [p, p, i64, i64, p, i64, i32, p, p, p, p]),
+        "lbq_expert_workspace_bytes": (sz, [W, i32, i64]),
+        "lbq_expert_gemm": (ctypes.c_int, [W, i32, p, i64, p, p, i32, i64, p, p, sz, p]),
         "lbq_last_cuda_error": (i32, []),
         "lbq_last_cuda_error_string": (ctypes.c_char_p, []),
     }
@@ -155,7 +165,7 @@ def lbq_pack(fmt: int, W: torch.Tensor, stream=None) -> PackedWeights:
 
 def lbq_unpack(pw: PackedWeights, stream=None):
     """-> (int8 codes [N][K], fp32 block scales [N][K/blk]) on the device."""
-    blk = 32 if pw.fmt == LBQ_Q2RHT else 128
+    blk = 32 if pw.fmt in (LBQ_Q2RHT, LBQ_Q4G32) else 128
     out = torch.empty((pw.N, pw.K), dtype=torch.int8, device=pw.codes.device)
     sc = torch.empty((pw.N, pw.K // blk), dtype=torch.float32, device=pw.codes.device)
     d = pw.desc()
@@ -321,3 +331,162 @@ def workspace_for_batch(plist: ProductList, device=None) -> torch.Tensor:
         _check(LBQ_ERR_ARG, "lbq_gemv_batch_workspace_bytes")
     dev = device or plist.items[0][1].device
     return torch.zeros(((n + 15) // 16) * 16, dtype=torch.uint8, device=dev)
+
+
+def _arg(where: str, t, dtype, shape=None):
+    """The expert calls take dense tensors of one type on the current device: anything
+    else is refused here (the C call sees pointers only)."""
+    if t is None:
+        return
+    dtypes = dtype if isinstance(dtype, tuple) else (dtype,)
+    if t.dtype not in dtypes or not t.is_contiguous() or not t.is_cuda \
+            or t.device.index != torch.cuda.current_device():
+        _check(LBQ_ERR_ARG, where)
+    if shape is not None and tuple(t.shape) != tuple(shape):
+        _check(LBQ_ERR_SHAPE, where)
+
+
+@dataclass
+class ExpertWeights:
+    """E packed K x N matrices of one 4-bit format: codes uint8 [E][ceil(N/4)][4 *
+    code_stride], scales fp16 (as int16) [E][ceil(N/4)][4 * scale_stride]."""
+    fmt: int
+    K: int
+    N: int
+    E: int
+    codes: torch.Tensor
+    scales: torch.Tensor
+
+    def desc(self) -> lbq_weights:
+        return lbq_weights(self.fmt, 0, self.K, self.N, self.codes.data_ptr(),
+                           self.scales.data_ptr(), self.codes.stride(1) // 4,
+                           self.scales.stride(1) // 4)
+
+
+def pack_experts(fmt: int, W: torch.Tensor, stream=None) -> ExpertWeights:
+    """lbq_pack of every expert's fp32 matrix, W [E][N][K] (device), behind one another."""
+    assert W.is_cuda and W.dtype == torch.float32 and W.is_contiguous() and W.dim() == 3
+    E, N, K = W.shape
+    cs, ss, _, _ = lbq_packed_layout(fmt, K, N)
+    if ss == 0:
+        _check(LBQ_ERR_FORMAT, "pack_experts")
+    G = (N + 3) // 4
+    codes = torch.empty((E, G, 4 * cs), dtype=torch.uint8, device=W.device)
+    scales = torch.empty((E, G, 4 * ss), dtype=torch.int16, device=W.device)
+    for e in range(E):
+        _check(_lib.lbq_pack(fmt, _ptr(W[e]), K, N, _ptr(codes[e]), _ptr(scales[e]),
+                             _stream(stream)), "lbq_pack")
+    return ExpertWeights(fmt, K, N, E, codes, scales)
+
+
+def lbq_expert_sort(expert: torch.Tensor, E: int, offsets=None, rows=None, slots=None, stream=None):
+    """expert int32 or int64 [T][topk] -> (offsets int32 [E+1], rows int32 [T][topk], slots
+    int32 [T*topk]): a stable sort of the slots by expert (ids outside 0..E-1 left out)."""
+    T, topk = expert.shape
+    w = "lbq_expert_sort"
+    _arg(w, expert, (torch.int32, torch.int64))
+    _arg(w, offsets, torch.int32, (E + 1,))
+    _arg(w, rows, torch.int32, (T, topk))
+    _arg(w, slots, torch.int32, (T * topk,))
+    new = lambda *shape: torch.empty(shape, dtype=torch.int32, device=expert.device)  # noqa: E731
+    offsets = new(E + 1) if offsets is None else offsets
+    rows = new(T, topk) if rows is None else rows
+    slots = new(T * topk) if slots is None else slots
+    _check(_lib.lbq_expert_sort(_ptr(expert), expert.element_size(), T, topk, E, _ptr(offsets),
+                                _ptr(rows), _ptr(slots), _stream(stream)), "lbq_expert_sort")
+    return offsets, rows, slots
+
+
+def lbq_expert_dispatch(X: torch.Tensor, rows: torch.Tensor, weights=None, out=None,
+                        stream=None) -> torch.Tensor:
+    """out[rows[t][j]] = (weights[t][j] *) X[t] for bf16 X [T][K]; out [R][K], by default
+    R = T * topk (rows behind the last sorted one are then uninitialised)."""
+    T, K = X.shape
+    topk = rows.shape[1]
+    w = "lbq_expert_dispatch"
+    _arg(w, X, torch.bfloat16)
+    _arg(w, rows, torch.int32, (T, topk))
+    _arg(w, weights, torch.float32, (T, topk))
+    if out is not None:
+        _arg(w, out, torch.bfloat16, (out.shape[0], K))
+    else:
+        out = torch.empty((T * topk, K), dtype=torch.bfloat16, device=X.device)
+    _check(_lib.lbq_expert_dispatch(_ptr(X), T, K, _ptr(rows), topk, _ptr(weights), out.shape[0],
+                                    _ptr(out), _stream(stream)), "lbq_expert_dispatch")
+    return out
+
+
+def lbq_expert_combine(Y: torch.Tensor, rows: torch.Tensor, weights=None, out=None,
+                       stream=None) -> torch.Tensor:
+    """bf16 out [T][N]: out[t] = sum_j (weights[t][j] *) Y[rows[t][j]] for bf16 Y [R][N]."""
+    R, N = Y.shape
+    T, topk = rows.shape
+    w = "lbq_expert_combine"
+    _arg(w, Y, torch.bfloat16)
+    _arg(w, rows, torch.int32)
+    _arg(w, weights, torch.float32, (T, topk))
+    _arg(w, out, torch.bfloat16, (T, N))
+    if out is None:
+        out = torch.empty((T, N), dtype=torch.bfloat16, device=Y.device)
+    _check(_lib.lbq_expert_combine(_ptr(Y), R, N, _ptr(rows), T, topk, _ptr(weights), _ptr(out),
+                                   _stream(stream)), "lbq_expert_combine")
+    return out
+
+
+def lbq_expert_combine_grad(dout: torch.Tensor, Y: torch.Tensor, rows: torch.Tensor,
+                            weights: torch.Tensor, dY=None, dweights=None, stream=None):
+    """The gradients of lbq_expert_combine: (dY bf16 [R][N], dweights fp32 [T][topk]). Rows
+    of dY that no slot names are left as they were (uninitialised in a new dY)."""
+    R, N = Y.shape
+    T, topk = rows.shape
+    w = "lbq_expert_combine_grad"
+    _arg(w, Y, torch.bfloat16)
+    _arg(w, dout, torch.bfloat16, (T, N))
+    _arg(w, rows, torch.int32)
+    _arg(w, weights, torch.float32, (T, topk))
+    _arg(w, dY, torch.bfloat16, (R, N))
+    _arg(w, dweights, torch.float32, (T, topk))
+    if dY is None:
+        dY = torch.empty((R, N), dtype=torch.bfloat16, device=Y.device)
+    if dweights is None:
+        dweights = torch.empty((T, topk), dtype=torch.float32, device=Y.device)
+    _check(_lib.lbq_expert_combine_grad(_ptr(dout), _ptr(Y), R, N, _ptr(rows), T, topk,
+                                        _ptr(weights), _ptr(dY), _ptr(dweights), _stream(stream)),
+           "lbq_expert_combine_grad")
+    return dY, dweights
+
+
+def lbq_expert_workspace_bytes(ew: ExpertWeights, R: int) -> int:
+    d = ew.desc()
+    return int(_lib.lbq_expert_workspace_bytes(ctypes.byref(d), ew.E, R))
+
+
+def workspace_for_experts(ew: ExpertWeights, R: int, device=None) -> torch.Tensor | None:
+    """A workspace of lbq_expert_workspace_bytes(ew, R) bytes (None if 0)."""
+    n = lbq_expert_workspace_bytes(ew, R)
+    if n == 0:
+        return None
+    return torch.empty(((n + 15) // 16) * 16, dtype=torch.uint8, device=device or ew.codes.device)
+
+
+def lbq_expert_gemm(ew: ExpertWeights, X: torch.Tensor, offsets: torch.Tensor, slots=None,
+                    topk: int = 1, Y=None, workspace=None, stream=None) -> torch.Tensor:
+    """bf16 Y [R][N]: row r of expert e is W_hat_e X[slots[r] // topk] (X[r] with slots None)
+    for offsets[e] <= r < offsets[e+1]; other rows are left as they were."""
+    T = X.shape[0]
+    w = "lbq_expert_gemm"
+    R = Y.shape[0] if Y is not None else (T if slots is None else slots.shape[0])
+    _arg(w, X, torch.bfloat16, (T, ew.K))
+    _arg(w, offsets, torch.int32, (ew.E + 1,))
+    _arg(w, slots, torch.int32, (R,))
+    _arg(w, Y, torch.bfloat16, (R, ew.N))
+    if Y is None:
+        Y = torch.empty((R, ew.N), dtype=torch.bfloat16, device=X.device)
+    if workspace is None:
+        workspace = workspace_for_experts(ew, R, X.device)
+    wsb = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    d = ew.desc()
+    _check(_lib.lbq_expert_gemm(ctypes.byref(d), ew.E, _ptr(X), T, _ptr(offsets), _ptr(slots), topk,
+                                R, _ptr(Y), _ptr(workspace), wsb, _stream(stream)),
+           "lbq_expert_gemm")
+    return Y

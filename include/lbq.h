@@ -2,7 +2,7 @@
  * lbq.h -- C ABI of the low-bit weight-only GEMV/GEMM library for B200 (sm_100a).
  *
  * The library computes y = s * T(W)^T * (H x): bf16 activations times LLM weights
- * stored in one of three packed low-bit formats, dequantized on the fly inside
+ * stored in a packed low-bit format, dequantized on the fly inside
  * the kernels, accumulated in fp32 and written as bf16.
  *
  * Sources (web pages on extreme low-bit 27B inference):
@@ -65,6 +65,17 @@
  *     The weights are expressed in the rotated basis, so the product uses
  *     x' = H_512 D x / sqrt(512) (see lbq_hadamard) in place of x. K % 512 == 0.
  *
+ *   LBQ_Q4G32, LBQ_Q4G128 (4-bit, one scale per group of 32 or 128 weights): codes
+ *     [N][K/2] bytes; the eight weights 8w .. 8w+7 of a row share its 32-bit word w,
+ *     weight 8w+i in bits 4p..4p+3 with p = (i >> 1) + 4 (i & 1), so that shifting the
+ *     word by 0, 4, 8 or 12 bits brings a pair of neighbours to bits 0 and 16. Code q
+ *     in 0..15 means q - 8. scales [N][scale_stride] fp16 with scale_stride =
+ *     round_up(K/g, 8), padded with zeros (g = 32 or 128); any fp16 value is a scale
+ *     (codes and scales of another quantiser can be laid out like this and used).
+ *     lbq_pack: s16 = fp16_rne(min(max|w| / 7, 65504)) per group (quotient in fp64),
+ *     q = clip(round_half_even(w/s16), -8, 7) + 8, q = 8 everywhere when s16 == 0.
+ *     Dequantised weight = s16 * (q - 8).
+ *
  * Storage order (all formats). The per-row byte strings above are stored with rows
  *   interleaved in groups of four, so that one 16-byte load brings the same 32-bit
  *   word of four rows. N is padded to a multiple of four with zero rows. In group g
@@ -74,7 +85,8 @@
  *   start at element g * 4 * scale_stride, and scale e of row 4g+q is element 4 e + q
  *   of the group. Padding rows and padding words are zero bytes.
  *
- * Shape rules: K % 128 == 0 (LBQ_Q2RHT: K % 512 == 0), K >= 128, N >= 1, M >= 1;
+ * Shape rules: K % 128 == 0 (LBQ_Q2RHT: K % 512 == 0), K >= 128, N >= 1, M >= 1
+ * (4-bit formats: K and N at most 2^28);
  * a batch-1 product split over K (K > 512, or > 1024 for LBQ_SIGN1) has N <= 524288.
  * Alignment rules: codes, scales, x/X, W, D, out and workspace 16-byte aligned;
  * y/Y 2-byte aligned. Strides must be at least the packed row size; code strides a
@@ -105,7 +117,10 @@ typedef enum lbq_status {
 typedef enum lbq_format {
   LBQ_TERN5 = 1, /* ternary, 5 trits per byte, fp16 scale per 128, in-block     */
   LBQ_SIGN1 = 2, /* 1-bit sign, fp16 scale per 128, separate scale array       */
-  LBQ_Q2RHT = 3  /* 2-bit 4-level, fp16 scale per 32, input rotated by RHT-512  */
+  LBQ_Q2RHT = 3, /* 2-bit 4-level, fp16 scale per 32, input rotated by RHT-512  */
+  /* 4 names no format */
+  LBQ_Q4G32 = 5, /* 4-bit, levels -8..7, fp16 scale per 32, separate scale array */
+  LBQ_Q4G128 = 6 /* 4-bit, levels -8..7, fp16 scale per 128                     */
 } lbq_format;
 
 /* A packed weight matrix (descriptor only; the buffers belong to the caller). */
@@ -149,8 +164,9 @@ lbq_status lbq_pack(int32_t fmt, const float* W, int64_t K, int64_t N, void* cod
                     void* scales, void* stream);
 
 /* Unpack codes to int8 values (t in {-1,0,1} for TERN5, 2b-1 in {-1,1} for SIGN1,
- * q in {0,1,2,3} for Q2RHT) into out [N][K] (device), and the block scales as fp32
- * into scales_out [N][K/blk] (device; blk = 128, or 32 for Q2RHT) when non-NULL.
+ * q in {0,1,2,3} for Q2RHT, q - 8 in -8..7 for the 4-bit formats) into out [N][K] (device), and the block scales as fp32
+ * into scales_out [N][K/blk] (device; blk = 128, or 32 for Q2RHT and Q4G32) when
+ * non-NULL.
  * A test hook for the bit-exact code check. */
 lbq_status lbq_unpack(const lbq_weights* w, int8_t* out, float* scales_out, void* stream);
 
@@ -274,9 +290,77 @@ lbq_status lbq_gemv_batch(const lbq_product* ps, int32_t n, void* workspace,
  * whose first unit-slice lies in [bound[c], bound[c + 1]) (unit u of piece s of product
  * i starts at c0_i + NU_i * j0 + u * (j1 - j0)), and *total, the list's unit-slices.
  * Errors: LBQ_ERR_ARG (NULL outputs, ctas < 1 or > LBQ_BATCH_MAX_CTAS, n > LBQ_BATCH_MAX,
- * mixed formats), and those of lbq_gemv_batch's checks. */
+ * mixed formats), LBQ_ERR_FORMAT (a 4-bit list: its launch cuts products into 32-row
+ * tiles of full K, one CTA each, and has no such schedule), and those of
+ * lbq_gemv_batch's checks. */
 lbq_status lbq_gemv_batch_plan(const lbq_product* ps, int32_t n, int32_t ctas, int32_t* pieces,
                                int64_t* bound, int64_t* total);
+
+/* Mixture-of-experts layers. Token t of T is sent to topk experts; slot t * topk + j
+ * is its j-th choice. lbq_expert_sort gives every slot a row so that each expert's rows
+ * lie together; lbq_expert_gemm multiplies each row by its expert's weights;
+ * lbq_expert_combine adds a token's rows up again. The layer
+ *   out[t] = sum_j weights[t][j] * f_e(x[t]),  e = expert[t][j]
+ * is sort, then products and activations on rows, then combine. `rows` (slot -> row)
+ * and `slots` (row -> slot) come from lbq_expert_sort; entries outside their range are
+ * left out, never followed. */
+#define LBQ_MAX_EXPERTS 1024
+
+/* Stable counting sort of the T * topk slots by expert: expert [T][topk] (device, ids of
+ * id_bytes = 4 or 8 bytes), ids outside 0 .. E-1 mark slots that are left out (experts
+ * that another device holds, padding). offsets [E+1]: expert e has rows offsets[e] ..
+ * offsets[e+1] - 1, in slot order; rows [T][topk]: each slot's row, -1 when left out;
+ * slots [T * topk]: each row's slot, -1 behind the last row (offsets[E]). One launch.
+ * T * topk <= 2^30, topk <= 1024, E <= LBQ_MAX_EXPERTS.
+ * Errors: LBQ_ERR_ARG, LBQ_ERR_SHAPE, LBQ_ERR_ALIGN (natural alignment), LBQ_ERR_CUDA. */
+lbq_status lbq_expert_sort(const void* expert, int32_t id_bytes, int64_t T, int32_t topk, int32_t E,
+                           int32_t* offsets, int32_t* rows, int32_t* slots, void* stream);
+
+/* out[rows[t][j]] = X[t] (bf16 rows of K values, any K up to 2^24), times weights[t][j]
+ * (fp32 [T][topk]; one rounding) unless weights is NULL. out has R rows; slots whose row
+ * is outside 0 .. R-1 are left out, rows no slot names are left as they were, and rows
+ * must be distinct. With weights NULL its gradient with respect to X is
+ * lbq_expert_combine(dout, R, K, rows, T, topk, NULL, dX).
+ * Errors: LBQ_ERR_ARG (nulls, X and out overlap), LBQ_ERR_SHAPE, LBQ_ERR_ALIGN (bf16 on
+ * 2 bytes, the rest on 4; 16-byte aligned X and out with K % 8 == 0 are faster),
+ * LBQ_ERR_CUDA. */
+lbq_status lbq_expert_dispatch(const uint16_t* X, int64_t T, int64_t K, const int32_t* rows, int32_t topk,
+                               const float* weights, int64_t R, uint16_t* out, void* stream);
+
+/* out[t] = sum_j weights[t][j] * Y[rows[t][j]] over Y's R rows of N bf16 values: fp32
+ * sums in the order of j, one rounding. weights NULL: all 1. Slots whose row is outside
+ * 0 .. R-1 add nothing (a token without any gives zeros). Limits and errors as
+ * lbq_expert_dispatch. */
+lbq_status lbq_expert_combine(const uint16_t* Y, int64_t R, int64_t N, const int32_t* rows, int64_t T,
+                              int32_t topk, const float* weights, uint16_t* out, void* stream);
+
+/* Both gradients of lbq_expert_combine in one pass: dY[rows[t][j]] = weights[t][j] *
+ * dout[t] (rows no slot names are left as they were; rows must be distinct) and
+ * dweights[t][j] = sum_n dout[t][n] Y[rows[t][j]][n] (fp32, a fixed order of sums; 0 for
+ * slots left out). Limits and errors as lbq_expert_dispatch; dY may overlap neither Y
+ * nor dout, dweights not weights. */
+lbq_status lbq_expert_combine_grad(const uint16_t* dout, const uint16_t* Y, int64_t R, int64_t N,
+                                   const int32_t* rows, int64_t T, int32_t topk, const float* weights,
+                                   uint16_t* dY, float* dweights, void* stream);
+
+/* Bytes of workspace lbq_expert_gemm needs for R rows (0: none, or bad arguments). The
+ * counter rule of lbq_workspace_bytes does not apply: it is scratch only. */
+size_t lbq_expert_workspace_bytes(const lbq_weights* w, int32_t E, int64_t R);
+
+/* Y[r] = W_hat_e x_r for every row r in [offsets[e], offsets[e+1]), x_r = X[slots[r] /
+ * topk] (X [T][K] bf16: the gather by token is part of the product) or, with slots NULL,
+ * x_r = X[r] (T >= R). Y is [R][N] bf16; rows behind offsets[E] are left as they were.
+ * w describes ONE expert's K x N matrix (4-bit formats; LBQ_ERR_FORMAT otherwise) and
+ * points to expert 0's codes and scales; expert e's lie e * ceil(N/4) * 4 * code_stride
+ * bytes of codes and e * ceil(N/4) * 4 * scale_stride scales behind them. offsets and
+ * slots are read on the device: the call needs no host copy of the routing, so it can be
+ * captured; offsets are clamped to 0 .. R and a slot of no token gives a row of zeros.
+ * Workspace as lbq_expert_workspace_bytes; calls sharing one must not overlap. Each sum
+ * is fp32, rounded to bf16 once.
+ * Errors: those of lbq_gemv, LBQ_ERR_SHAPE (E, T, R or topk out of range). */
+lbq_status lbq_expert_gemm(const lbq_weights* w, int32_t E, const uint16_t* X, int64_t T,
+                           const int32_t* offsets, const int32_t* slots, int32_t topk, int64_t R,
+                           uint16_t* Y, void* workspace, size_t workspace_bytes, void* stream);
 
 /* Size of the scratch array that lbq_gemv_noalloc uses (4 MiB). */
 #define LBQ_NOALLOC_SCRATCH_BYTES (4u << 20)

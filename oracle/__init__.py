@@ -22,7 +22,7 @@ _HERE = os.path.dirname(os.path.abspath(__file__))
 _SRC = os.path.join(_HERE, "lbq_oracle.c")
 _LIB = os.path.join(_HERE, "liblbq_oracle.so")
 
-TERN5, SIGN1, Q2RHT = 1, 2, 3
+TERN5, SIGN1, Q2RHT, Q4G32, Q4G128 = 1, 2, 3, 5, 6
 
 
 def build(force: bool = False) -> str:

@@ -76,7 +76,9 @@ double orc_bf16_to_f64(uint16_t b) {
 /* Format 1 (ternary): 128-weight blocks of 28 bytes = 26 code bytes + fp16 scale,
  *   rows padded to 16 bytes. Format 2 (sign): K/8 code bytes per row, one fp16
  *   scale per 128, scale rows padded with zeros to a multiple of 8 entries.
- *   Format 3 (2-bit): K/4 code bytes per row, one fp16 scale per 32. */
+ *   Format 3 (2-bit): K/4 code bytes per row, one fp16 scale per 32.
+ *   Formats 5 and 6 (4-bit): K/2 code bytes per row, one fp16 scale per 32 or 128,
+ *   scale rows padded as format 2's. */
 int orc_layout(int fmt, int64_t K, int64_t* code_stride, int64_t* scale_stride,
                int64_t* block) {
   int64_t cs, ss, blk;
@@ -95,6 +97,10 @@ int orc_layout(int fmt, int64_t K, int64_t* code_stride, int64_t* scale_stride,
     cs = K / 4;
     ss = K / 32;
     blk = 32;
+  } else if (fmt == 5 || fmt == 6) {
+    blk = fmt == 5 ? 32 : 128;
+    cs = K / 2;
+    ss = (K / blk + 7) / 8 * 8;
   } else {
     return -1;
   }
@@ -151,6 +157,26 @@ static uint16_t q2_scale(const float* w) {
   return orc_f16_from_f64(m);
 }
 
+/* 4-bit: the outermost level 7 is the largest weight's, s = max|w| / 7; q - 8 is the
+ * nearest integer of w / s (ties to even), clipped to -8..7. A zero scale gives 0. */
+static uint16_t q4_scale(const float* w, int n) {
+  double mx = 0.0;
+  for (int k = 0; k < n; ++k) mx = fmax(mx, fabs((double)w[k]));
+  double m = mx / 7.0;
+  return orc_f16_from_f64(m > 65504.0 ? 65504.0 : m);
+}
+
+static int quant4(float w, double s) {
+  if (s == 0.0) return 0;
+  double r = rint((double)w / s);
+  return (int)(r < -8.0 ? -8.0 : (r > 7.0 ? 7.0 : r));
+}
+
+/* Weight k of a 4-bit row sits in nibble (i / 2) + 4 (i % 2) of the four bytes of its
+ * group of eight, i = k % 8: byte offset and shift. */
+static int64_t q4_byte(int64_t k) { return k / 8 * 4 + (k % 8 / 2 + 4 * (k % 2)) / 2; }
+static int q4_shift(int64_t k) { return 4 * ((int)(k % 8 / 2) % 2); }
+
 int orc_pack(int fmt, const float* W, int64_t K, int64_t N, uint8_t* codes,
              uint16_t* scales) {
   int64_t cs, ss, blk;
@@ -187,6 +213,12 @@ int orc_pack(int fmt, const float* W, int64_t K, int64_t N, uint8_t* codes,
         scales[n * ss + b] = absmean_scale(wb, 128);
         for (int k = 0; k < 128; ++k)
           if (wb[k] >= 0.0f) cr[(b * 128 + k) / 8] |= (uint8_t)(1u << (k % 8));
+      } else if (fmt >= 5) {
+        uint16_t h = q4_scale(wb, (int)blk);
+        double s = orc_f16_to_f64(h);
+        scales[n * ss + b] = h;
+        for (int k = 0; k < blk; ++k)
+          cr[q4_byte(b * blk + k)] |= (uint8_t)((quant4(wb[k], s) + 8) << q4_shift(b * blk + k));
       } else {
         uint16_t h = q2_scale(wb);
         double s = orc_f16_to_f64(h);
@@ -234,6 +266,10 @@ int orc_unpack(int fmt, const uint8_t* codes, const uint16_t* scales, int64_t K,
           int64_t kk = b * 128 + k;
           orow[kk] = (cr[kk / 8] >> (kk % 8)) & 1 ? 1 : -1;
         }
+      } else if (fmt >= 5) {
+        s = orc_f16_to_f64(scales[n * ss + b]);
+        for (int64_t kk = b * blk; kk < (b + 1) * blk; ++kk)
+          orow[kk] = (int8_t)(((cr[q4_byte(kk)] >> q4_shift(kk)) & 15) - 8);
       } else {
         s = orc_f16_to_f64(scales[n * ss + b]);
         for (int k = 0; k < 32; ++k) {
