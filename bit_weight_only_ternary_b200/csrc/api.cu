@@ -60,6 +60,7 @@ lbq_status check_operands(const lbq_weights* w, const void* x, int64_t M, const 
   lbq_status st = check_weights(w, L);
   if (st != LBQ_OK) return st;
   if (M < 1) return LBQ_ERR_SHAPE;
+  if (lbq::is_q4(w->fmt) && M > (int64_t{1} << 30)) return LBQ_ERR_SHAPE;
   if (!x || !y) return LBQ_ERR_ARG;
   if (!aligned(x, 16) || !aligned(y, 2)) return LBQ_ERR_ALIGN;
   if (w->fmt == LBQ_Q2RHT) {
@@ -143,12 +144,17 @@ lbq_status check_routing(int64_t T, int32_t topk, int32_t E) {
   return T > kMaxSlots / topk ? LBQ_ERR_SHAPE : LBQ_OK;
 }
 
+// The experts' products: few rows an expert run on the warp-level matrix instructions,
+// more on the tensor cores. The routing is on the device, so the rule takes the average.
+inline bool expert_few(int32_t E, int64_t R) { return R <= 12 * static_cast<int64_t>(E); }
+
 // E matrices of one format and shape behind one another (4-bit formats).
 lbq_status check_expert_weights(const lbq_weights* w, int32_t E, Layout* L) {
   const lbq_status st = check_weights(w, L);
   if (st != LBQ_OK) return st;
   if (!lbq::is_q4(w->fmt)) return LBQ_ERR_FORMAT;
-  return E < 1 || E > LBQ_MAX_EXPERTS ? LBQ_ERR_SHAPE : LBQ_OK;
+  if (E < 1 || E > LBQ_MAX_EXPERTS) return LBQ_ERR_SHAPE;
+  return w->N > (int64_t{1} << 30) / E ? LBQ_ERR_SHAPE : LBQ_OK;  // rows of all experts: 32-bit counts
 }
 }  // namespace
 
@@ -410,7 +416,7 @@ lbq_status lbq_expert_combine_grad(const uint16_t* dout, const uint16_t* Y, int6
 size_t lbq_expert_workspace_bytes(const lbq_weights* w, int32_t E, int64_t R) {
   Layout L;
   if (check_expert_weights(w, E, &L) != LBQ_OK || R < 1 || R > kMaxSlots) return 0;
-  return 0;
+  return expert_few(E, R) ? 0 : lbq_q4_expert_tc_workspace(w, E, R);
 }
 
 lbq_status lbq_expert_gemm(const lbq_weights* w, int32_t E, const uint16_t* X, int64_t T,
@@ -430,7 +436,8 @@ lbq_status lbq_expert_gemm(const lbq_weights* w, int32_t E, const uint16_t* X, i
     if (!aligned(workspace, 16)) return LBQ_ERR_ALIGN;
   }
   const lbq_expert_rows rows = {X, offsets, slots, Y, T, R, topk, E};
-  return from_cuda(lbq_launch_q4_expert_few(w, rows, as_stream(stream)));
+  return from_cuda(expert_few(E, R) ? lbq_launch_q4_expert_few(w, rows, as_stream(stream))
+                                    : lbq_launch_q4_expert_tc(w, rows, workspace, as_stream(stream)));
 }
 
 }  // extern "C"

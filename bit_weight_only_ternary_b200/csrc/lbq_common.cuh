@@ -204,6 +204,12 @@ struct lbq_expert_rows {
   int64_t T, R;
   int32_t topk, E;
 };
+// The same on the tensor cores (q4_tc.cu), for more than a few tokens.
+size_t lbq_q4_tc_workspace(const lbq_weights* w, int64_t M);
+cudaError_t lbq_launch_q4_tc(const lbq_weights* w, const uint16_t* X, int64_t M, uint16_t* Y, void* ws,
+                             cudaStream_t s);
+size_t lbq_q4_expert_tc_workspace(const lbq_weights* w, int32_t E, int64_t R);
+cudaError_t lbq_launch_q4_expert_tc(const lbq_weights* w, const lbq_expert_rows& r, void* ws, cudaStream_t s);
 cudaError_t lbq_launch_q4_expert_few(const lbq_weights* w, const lbq_expert_rows& r, cudaStream_t s);
 // Slots sorted by expert and the rows' way there and back (expert.cu).
 cudaError_t lbq_launch_expert_sort(const void* ids, int id_bytes, int64_t R, int32_t E,

@@ -1,0 +1,827 @@
+// q4_tc.cu -- 4-bit products of many tokens on the 5th-generation tensor cores: one
+// matrix for all rows (lbq_gemm) or a matrix per expert (lbq_expert_gemm).
+//
+// Y[m][n] = sum_k s[n][k/g] (q[n][k] - 8) x[m][k]. The kernel decodes tiles of 128 weight
+// rows x 128 K into tensor memory as fp16 and multiplies them with fp16 activations
+// (tcgen05.mma kind::f16, fp32 accumulators in tensor memory).
+//
+// Roundings. Activations: each row is scaled by a power of two into fp16, exactly; a row
+// that spans more than fp16 holds is flagged and recomputed in fp32 (as in the ternary
+// product). Weights: s (q - 8) has up to 15 significant bits and is rounded to fp16's 11,
+// at most 2^-11 of each term (bf16 would be 2^-8, as much as the final rounding of y
+// itself; keeping q - 8 exact and scaling the accumulators would cost one tensor-memory
+// read and one multiply per accumulator and group of K: for groups of 32 as many fp32
+// operations as the SM has in that time). Every weight row's scales are first multiplied
+// by a power of two that brings the row's largest scale to [2^11, 2^12), so that neither
+// large nor tiny scales leave fp16's normal range; the epilogue undoes both powers.
+//
+// Persistent: one CTA an SM walks over output tiles of 128 weight rows x up to 256 tokens
+// (balanced: a batch or an expert's rows are cut into equal tiles, the matrix instruction
+// takes the tile's own token count rounded up to 16). Warp roles:
+//   warp 0   one lane copies activation slabs (64 K x tokens) with 2D TMA, 32 rows a box
+//   warp 1   allocates tensor memory; one lane issues the MMAs
+//   warp 2   one lane copies packed weights and scales, 256 K x 128 rows a copy
+//   warps 4-19 decode: four threads a weight row, 32 weights of each 128 each; then, four
+//            blocks later (the weight stages are refilled for the next tile first, so the
+//            tensor cores go on as soon as the accumulators have been read), the tile's
+//            epilogue
+// Every wait is bounded (sm100_async.cuh).
+#include <cudaTypedefs.h>
+
+#include "sm100_async.cuh"
+
+namespace {
+
+using namespace lbq;
+
+constexpr int kTileN = 128, kTileK = 128, kMaxTileM = 256;
+constexpr int kStages = 4;             // weight stages in tensor memory
+constexpr int kDec = 4 * kTileN;       // decoder threads
+constexpr int kThreads = 128 + kDec;
+constexpr int kSlabs = 4;              // activation slabs (64 K) in shared memory
+constexpr uint32_t kSlabBytes = kMaxTileM * 128;
+constexpr int kBoxRows = 32;           // tokens per activation copy
+constexpr uint32_t kBoxBytes = kBoxRows * 128;
+// A weight copy: 32 row groups x (2 blocks = 32 words of four rows, plus one word of
+// four rows so that a group's row is 33 16-byte units, an odd number: the eight groups a
+// warp decodes then read from different banks).
+constexpr int kChunkBlocks = 2;
+constexpr uint32_t kGroupWords = 4 * 32 + 4;
+constexpr uint32_t kRawBytes = kGroupWords * 4 * (kTileN / 4);
+constexpr int kRawStages = 4;
+constexpr uint32_t kScaleStage = 2048;  // bytes reserved for a chunk's scales
+// Tensor memory: accumulators in columns [0, 256), weight stage s at 256 + 64 s.
+constexpr uint32_t kTmemCols = 512, kTmemA = 256;
+// Shared memory, from a 1 KB boundary.
+constexpr uint32_t kOffSlab = 0;
+constexpr uint32_t kOffRaw = kOffSlab + kSlabs * kSlabBytes;
+constexpr uint32_t kOffScale = kOffRaw + kRawStages * kRawBytes;
+constexpr uint32_t kOffXe = kOffScale + kRawStages * kScaleStage;  // [256] exponents, [256] flags
+constexpr uint32_t kOffRed = kOffXe + 2 * kMaxTileM * 4;           // [512] floats
+constexpr uint32_t kOffPre = kOffRed + kDec * 4;                   // [E + 1] tiles before expert e
+constexpr uint32_t kOffBar = kOffPre + (LBQ_MAX_EXPERTS + 2) * 4;
+constexpr uint32_t kSmem = kOffBar + 256 + 1024;
+static_assert(kSmem <= 232448, "over the shared-memory limit");
+constexpr unsigned kFaultX = 14, kFaultMma = 15, kFaultW = 16, kFaultDecode = 17, kFaultEpilogue = 18;
+
+struct Args {
+  int64_t K;
+  int32_t N, M;              // rows of one matrix; token rows (sorted rows for experts)
+  int32_t E, groups;         // matrices; row groups of one matrix
+  int32_t tile_m, ntm, splits, kb_split;  // dense: tokens a tile, token tiles, K splits, blocks a split
+  const int32_t* offsets;    // experts: rows of each (null: dense)
+  const int32_t* slots;
+  int32_t topk;
+  int64_t T;
+  const int* xexp;           // token row m was scaled by 2^-xexp[m]
+  const int* xflag;          // 1: row m is recomputed in fp32
+  const int* wexp;           // weight row was scaled by 2^-wexp (rows padded to groups)
+  const uint16_t* X;
+  const uint8_t* codes;
+  const uint16_t* scales;
+  int64_t code_stride, scale_stride;
+  uint16_t* Y;
+  float* part;               // [splits][M][N] partial sums, or null
+  unsigned* fault;
+};
+
+// Source row of sorted row r: its slot's token, or -1.
+__device__ __forceinline__ int64_t source_row(const int32_t* slots, int topk, int64_t T, int64_t r) {
+  if (slots) {
+    const int32_t s = __ldg(slots + r);
+    r = s < 0 ? -1 : s / topk;
+  }
+  return r < T ? r : -1;
+}
+
+__device__ __forceinline__ int clamp_row(int v, int R) { return v < 0 ? 0 : (v > R ? R : v); }
+
+// ------------------------------------------------------------------- preparation
+// Blocks [0, rows): one activation row each to fp16 (exact power-of-two scaling, flag if
+// not exact). The blocks behind: eight groups of four weight rows each, one a warp; the
+// exponent that brings the row's largest scale to [2^11, 2^12).
+__global__ void __launch_bounds__(256)
+    q4_prepare_kernel(const Args a, uint16_t* __restrict__ Xh, int* __restrict__ xexp,
+                      int* __restrict__ xflag, int* __restrict__ wexp, int ngroups) {
+  pdl_launch_dependents();
+  __shared__ float red[8];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (static_cast<int64_t>(blockIdx.x) >= a.M) {
+    const int64_t grp = (static_cast<int64_t>(blockIdx.x) - a.M) * 8 + warp;
+    if (grp >= ngroups) return;
+    const uint2* s = reinterpret_cast<const uint2*>(a.scales + grp * 4 * a.scale_stride);
+    const int ns = static_cast<int>(a.K / a.kb_split);  // (scales a row, passed in kb_split)
+    uint32_t m01 = 0, m23 = 0;
+    for (int e = lane; e < ns; e += 32) {
+      const uint2 v = __ldg(s + e);
+      m01 = __vmaxu2(m01, v.x & 0x7fff7fffu);
+      m23 = __vmaxu2(m23, v.y & 0x7fff7fffu);
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      m01 = __vmaxu2(m01, __shfl_xor_sync(0xffffffffu, m01, o));
+      m23 = __vmaxu2(m23, __shfl_xor_sync(0xffffffffu, m23, o));
+    }
+    if (lane < 4) {
+      const uint32_t h = (lane & 2 ? m23 : m01) >> (16 * (lane & 1)) & 0xffffu;
+      // an infinite or NaN scale makes its row's outputs so whatever the exponent
+      wexp[grp * 4 + lane] = h == 0 ? 0 : (h >= 0x7c00u ? 4 : ilogbf(f16_bits_to_f32(static_cast<uint16_t>(h))) - 11);
+    }
+    return;
+  }
+  const int64_t m = blockIdx.x;
+  int64_t src = m;
+  if (a.offsets) {
+    if (m >= clamp_row(__ldg(a.offsets + a.E), a.M)) return;
+    src = source_row(a.slots, a.topk, a.T, m);
+  }
+  uint4* hr = reinterpret_cast<uint4*>(Xh + m * a.K);
+  const int64_t K8 = a.K / 8;
+  if (src < 0) {  // a slot of no token: zeros
+    for (int64_t k = threadIdx.x; k < K8; k += blockDim.x) hr[k] = make_uint4(0, 0, 0, 0);
+    if (threadIdx.x == 0) xexp[m] = xflag[m] = 0;
+    return;
+  }
+  const uint4* xr = reinterpret_cast<const uint4*>(a.X + src * a.K);
+  auto lo = [](uint32_t w) { return __uint_as_float(w << 16); };
+  auto hi = [](uint32_t w) { return __uint_as_float(w & 0xffff0000u); };
+  float mx = 0.0f;
+  for (int64_t k = threadIdx.x; k < K8; k += blockDim.x) {
+    const uint4 v = xr[k];
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int q = 0; q < 4; ++q) mx = fmaxf(mx, fmaxf(fabsf(lo(w[q])), fabsf(hi(w[q]))));
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+  if (lane == 0) red[warp] = mx;
+  __syncthreads();
+  mx = red[0];
+  for (int i = 1; i < 8; ++i) mx = fmaxf(mx, red[i]);
+  const int e = mx > 0.0f ? ilogbf(mx) - 14 : 0;  // max |x| 2^-e in [2^14, 2^15)
+  bool inexact = false;
+  auto pack = [&inexact](float a0, float a1) {
+    const __half h0 = __float2half_rn(a0), h1 = __float2half_rn(a1);
+    inexact = inexact || __half2float(h0) != a0 || __half2float(h1) != a1;
+    return static_cast<uint32_t>(__half_as_ushort(h0)) | (static_cast<uint32_t>(__half_as_ushort(h1)) << 16);
+  };
+  if (-e >= -126 && -e <= 127) {
+    const float f = __int_as_float((127 - e) << 23);
+    for (int64_t k = threadIdx.x; k < K8; k += blockDim.x) {
+      const uint4 v = xr[k];
+      hr[k] = make_uint4(pack(lo(v.x) * f, hi(v.x) * f), pack(lo(v.y) * f, hi(v.y) * f),
+                         pack(lo(v.z) * f, hi(v.z) * f), pack(lo(v.w) * f, hi(v.w) * f));
+    }
+  } else {
+    for (int64_t k = threadIdx.x; k < K8; k += blockDim.x) {
+      const uint4 v = xr[k];
+      auto sc = [&](float x) { return ldexpf(x, -e); };
+      hr[k] = make_uint4(pack(sc(lo(v.x)), sc(hi(v.x))), pack(sc(lo(v.y)), sc(hi(v.y))),
+                         pack(sc(lo(v.z)), sc(hi(v.z))), pack(sc(lo(v.w)), sc(hi(v.w))));
+    }
+  }
+  const int any = __syncthreads_or(inexact ? 1 : 0);
+  if (threadIdx.x == 0) {
+    xexp[m] = e;
+    xflag[m] = any ? 1 : 0;
+  }
+}
+
+// ----------------------------------------------------------------------- the tiles
+struct Tile {
+  int e, n0;     // matrix, first weight row
+  int m0, cnt;   // first token row, token rows
+  int split, kb0, nkb;
+};
+
+// Token tiles of `cnt` rows: as few as fit, all alike up to 16 rows.
+__device__ __forceinline__ int tiles_for(int cnt) { return (cnt + kMaxTileM - 1) / kMaxTileM; }
+__device__ __forceinline__ int tile_rows(int cnt, int nt) { return ((cnt + nt - 1) / nt + 15) / 16 * 16; }
+
+// Tile `i` of the walk. Token tiles run fastest: the CTAs at work share weight tiles
+// (read from HBM once), and all activations stay in L2.
+__device__ __forceinline__ Tile tile_at(const Args& a, const int* pre, int ntn, int i) {
+  Tile t;
+  const int nkb = static_cast<int>(a.K / kTileK);
+  if (!a.offsets) {
+    const int tm = i % a.ntm, r = i / a.ntm;
+    t.e = 0;
+    t.n0 = (r % ntn) * kTileN;
+    t.split = r / ntn;
+    t.m0 = tm * a.tile_m;
+    t.cnt = a.M - t.m0 < a.tile_m ? a.M - t.m0 : a.tile_m;
+    t.kb0 = t.split * a.kb_split;
+    t.nkb = nkb - t.kb0 < a.kb_split ? nkb - t.kb0 : a.kb_split;
+    return t;
+  }
+  int lo = 0, hi = a.E;  // the expert: the last with pre[e] <= i
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (pre[mid] <= i) lo = mid; else hi = mid;
+  }
+  const int r0 = clamp_row(__ldg(a.offsets + lo), a.M), r1 = clamp_row(__ldg(a.offsets + lo + 1), a.M);
+  const int nt = tiles_for(r1 - r0), rows = tile_rows(r1 - r0, nt), l = i - pre[lo];
+  t.e = lo;
+  t.n0 = (l / nt) * kTileN;
+  t.m0 = r0 + (l % nt) * rows;
+  t.cnt = r1 - t.m0 < rows ? r1 - t.m0 : rows;  // (rounding up may leave the last tile empty: 0 or less)
+  t.split = 0;
+  t.kb0 = 0;
+  t.nkb = nkb;
+  return t;
+}
+
+// Tokens of the matrix instruction, and how many accumulators take its K steps in turn
+// (an instruction on the previous one's accumulator waits for it; small ones are shorter
+// than that wait).
+__device__ __forceinline__ int mma_n(int cnt) { return cnt <= 16 ? 16 : (cnt + 15) / 16 * 16; }
+__device__ __forceinline__ int accs_for(int n) { return n > 128 ? 1 : (n > 64 ? 2 : (n > 32 ? 4 : 8)); }
+
+__device__ __forceinline__ uint64_t sw128_desc(uint32_t saddr) {
+  uint64_t d = static_cast<uint64_t>((saddr >> 4) & 0x3FFFu);
+  d |= static_cast<uint64_t>(1) << 16;
+  d |= static_cast<uint64_t>(1024 >> 4) << 32;
+  d |= static_cast<uint64_t>(1) << 46;
+  d |= static_cast<uint64_t>(2) << 61;
+  return d;
+}
+__device__ __forceinline__ uint32_t idesc_f16_m128(int n) {
+  return (1u << 4) | (static_cast<uint32_t>(n >> 3) << 17) | (static_cast<uint32_t>(128 >> 4) << 24);
+}
+
+__device__ __forceinline__ uint32_t lds32(uint32_t addr) {
+  uint32_t v;
+  asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(addr));
+  return v;
+}
+__device__ __forceinline__ uint32_t lds16(uint32_t addr) {
+  uint16_t v;
+  asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(addr));
+  return v;
+}
+__device__ __forceinline__ bool named_bar_or(uint32_t id, uint32_t count, bool v) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.u32 p, %1, 0;\n\t"
+      "bar.red.or.pred q, %2, %3, p;\n\t"
+      "selp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"(v ? 1u : 0u), "r"(id), "r"(count)
+      : "memory");
+  return r != 0;
+}
+
+// The eight codes of a word as fp16 pairs s (q - 8), in K order. 0x6400 | q is 1024 + q
+// and 0x6400 | 16 q is 1024 + 16 q: q - 8 exactly after one subtraction or one fused
+// multiply-add; the product with s is rounded to fp16.
+__device__ __forceinline__ void decode_word(uint32_t w, __half2 s, uint32_t* out) {
+  const __half2 c1032 = __half2half2(__ushort_as_half(0x6408));   // 1032
+  const __half2 c16th = __half2half2(__ushort_as_half(0x2c00));   // 1/16
+  const __half2 cm72 = __half2half2(__ushort_as_half(0xd480));    // -72
+  const uint32_t w8 = w >> 8;
+  const uint32_t v[4] = {(w & 0x000f000fu) | 0x64006400u, (w & 0x00f000f0u) | 0x64006400u,
+                         (w8 & 0x000f000fu) | 0x64006400u, (w8 & 0x00f000f0u) | 0x64006400u};
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const __half2 h = *reinterpret_cast<const __half2*>(&v[j]);
+    const __half2 q = (j & 1) ? __hfma2(h, c16th, cm72) : __hsub2(h, c1032);
+    const __half2 p = __hmul2(q, s);
+    out[j] = *reinterpret_cast<const uint32_t*>(&p);
+  }
+}
+
+// fp32 recomputation of a tile's flagged tokens by all decoder threads d (four a weight
+// row, each every fourth block of K); put(token, row, value) on threads d < kTileN. The
+// control flow depends on shared data only, so every thread meets every barrier.
+template <int kG, typename Put>
+__device__ __forceinline__ void fixup_flagged(const Args& a, const Tile& t, const int* xf, float* red,
+                                              int d, Put put) {
+  const int row = d & (kTileN - 1), qtr = d / kTileN, n = t.n0 + row;
+  const int64_t grow = static_cast<int64_t>(t.e) * a.groups * 4 + n;
+  for (int i = 0; i < t.cnt; ++i) {
+    if (!xf[i]) continue;
+    const int64_t src = a.offsets ? source_row(a.slots, a.topk, a.T, t.m0 + i) : t.m0 + i;
+    float acc = 0.0f;
+    if (n < a.N && src >= 0) {
+      const uint16_t* x = a.X + src * a.K;
+      for (int kb = t.kb0 + qtr; kb < t.kb0 + t.nkb; kb += 4) {
+        for (int g = 0; g < kTileK / kG; ++g) {
+          const float s = f16_bits_to_f32(__ldg(a.scales + g4_scale_elem(grow, kb * (kTileK / kG) + g, a.scale_stride)));
+          float p = 0.0f;
+          for (int w = 0; w < kG / 8; ++w) {
+            const int64_t wi = static_cast<int64_t>(kb) * (kTileK / 8) + g * (kG / 8) + w;
+            const uint32_t c = __ldg(reinterpret_cast<const uint32_t*>(a.codes + g4_word_byte(grow, wi, a.code_stride)));
+#pragma unroll
+            for (int q = 0; q < 8; ++q) {
+              const int v = static_cast<int>((c >> (4 * ((q >> 1) + 4 * (q & 1)))) & 15u) - 8;
+              p += static_cast<float>(v) * bf16_bits_to_f32(__ldg(x + 8 * wi + q));
+            }
+          }
+          acc += s * p;
+        }
+      }
+    }
+    red[qtr * kTileN + row] = acc;
+    named_bar_sync(3, kDec);
+    if (d < kTileN && n < a.N)
+      put(i, row, ((red[row] + red[kTileN + row]) + red[2 * kTileN + row]) + red[3 * kTileN + row]);
+    named_bar_sync(3, kDec);
+  }
+}
+
+// v * 2^e with one rounding.
+__device__ __forceinline__ float scale_pow2(float v, int e) {
+  return (e >= -126 && e <= 127) ? v * __int_as_float((e + 127) << 23) : ldexpf(v, e);
+}
+
+template <int kG>
+__global__ void __launch_bounds__(kThreads, 1)
+    q4_tc_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_w,
+                 const __grid_constant__ CUtensorMap tm_s, const __grid_constant__ Args a) {
+  extern __shared__ __align__(1024) unsigned char smem_raw[];
+  const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
+  unsigned char* sp = smem_raw + (base - smem_u32(smem_raw));
+  int* pre = reinterpret_cast<int*>(sp + kOffPre);
+  const uint32_t bars = base + kOffBar;
+  const uint32_t fullA = bars, emptyA = fullA + 8 * kStages, fullB = emptyA + 8 * kStages,
+                 emptyB = fullB + 8 * kSlabs, fullR = emptyB + 8 * kSlabs,
+                 emptyR = fullR + 8 * kRawStages, accum = emptyR + 8 * kRawStages, dfree = accum + 8,
+                 tslot = dfree + 8;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  if (tid == 0) {
+    for (int s = 0; s < kStages; ++s) {
+      mbar_init(fullA + 8 * s, kDec / 32);
+      mbar_init(emptyA + 8 * s, 1);
+    }
+    for (int s = 0; s < kSlabs; ++s) {
+      mbar_init(fullB + 8 * s, 1);
+      mbar_init(emptyB + 8 * s, 1);
+    }
+    for (int s = 0; s < kRawStages; ++s) {
+      mbar_init(fullR + 8 * s, 1);
+      mbar_init(emptyR + 8 * s, kDec / 32);
+    }
+    mbar_init(accum, 1);
+    mbar_init(dfree, kDec / 32);
+    fence_mbar_init();
+  }
+  if (warp == 1) {
+    tmem_alloc(tslot, kTmemCols);
+    tmem_relinquish();
+  }
+  pdl_wait();
+  const int ntn = (a.N + kTileN - 1) / kTileN;
+  int total;
+  if (a.offsets) {  // tiles before each expert (warp 0: a running sum, 32 experts at a time)
+    if (warp == 0) {
+      int run = 0;
+      for (int e0 = 0; e0 < a.E; e0 += 32) {
+        const int e = e0 + lane;
+        int c = 0;
+        if (e < a.E) {
+          const int rows = clamp_row(__ldg(a.offsets + e + 1), a.M) - clamp_row(__ldg(a.offsets + e), a.M);
+          c = rows > 0 ? tiles_for(rows) * ntn : 0;
+        }
+        int inc = c;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const int v = __shfl_up_sync(0xffffffffu, inc, o);
+          if (lane >= o) inc += v;
+        }
+        if (e < a.E) pre[e] = run + inc - c;
+        run += __shfl_sync(0xffffffffu, inc, 31);
+      }
+      if (lane == 0) pre[a.E] = run;
+    }
+  }
+  tc_fence_before_sync();
+  __syncthreads();
+  tc_fence_after_sync();
+  total = a.offsets ? pre[a.E] : a.ntm * ntn * a.splits;
+  const uint32_t tmem = lds32(tslot);
+  const int first = static_cast<int>(blockIdx.x), step = static_cast<int>(gridDim.x);
+
+  if (warp == 0) {
+    // ---------------- activations
+    if (lane == 0) {
+      prefetch_tmap(&tm_x);
+      int slab = 0;  // slabs issued
+      bool ok = true;
+      for (int i = first; i < total && ok; i += step) {
+        const Tile t = tile_at(a, pre, ntn, i);
+        if (t.cnt <= 0) continue;
+        const int boxes = (mma_n(t.cnt) + kBoxRows - 1) / kBoxRows;
+        for (int h = 0; h < 2 * t.nkb; ++h) {
+          const int s = slab % kSlabs;
+          if (!mbar_wait(emptyB + 8 * s, (static_cast<uint32_t>(slab / kSlabs) & 1) ^ 1, a.fault, kFaultX)) {
+            ok = false;
+            break;
+          }
+          mbar_arrive_expect_tx(fullB + 8 * s, static_cast<uint32_t>(boxes) * kBoxBytes);
+          for (int b = 0; b < boxes; ++b)
+            tma_load_2d(base + kOffSlab + s * kSlabBytes + b * kBoxBytes, &tm_x, t.kb0 * kTileK + 64 * h,
+                        t.m0 + b * kBoxRows, fullB + 8 * s);
+          ++slab;
+        }
+      }
+      // every issued copy lands before the CTA ends
+      for (int s = slab > kSlabs ? slab - kSlabs : 0; s < slab; ++s)
+        mbar_wait(fullB + 8 * (s % kSlabs), static_cast<uint32_t>(s / kSlabs) & 1, a.fault, kFaultX, false);
+    }
+  } else if (warp == 1) {
+    // ---------------- MMA issue: eight K = 16 steps a weight stage
+    if (lane == 0) {
+      int blk = 0, slab = 0, nt = 0;
+      bool ok = true;
+      for (int i = first; i < total && ok; i += step) {
+        const Tile t = tile_at(a, pre, ntn, i);
+        if (t.cnt <= 0) continue;
+        const int n = mma_n(t.cnt), nacc = accs_for(n);
+        const uint32_t idesc = idesc_f16_m128(n);
+        uint32_t dcol[8];
+#pragma unroll
+        for (int ks = 0; ks < 8; ++ks) dcol[ks] = tmem + static_cast<uint32_t>((ks & (nacc - 1)) * n);
+        // the accumulators are free once the previous tile's have been read
+        ok = mbar_wait(dfree, (static_cast<uint32_t>(nt) & 1) ^ 1, a.fault, kFaultMma);
+        for (int kb = 0; kb < t.nkb && ok; ++kb, ++blk) {
+          const int s = blk % kStages;
+          ok = mbar_wait(fullA + 8 * s, static_cast<uint32_t>(blk / kStages) & 1, a.fault, kFaultMma);
+          if (!ok) break;
+          const uint32_t ta = tmem + kTmemA + 64u * s;
+#pragma unroll
+          for (int h = 0; h < 2; ++h, ++slab) {
+            const int sb = slab % kSlabs;
+            ok = mbar_wait(fullB + 8 * sb, static_cast<uint32_t>(slab / kSlabs) & 1, a.fault, kFaultMma);
+            if (!ok) break;
+            tc_fence_after_sync();
+            const uint64_t bdesc = sw128_desc(base + kOffSlab + sb * kSlabBytes);
+#pragma unroll
+            for (int k4 = 0; k4 < 4; ++k4) {
+              const int ks = 4 * h + k4;
+              mma_f16_ts(dcol[ks], ta + 8u * ks, bdesc + 2u * k4, idesc, (kb > 0 || ks >= nacc) ? 1u : 0u);
+            }
+            mma_commit(emptyB + 8 * sb);
+          }
+          if (!ok) break;
+          mma_commit(emptyA + 8 * s);
+        }
+        mma_commit(accum);
+        ++nt;
+      }
+    }
+    __syncwarp();
+  } else if (warp == 2) {
+    // ---------------- packed weights and scales
+    if (lane == 0) {
+      prefetch_tmap(&tm_w);
+      prefetch_tmap(&tm_s);
+      constexpr uint32_t kScaleBytes = (kChunkBlocks * kTileK / kG) * 8 * (kTileN / 4);
+      int c = 0;
+      bool ok = true;
+      for (int i = first; i < total && ok; i += step) {
+        const Tile t = tile_at(a, pre, ntn, i);
+        if (t.cnt <= 0) continue;
+        const int g0 = t.e * a.groups + t.n0 / 4;
+        for (int kb = t.kb0; kb < t.kb0 + t.nkb; kb += kChunkBlocks) {
+          const int r = c % kRawStages;
+          if (!mbar_wait(emptyR + 8 * r, (static_cast<uint32_t>(c / kRawStages) & 1) ^ 1, a.fault, kFaultW)) {
+            ok = false;
+            break;
+          }
+          mbar_arrive_expect_tx(fullR + 8 * r, kRawBytes + kScaleBytes);
+          tma_load_2d(base + kOffRaw + r * kRawBytes, &tm_w, kb * (kTileK / 8) * 4, g0, fullR + 8 * r);
+          tma_load_2d(base + kOffScale + r * kScaleStage, &tm_s, kb * (kTileK / kG) * 4, g0, fullR + 8 * r);
+          ++c;
+        }
+      }
+      for (int q = c > kRawStages ? c - kRawStages : 0; q < c; ++q)
+        mbar_wait(fullR + 8 * (q % kRawStages), static_cast<uint32_t>(q / kRawStages) & 1, a.fault, kFaultW, false);
+    }
+  } else if (warp >= 4) {
+    // ---------------- decode, and the epilogue kStages blocks behind
+    const int d = tid - 128, row = d & (kTileN - 1), r4 = d >> 7;
+    const int q = warp & 3, grp = (warp - 4) >> 2;  // row = 32 q + lane; grp = r4
+    int* xe = reinterpret_cast<int*>(sp + kOffXe);
+    int* xf = xe + kMaxTileM;
+    float* red = reinterpret_cast<float*>(sp + kOffRed);
+    const uint32_t lane_base = tmem + (static_cast<uint32_t>(32 * q) << 16);
+    const uint32_t tA = lane_base + kTmemA + 16u * r4;
+    const uint32_t myword = 4u * (static_cast<uint32_t>(row >> 2) * kGroupWords + (row & 3)) + 64u * r4;
+    constexpr uint32_t kScalePitch = (kChunkBlocks * kTileK / kG) * 8;  // bytes a row group
+    const uint32_t myscale = static_cast<uint32_t>(row >> 2) * kScalePitch + 2u * (row & 3) + (kG == 32 ? 8u * r4 : 0u);
+    bool ok = true;
+    int blk = 0, chunk = 0, done_tiles = 0;  // blocks stored, chunks read, epilogues finished
+    int pend = first, pend_last = -1;        // the tile whose epilogue is next, its last block
+
+    auto epilogue = [&](int i) {
+      const Tile t = tile_at(a, pre, ntn, i);
+      const int n = mma_n(t.cnt), nacc = accs_for(n);
+      const int nr = t.n0 + 32 * q + lane;
+      bool flagged = false;
+      for (int m = d; m < kMaxTileM; m += kDec) {
+        const bool in = m < t.cnt;
+        xe[m] = in ? __ldg(a.xexp + t.m0 + m) : 0;
+        xf[m] = in ? __ldg(a.xflag + t.m0 + m) : 0;
+        flagged = flagged || xf[m] != 0;
+      }
+      const int we = nr < a.N ? __ldg(a.wexp + static_cast<int64_t>(t.e) * a.groups * 4 + nr) : 0;
+      flagged = named_bar_or(3, kDec, flagged);
+      if (ok) ok = mbar_wait(accum, static_cast<uint32_t>(done_tiles) & 1, a.fault, kFaultEpilogue);
+      __syncwarp();
+      tc_fence_after_sync();
+      float* const part = a.part ? a.part + static_cast<int64_t>(t.split) * a.M * a.N : nullptr;
+      for (int c0 = 16 * grp; c0 < n; c0 += 64) {
+        uint32_t v[16];
+        tmem_ld16(lane_base + static_cast<uint32_t>(c0), v);
+        tmem_ld_wait();
+        for (int j = 1; j < nacc; ++j) {  // accumulators summed in order
+          uint32_t u[16];
+          tmem_ld16(lane_base + static_cast<uint32_t>(j * n + c0), u);
+          tmem_ld_wait();
+#pragma unroll
+          for (int x = 0; x < 16; ++x) v[x] = __float_as_uint(__uint_as_float(v[x]) + __uint_as_float(u[x]));
+        }
+        if (c0 + 64 >= n) {  // this warp's last read of the accumulators
+          tc_fence_before_sync();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(dfree);
+        }
+        if (!ok || nr >= a.N) continue;
+#pragma unroll
+        for (int x = 0; x < 16; ++x) {
+          const int m = c0 + x;
+          if (m < t.cnt && !xf[m]) {
+            const float y = scale_pow2(__uint_as_float(v[x]), xe[m] + we);
+            const int64_t o = static_cast<int64_t>(t.m0 + m) * a.N + nr;
+            if (part) part[o] = y;
+            else a.Y[o] = f32_to_bf16_bits(y);
+          }
+        }
+      }
+      if (16 * grp >= n) {  // nothing to read for this warp
+        __syncwarp();
+        if (lane == 0) mbar_arrive(dfree);
+      }
+      if (flagged)
+        fixup_flagged<kG>(a, t, xf, red, d, [&](int m, int r, float y) {
+          if (!ok) return;
+          const int64_t o = static_cast<int64_t>(t.m0 + m) * a.N + t.n0 + r;
+          if (part) part[o] = y;
+          else a.Y[o] = f32_to_bf16_bits(y);
+        });
+      named_bar_sync(3, kDec);  // xe and xf are free again
+      ++done_tiles;
+    };
+    // the next tile of this CTA from i on that has rows
+    auto skip_empty = [&](int i) {
+      while (i < total && tile_at(a, pre, ntn, i).cnt <= 0) i += step;
+      return i;
+    };
+    uint32_t hv[16];
+    auto publish_prev = [&]() {  // the last block's store has landed: hand its stage over
+      tmem_st_wait();
+      tc_fence_before_sync();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(fullA + 8 * ((blk - 1) % kStages));
+    };
+    pend = skip_empty(first);
+    if (pend < total) pend_last = tile_at(a, pre, ntn, pend).nkb - 1;
+    for (int i = pend; i < total; i = skip_empty(i + step)) {
+      const Tile t = tile_at(a, pre, ntn, i);
+      const int nr = t.n0 + row;
+      const int we = nr < a.N ? __ldg(a.wexp + static_cast<int64_t>(t.e) * a.groups * 4 + nr) : 0;
+      const float wf = __int_as_float((127 - we) << 23);  // 2^-we (we is in -35 .. 4)
+      for (int kb = 0; kb < t.nkb; kb += kChunkBlocks, ++chunk) {
+        const int r = chunk % kRawStages;
+        if (ok) ok = mbar_wait(fullR + 8 * r, static_cast<uint32_t>(chunk / kRawStages) & 1, a.fault, kFaultDecode);
+        __syncwarp();
+        const uint32_t src = base + kOffRaw + r * kRawBytes + myword;
+        const uint32_t ssrc = base + kOffScale + r * kScaleStage + myscale;
+        uint32_t w[2][4], sc[2];
+#pragma unroll
+        for (int b = 0; b < 2; ++b) {
+#pragma unroll
+          for (int x = 0; x < 4; ++x) w[b][x] = lds32(src + 256u * b + 16u * x);
+          sc[b] = lds16(ssrc + (kG == 32 ? 32u : 8u) * b);
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(emptyR + 8 * r);
+#pragma unroll
+        for (int b = 0; b < 2; ++b) {
+          if (kb + b >= t.nkb) break;
+          const __half2 s2 = __half2half2(__float2half_rn(f16_bits_to_f32(static_cast<uint16_t>(sc[b])) * wf));
+#pragma unroll
+          for (int x = 0; x < 4; ++x) decode_word(w[b][x], s2, hv + 4 * x);
+          if (blk > 0) publish_prev();
+          // the epilogue of a tile whose last block is kStages back: every stage is full of
+          // later blocks, so the tensor cores go on as soon as the accumulators are read
+          if (blk - 1 == pend_last + kStages) {
+            epilogue(pend);
+            pend = skip_empty(pend + step);
+            pend_last = pend < total ? pend_last + tile_at(a, pre, ntn, pend).nkb : -1;
+          }
+          const int s = blk % kStages;
+          if (ok) ok = mbar_wait(emptyA + 8 * s, (static_cast<uint32_t>(blk / kStages) & 1) ^ 1, a.fault, kFaultDecode);
+          __syncwarp();
+          tc_fence_after_sync();
+          tmem_st16(tA + 64u * s, hv);
+          ++blk;
+        }
+      }
+    }
+    if (blk > 0) publish_prev();
+    for (; pend < total; pend = skip_empty(pend + step)) epilogue(pend);
+  }
+
+  tc_fence_before_sync();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after_sync();
+    tmem_dealloc(tmem, kTmemCols);
+  }
+}
+
+// Y = bf16(sum over splits of the fp32 partial products), splits in order.
+__global__ void __launch_bounds__(256) q4_split_sum_kernel(const float* __restrict__ part, int splits,
+                                                           int64_t MN, uint16_t* __restrict__ Y) {
+  const int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x;
+  if (i >= MN) return;
+  float sum = 0.0f;
+  for (int z = 0; z < splits; ++z) sum += __ldcg(part + z * MN + i);
+  Y[i] = f32_to_bf16_bits(sum);
+}
+
+struct Plan {
+  int tile_m, ntm, splits, kb_split;
+};
+
+// Dense: equal token tiles; K is split when the tiles alone leave SMs idle.
+Plan plan_for(const lbq_weights* w, int64_t M) {
+  Plan p;
+  p.ntm = static_cast<int>((M + kMaxTileM - 1) / kMaxTileM);
+  p.tile_m = static_cast<int>((M + p.ntm - 1) / p.ntm + 15) / 16 * 16;
+  p.ntm = static_cast<int>((M + p.tile_m - 1) / p.tile_m);
+  const int64_t tiles = (w->N + kTileN - 1) / kTileN * p.ntm;
+  const int nkb = static_cast<int>(w->K / kTileK);
+  int splits = tiles < sm_count() ? static_cast<int>(sm_count() / tiles) : 1;
+  const int most = (nkb + 3) / 4;  // at least four blocks each
+  if (splits > most) splits = most;
+  p.kb_split = ((nkb + splits - 1) / splits + kChunkBlocks - 1) / kChunkBlocks * kChunkBlocks;
+  p.splits = (nkb + p.kb_split - 1) / p.kb_split;
+  return p;
+}
+
+inline size_t align_up(size_t v, size_t a) { return (v + a - 1) / a * a; }
+
+struct Scratch {
+  size_t xh, xexp, xflag, wexp, part, total;
+};
+Scratch scratch_for(const lbq_weights* w, int64_t rows, int E, size_t part_floats) {
+  Scratch s;
+  size_t o = 0;
+  auto take = [&](size_t bytes) {
+    const size_t at = o;
+    o = align_up(o + bytes, 1024);
+    return at;
+  };
+  s.xh = take(static_cast<size_t>(rows) * w->K * 2);
+  s.xexp = take(static_cast<size_t>(rows) * 4);
+  s.xflag = take(static_cast<size_t>(rows) * 4);
+  s.wexp = take(static_cast<size_t>(E) * g4_rows(w->N) * 4);
+  s.part = take(part_floats * 4);
+  s.total = o;
+  return s;
+}
+
+template <int kG>
+cudaError_t configure() {
+  static PerDevice<bool> configured;
+  bool done = false;
+  return configured.get(
+      [](int, bool* v) {
+        *v = true;
+        return cudaFuncSetAttribute(q4_tc_kernel<kG>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                    static_cast<int>(kSmem));
+      },
+      &done);
+}
+
+template <int kG>
+cudaError_t launch(const lbq_weights* w, const Plan& plan, const lbq_expert_rows* er, const uint16_t* X,
+                   int64_t rows, uint16_t* Y, char* ws, cudaStream_t s) {
+  cudaError_t e = configure<kG>();
+  if (e != cudaSuccess) return e;
+  auto encode = tensor_map_encoder();
+  if (!encode) return cudaErrorInvalidValue;
+  const int E = er ? er->E : 1;
+  const int64_t ng = (w->N + 3) / 4;
+  const size_t part_floats = plan.splits > 1 ? static_cast<size_t>(plan.splits) * rows * w->N : 0;
+  const Scratch sc = scratch_for(w, rows, E, part_floats);
+  Args a = {};
+  a.K = w->K;
+  a.N = static_cast<int32_t>(w->N);
+  a.M = static_cast<int32_t>(rows);
+  a.E = E;
+  a.groups = static_cast<int32_t>(ng);
+  a.tile_m = plan.tile_m;
+  a.ntm = plan.ntm;
+  a.splits = plan.splits;
+  if (er) {
+    a.offsets = er->offsets;
+    a.slots = er->slots;
+    a.topk = er->topk;
+    a.T = er->T;
+  }
+  uint16_t* Xh = reinterpret_cast<uint16_t*>(ws + sc.xh);
+  int* xexp = reinterpret_cast<int*>(ws + sc.xexp);
+  int* xflag = reinterpret_cast<int*>(ws + sc.xflag);
+  int* wexp = reinterpret_cast<int*>(ws + sc.wexp);
+  a.xexp = xexp;
+  a.xflag = xflag;
+  a.wexp = wexp;
+  a.X = X;
+  a.codes = static_cast<const uint8_t*>(w->codes);
+  a.scales = static_cast<const uint16_t*>(w->scales);
+  a.code_stride = w->code_stride;
+  a.scale_stride = w->scale_stride;
+  a.Y = Y;
+  a.part = part_floats ? reinterpret_cast<float*>(ws + sc.part) : nullptr;
+  a.fault = lbq_fault_word();
+  if (!a.fault) return cudaErrorInvalidDevicePointer;
+
+  CUtensorMap tx, tw, ts;
+  const cuuint32_t estr[2] = {1, 1};
+  auto map = [&](CUtensorMap* m, CUtensorMapDataType dt, void* p, cuuint64_t cols, cuuint64_t n, cuuint64_t pitch,
+                 cuuint32_t bx, cuuint32_t by, CUtensorMapSwizzle sw) {
+    const cuuint64_t dims[2] = {cols, n};
+    const cuuint64_t strides[1] = {pitch};
+    const cuuint32_t box[2] = {bx, by};
+    return encode(m, dt, 2, p, dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, sw,
+                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+  };
+  const cuuint64_t G = static_cast<cuuint64_t>(E) * ng, cw = static_cast<cuuint64_t>(w->code_stride),
+                   se = static_cast<cuuint64_t>(w->scale_stride) * 4;
+  if (!map(&tx, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, Xh, w->K, rows, static_cast<cuuint64_t>(w->K) * 2, 64, kBoxRows,
+           CU_TENSOR_MAP_SWIZZLE_128B) ||
+      !map(&tw, CU_TENSOR_MAP_DATA_TYPE_UINT32, const_cast<void*>(w->codes), cw, G, cw * 4, kGroupWords, kTileN / 4,
+           CU_TENSOR_MAP_SWIZZLE_NONE) ||
+      !map(&ts, CU_TENSOR_MAP_DATA_TYPE_UINT16, const_cast<void*>(w->scales), se, G, se * 2,
+           (kChunkBlocks * kTileK / kG) * 4, kTileN / 4, CU_TENSOR_MAP_SWIZZLE_NONE))
+    return cudaErrorInvalidValue;
+
+  Args prep = a;
+  prep.kb_split = kG;  // weights a scale
+  const int64_t wblocks = (static_cast<int64_t>(E) * ng + 7) / 8;
+  q4_prepare_kernel<<<static_cast<unsigned>(rows + wblocks), 256, 0, s>>>(prep, Xh, xexp, xflag, wexp,
+                                                                          static_cast<int>(E * ng));
+  e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  a.kb_split = plan.kb_split;
+  const int64_t ntn = (w->N + kTileN - 1) / kTileN;
+  // experts: at most rows / 256 + E token tiles
+  const int64_t most = er ? (rows / kMaxTileM + E) * ntn : static_cast<int64_t>(plan.ntm) * ntn * plan.splits;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(most < sm_count() ? most : sm_count()));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = kSmem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  e = cudaLaunchKernelEx(&cfg, q4_tc_kernel<kG>, tx, tw, ts, a);
+  if (e != cudaSuccess || plan.splits == 1) return e;
+  const int64_t MN = rows * w->N;
+  q4_split_sum_kernel<<<static_cast<unsigned>((MN + 255) / 256), 256, 0, s>>>(a.part, plan.splits, MN, Y);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+// [64 KB left alone: the counter rule][fp16 X][exponents, flags][weight exponents][partials]
+size_t lbq_q4_tc_workspace(const lbq_weights* w, int64_t M) {
+  const Plan p = plan_for(w, M);
+  return kWsCounterBytes +
+         scratch_for(w, M, 1, p.splits > 1 ? static_cast<size_t>(p.splits) * M * w->N : 0).total;
+}
+
+cudaError_t lbq_launch_q4_tc(const lbq_weights* w, const uint16_t* X, int64_t M, uint16_t* Y, void* ws,
+                             cudaStream_t s) {
+  const Plan p = plan_for(w, M);
+  char* base = static_cast<char*>(ws) + kWsCounterBytes;
+  return w->fmt == LBQ_Q4G32 ? launch<32>(w, p, nullptr, X, M, Y, base, s)
+                             : launch<128>(w, p, nullptr, X, M, Y, base, s);
+}
+
+size_t lbq_q4_expert_tc_workspace(const lbq_weights* w, int32_t E, int64_t R) {
+  return scratch_for(w, R, E, 0).total;
+}
+
+cudaError_t lbq_launch_q4_expert_tc(const lbq_weights* w, const lbq_expert_rows& r, void* ws, cudaStream_t s) {
+  const Plan p = {kMaxTileM, 1, 1, static_cast<int>(w->K / kTileK)};
+  char* base = static_cast<char*>(ws);
+  return w->fmt == LBQ_Q4G32 ? launch<32>(w, p, &r, r.X, r.R, r.Y, base, s)
+                             : launch<128>(w, p, &r, r.X, r.R, r.Y, base, s);
+}

@@ -224,6 +224,10 @@ lbq_status lbq_gemv_f32(const lbq_weights* w, const uint16_t* x, const int8_t* D
  * span more than about 2^31) is recomputed in fp32 on the CUDA cores, which is
  * slower but keeps the same accuracy. 1-bit and 2-bit weights: a CUDA-core kernel
  * in which each warp decodes a weight row's blocks once for up to 8 activation rows.
+ * 4-bit weights: up to 16 rows on warp-level matrix instructions with nothing rounded
+ * before the output; more rows as ternary ones on the tensor cores, with the dequantised
+ * weights rounded to fp16 (a relative 2^-11 each; a row's scales below 2^-25 of its
+ * largest one count as subnormal).
  * Same formats, D and workspace rules as lbq_gemv (workspace for this M, from
  * lbq_workspace_bytes). */
 lbq_status lbq_gemm(const lbq_weights* w, const uint16_t* X, int64_t M, const int8_t* D,
@@ -371,7 +375,8 @@ lbq_status lbq_expert_gemm(const lbq_weights* w, int32_t E, const uint16_t* X, i
  * wait that runs out records a non-zero *code (3: shared-memory layout of the
  * batch-1 product, 4-9: tensor-core product stages, 10: the batch-1 product's
  * weight copies, 11: lbq_selftest_wait, 12: unused (lbq_gemv_batch has no waits),
- * 13: lbq_gemv_batch's shared-memory layout) and the kernel returns early with
+ * 13: lbq_gemv_batch's shared-memory layout, 14-18: 4-bit tensor-core product stages)
+ * and the kernel returns early with
  * incomplete outputs instead of hanging. Synchronises the device.
  * Returns LBQ_OK with *code = 0 when no wait gave up, LBQ_ERR_DEVICE_WAIT with the
  * code otherwise. Errors: LBQ_ERR_ARG (code NULL), LBQ_ERR_CUDA. */
