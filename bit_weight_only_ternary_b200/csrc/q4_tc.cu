@@ -15,16 +15,19 @@
 // by a power of two that brings the row's largest scale to [2^11, 2^12), so that neither
 // large nor tiny scales leave fp16's normal range; the epilogue undoes both powers.
 //
-// Persistent: one CTA an SM walks over output tiles of 128 weight rows x up to 256 tokens
-// (balanced: a batch or an expert's rows are cut into equal tiles, the matrix instruction
-// takes the tile's own token count rounded up to 16). Warp roles:
+// Persistent: each pair of CTAs (a cluster of two, cta_group::2) walks over output tiles of
+// 256 weight rows, 128 a CTA, x up to 256 tokens (balanced: a batch or an expert's rows are
+// cut into equal tiles, the matrix instruction takes the tile's own token count rounded up
+// to 16). Each CTA fetches half of the tile's activations, and the tensor cores read both
+// halves: with a CTA on its own every SM fetched all 256 tokens, 64 KB per 128 K and so 17
+// TB/s from L2 at the MMA's own rate, and that bound it (1.42 ms for 4096 x 5120 x 34816).
+// Warp roles:
 //   warp 0   one lane copies activation slabs (64 K x tokens) with 2D TMA, 32 rows a box
-//   warp 1   allocates tensor memory; one lane issues the MMAs
+//   warp 1   allocates tensor memory; in the pair's first CTA one lane issues the MMAs
 //   warp 2   one lane copies packed weights and scales, 256 K x 128 rows a copy
-//   warps 4-19 decode: four threads a weight row, 32 weights of each 128 each; then, four
-//            blocks later (the weight stages are refilled for the next tile first, so the
-//            tensor cores go on as soon as the accumulators have been read), the tile's
-//            epilogue
+//   warps 4-19 decode, four warps a weight stage; then, one block later (the stages are
+//            refilled for the next tile first, so the tensor cores go on as soon as the
+//            accumulators have been read), the tile's epilogue
 // Every wait is bounded (sm100_async.cuh).
 #include <cudaTypedefs.h>
 
@@ -38,8 +41,8 @@ constexpr int kTileN = 128, kTileK = 128, kMaxTileM = 256;
 constexpr int kStages = 4;             // weight stages in tensor memory
 constexpr int kDec = 4 * kTileN;       // decoder threads
 constexpr int kThreads = 128 + kDec;
-constexpr int kSlabs = 4;              // activation slabs (64 K) in shared memory
-constexpr uint32_t kSlabBytes = kMaxTileM * 128;
+constexpr int kSlabs = 8;              // activation slabs (64 K, half the tile's tokens) in shared memory
+constexpr uint32_t kSlabBytes = kMaxTileM / 2 * 128;
 constexpr int kBoxRows = 32;           // tokens per activation copy
 constexpr uint32_t kBoxBytes = kBoxRows * 128;
 // A weight copy: 32 row groups x (2 blocks = 32 words of four rows, plus one word of
@@ -56,11 +59,12 @@ constexpr uint32_t kTmemCols = 512, kTmemA = 256;
 constexpr uint32_t kOffSlab = 0;
 constexpr uint32_t kOffRaw = kOffSlab + kSlabs * kSlabBytes;
 constexpr uint32_t kOffScale = kOffRaw + kRawStages * kRawBytes;
-constexpr uint32_t kOffXe = kOffScale + kRawStages * kScaleStage;  // [256] exponents, [256] flags
-constexpr uint32_t kOffRed = kOffXe + 2 * kMaxTileM * 4;           // [512] floats
+constexpr uint32_t kOffXe = kOffScale + kRawStages * kScaleStage;  // exponents, flags, 2^exponent
+constexpr uint32_t kOffRed = kOffXe + 3 * kMaxTileM * 4;           // [512] floats
 constexpr uint32_t kOffPre = kOffRed + kDec * 4;                   // [E + 1] tiles before expert e
 constexpr uint32_t kOffBar = kOffPre + (LBQ_MAX_EXPERTS + 2) * 4;
-constexpr uint32_t kSmem = kOffBar + 256 + 1024;
+constexpr uint32_t kBarBytes = 8 * (2 * kStages + 2 * kSlabs + 2 * kRawStages + 2) + 8;  // and the TMEM slot
+constexpr uint32_t kSmem = kOffBar + kBarBytes + 1024;
 static_assert(kSmem <= 232448, "over the shared-memory limit");
 constexpr unsigned kFaultX = 14, kFaultMma = 15, kFaultW = 16, kFaultDecode = 17, kFaultEpilogue = 18;
 
@@ -125,7 +129,7 @@ __global__ void __launch_bounds__(256)
     if (lane < 4) {
       const uint32_t h = (lane & 2 ? m23 : m01) >> (16 * (lane & 1)) & 0xffffu;
       // an infinite or NaN scale makes its row's outputs so whatever the exponent
-      wexp[grp * 4 + lane] = h == 0 ? 0 : (h >= 0x7c00u ? 4 : ilogbf(f16_bits_to_f32(static_cast<uint16_t>(h))) - 11);
+      wexp[grp * 4 + lane] = h == 0 ? 0 : (h >= 0x7c00u ? 4 : max(-30, ilogbf(f16_bits_to_f32(static_cast<uint16_t>(h))) - 11));
     }
     return;
   }
@@ -189,7 +193,7 @@ __global__ void __launch_bounds__(256)
 
 // ----------------------------------------------------------------------- the tiles
 struct Tile {
-  int e, n0;     // matrix, first weight row
+  int e, n0;     // matrix, this CTA's first weight row (may lie behind the last)
   int m0, cnt;   // first token row, token rows
   int split, kb0, nkb;
 };
@@ -200,13 +204,13 @@ __device__ __forceinline__ int tile_rows(int cnt, int nt) { return ((cnt + nt - 
 
 // Tile `i` of the walk. Token tiles run fastest: the CTAs at work share weight tiles
 // (read from HBM once), and all activations stay in L2.
-__device__ __forceinline__ Tile tile_at(const Args& a, const int* pre, int ntn, int i) {
+__device__ __forceinline__ Tile tile_at(const Args& a, const int* pre, int ntn, int rank, int i) {
   Tile t;
   const int nkb = static_cast<int>(a.K / kTileK);
   if (!a.offsets) {
     const int tm = i % a.ntm, r = i / a.ntm;
     t.e = 0;
-    t.n0 = (r % ntn) * kTileN;
+    t.n0 = (2 * (r % ntn) + rank) * kTileN;
     t.split = r / ntn;
     t.m0 = tm * a.tile_m;
     t.cnt = a.M - t.m0 < a.tile_m ? a.M - t.m0 : a.tile_m;
@@ -222,7 +226,7 @@ __device__ __forceinline__ Tile tile_at(const Args& a, const int* pre, int ntn, 
   const int r0 = clamp_row(__ldg(a.offsets + lo), a.M), r1 = clamp_row(__ldg(a.offsets + lo + 1), a.M);
   const int nt = tiles_for(r1 - r0), rows = tile_rows(r1 - r0, nt), l = i - pre[lo];
   t.e = lo;
-  t.n0 = (l / nt) * kTileN;
+  t.n0 = (2 * (l / nt) + rank) * kTileN;
   t.m0 = r0 + (l % nt) * rows;
   t.cnt = r1 - t.m0 < rows ? r1 - t.m0 : rows;  // (rounding up may leave the last tile empty: 0 or less)
   t.split = 0;
@@ -245,8 +249,8 @@ __device__ __forceinline__ uint64_t sw128_desc(uint32_t saddr) {
   d |= static_cast<uint64_t>(2) << 61;
   return d;
 }
-__device__ __forceinline__ uint32_t idesc_f16_m128(int n) {
-  return (1u << 4) | (static_cast<uint32_t>(n >> 3) << 17) | (static_cast<uint32_t>(128 >> 4) << 24);
+__device__ __forceinline__ uint32_t idesc_f16_m256(int n) {
+  return (1u << 4) | (static_cast<uint32_t>(n >> 3) << 17) | (static_cast<uint32_t>(256 >> 4) << 24);
 }
 
 __device__ __forceinline__ uint32_t lds32(uint32_t addr) {
@@ -351,7 +355,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (tid == 0) {
     for (int s = 0; s < kStages; ++s) {
-      mbar_init(fullA + 8 * s, kDec / 32);
+      mbar_init(fullA + 8 * s, 2 * kDec / 32 / kStages);  // the stage's four warps of both CTAs
       mbar_init(emptyA + 8 * s, 1);
     }
     for (int s = 0; s < kSlabs; ++s) {
@@ -360,18 +364,16 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int s = 0; s < kRawStages; ++s) {
       mbar_init(fullR + 8 * s, 1);
-      mbar_init(emptyR + 8 * s, kDec / 32);
+      mbar_init(emptyR + 8 * s, kChunkBlocks * kDec / 32 / kStages);
     }
     mbar_init(accum, 1);
-    mbar_init(dfree, kDec / 32);
+    mbar_init(dfree, 2 * kDec / 32);
     fence_mbar_init();
   }
-  if (warp == 1) {
-    tmem_alloc(tslot, kTmemCols);
-    tmem_relinquish();
-  }
+  if (warp == 1) tmem_alloc_pair(tslot, kTmemCols);
   pdl_wait();
-  const int ntn = (a.N + kTileN - 1) / kTileN;
+  const int rank = static_cast<int>(cluster_rank());
+  const int ntn = (a.N + 2 * kTileN - 1) / (2 * kTileN);
   int total;
   if (a.offsets) {  // tiles before each expert (warp 0: a running sum, 32 experts at a time)
     if (warp == 0) {
@@ -397,76 +399,86 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   tc_fence_before_sync();
   __syncthreads();
+  cluster_sync_all();  // the other CTA's barriers and tensor memory are ready too
   tc_fence_after_sync();
   total = a.offsets ? pre[a.E] : a.ntm * ntn * a.splits;
   const uint32_t tmem = lds32(tslot);
-  const int first = static_cast<int>(blockIdx.x), step = static_cast<int>(gridDim.x);
+  const int first = static_cast<int>(blockIdx.x >> 1), step = static_cast<int>(gridDim.x >> 1);
+  // the barriers the first CTA waits on for both
+  const uint32_t fullA0 = map_to_rank(fullA, 0), fullB0 = map_to_rank(fullB, 0), dfree0 = map_to_rank(dfree, 0);
 
   if (warp == 0) {
     // ---------------- activations
     if (lane == 0) {
       prefetch_tmap(&tm_x);
-      int slab = 0;  // slabs issued
+      uint32_t slab = 0;  // slabs issued
       bool ok = true;
       for (int i = first; i < total && ok; i += step) {
-        const Tile t = tile_at(a, pre, ntn, i);
+        const Tile t = tile_at(a, pre, ntn, rank, i);
         if (t.cnt <= 0) continue;
-        const int boxes = (mma_n(t.cnt) + kBoxRows - 1) / kBoxRows;
+        const int half = mma_n(t.cnt) / 2, boxes = (half + kBoxRows - 1) / kBoxRows;
         for (int h = 0; h < 2 * t.nkb; ++h) {
-          const int s = slab % kSlabs;
-          if (!mbar_wait(emptyB + 8 * s, (static_cast<uint32_t>(slab / kSlabs) & 1) ^ 1, a.fault, kFaultX)) {
+          const uint32_t s = slab % kSlabs;
+          if (!mbar_wait(emptyB + 8 * s, ((slab / kSlabs) & 1) ^ 1, a.fault, kFaultX)) {
             ok = false;
             break;
           }
-          mbar_arrive_expect_tx(fullB + 8 * s, static_cast<uint32_t>(boxes) * kBoxBytes);
+          if (rank == 0) mbar_arrive_expect_tx(fullB + 8 * s, 2 * static_cast<uint32_t>(boxes) * kBoxBytes);
           for (int b = 0; b < boxes; ++b)
-            tma_load_2d(base + kOffSlab + s * kSlabBytes + b * kBoxBytes, &tm_x, t.kb0 * kTileK + 64 * h,
-                        t.m0 + b * kBoxRows, fullB + 8 * s);
+            tma_load_2d_pair(base + kOffSlab + s * kSlabBytes + b * kBoxBytes, &tm_x, t.kb0 * kTileK + 64 * h,
+                             t.m0 + rank * half + b * kBoxRows, fullB0 + 8 * s);
           ++slab;
         }
       }
-      // every issued copy lands before the CTA ends
-      for (int s = slab > kSlabs ? slab - kSlabs : 0; s < slab; ++s)
-        mbar_wait(fullB + 8 * (s % kSlabs), static_cast<uint32_t>(s / kSlabs) & 1, a.fault, kFaultX, false);
+      // every issued copy lands before the CTAs end (both halves complete on the first's barriers)
+      if (rank == 0)
+        for (uint32_t s = slab > kSlabs ? slab - kSlabs : 0; s < slab; ++s)
+          mbar_wait_cluster(fullB + 8 * (s % kSlabs), (s / kSlabs) & 1, a.fault, kFaultX, false);
     }
   } else if (warp == 1) {
     // ---------------- MMA issue: eight K = 16 steps a weight stage
-    if (lane == 0) {
-      int blk = 0, slab = 0, nt = 0;
+    if (lane == 0 && rank == 0) {
+      uint32_t blk = 0, slab = 0, nt = 0;
       bool ok = true;
       for (int i = first; i < total && ok; i += step) {
-        const Tile t = tile_at(a, pre, ntn, i);
+        const Tile t = tile_at(a, pre, ntn, rank, i);
         if (t.cnt <= 0) continue;
         const int n = mma_n(t.cnt), nacc = accs_for(n);
-        const uint32_t idesc = idesc_f16_m128(n);
+        const uint32_t idesc = idesc_f16_m256(n);
         uint32_t dcol[8];
 #pragma unroll
         for (int ks = 0; ks < 8; ++ks) dcol[ks] = tmem + static_cast<uint32_t>((ks & (nacc - 1)) * n);
         // the accumulators are free once the previous tile's have been read
-        ok = mbar_wait(dfree, (static_cast<uint32_t>(nt) & 1) ^ 1, a.fault, kFaultMma);
+        ok = mbar_wait_cluster(dfree, (nt & 1) ^ 1, a.fault, kFaultMma);
         for (int kb = 0; kb < t.nkb && ok; ++kb, ++blk) {
-          const int s = blk % kStages;
-          ok = mbar_wait(fullA + 8 * s, static_cast<uint32_t>(blk / kStages) & 1, a.fault, kFaultMma);
+          const uint32_t s = blk % kStages;
+          ok = mbar_wait_cluster(fullA + 8 * s, (blk / kStages) & 1, a.fault, kFaultMma);
           if (!ok) break;
           const uint32_t ta = tmem + kTmemA + 64u * s;
 #pragma unroll
           for (int h = 0; h < 2; ++h, ++slab) {
-            const int sb = slab % kSlabs;
-            ok = mbar_wait(fullB + 8 * sb, static_cast<uint32_t>(slab / kSlabs) & 1, a.fault, kFaultMma);
+            const uint32_t sb = slab % kSlabs;
+            ok = mbar_wait_cluster(fullB + 8 * sb, (slab / kSlabs) & 1, a.fault, kFaultMma);
             if (!ok) break;
             tc_fence_after_sync();
             const uint64_t bdesc = sw128_desc(base + kOffSlab + sb * kSlabBytes);
 #pragma unroll
             for (int k4 = 0; k4 < 4; ++k4) {
               const int ks = 4 * h + k4;
-              mma_f16_ts(dcol[ks], ta + 8u * ks, bdesc + 2u * k4, idesc, (kb > 0 || ks >= nacc) ? 1u : 0u);
+              mma_f16_ts_pair(dcol[ks], ta + 8u * ks, bdesc + 2u * k4, idesc, (kb > 0 || ks >= nacc) ? 1u : 0u);
             }
-            mma_commit(emptyB + 8 * sb);
+            mma_commit_pair(emptyB + 8 * sb);
           }
           if (!ok) break;
-          mma_commit(emptyA + 8 * s);
+          mma_commit_pair(emptyA + 8 * s);
         }
-        mma_commit(accum);
+        if ((t.nkb & 1) && ok) {  // the last chunk's second stage holds no block of this tile
+          const uint32_t s = blk % kStages;
+          ok = mbar_wait_cluster(fullA + 8 * s, (blk / kStages) & 1, a.fault, kFaultMma);
+          mma_commit_pair(emptyA + 8 * s);
+          ++blk;
+        }
+        mma_commit_pair(accum);
         ++nt;
       }
     }
@@ -477,15 +489,15 @@ __global__ void __launch_bounds__(kThreads, 1)
       prefetch_tmap(&tm_w);
       prefetch_tmap(&tm_s);
       constexpr uint32_t kScaleBytes = (kChunkBlocks * kTileK / kG) * 8 * (kTileN / 4);
-      int c = 0;
+      uint32_t c = 0;
       bool ok = true;
       for (int i = first; i < total && ok; i += step) {
-        const Tile t = tile_at(a, pre, ntn, i);
+        const Tile t = tile_at(a, pre, ntn, rank, i);
         if (t.cnt <= 0) continue;
         const int g0 = t.e * a.groups + t.n0 / 4;
         for (int kb = t.kb0; kb < t.kb0 + t.nkb; kb += kChunkBlocks) {
-          const int r = c % kRawStages;
-          if (!mbar_wait(emptyR + 8 * r, (static_cast<uint32_t>(c / kRawStages) & 1) ^ 1, a.fault, kFaultW)) {
+          const uint32_t r = c % kRawStages;
+          if (!mbar_wait(emptyR + 8 * r, ((c / kRawStages) & 1) ^ 1, a.fault, kFaultW)) {
             ok = false;
             break;
           }
@@ -495,150 +507,201 @@ __global__ void __launch_bounds__(kThreads, 1)
           ++c;
         }
       }
-      for (int q = c > kRawStages ? c - kRawStages : 0; q < c; ++q)
-        mbar_wait(fullR + 8 * (q % kRawStages), static_cast<uint32_t>(q / kRawStages) & 1, a.fault, kFaultW, false);
+      for (uint32_t q = c > kRawStages ? c - kRawStages : 0; q < c; ++q)
+        mbar_wait(fullR + 8 * (q % kRawStages), (q / kRawStages) & 1, a.fault, kFaultW, false);
     }
   } else if (warp >= 4) {
-    // ---------------- decode, and the epilogue kStages blocks behind
-    const int d = tid - 128, row = d & (kTileN - 1), r4 = d >> 7;
-    const int q = warp & 3, grp = (warp - 4) >> 2;  // row = 32 q + lane; grp = r4
+    // ---------------- decode: weight stage g belongs to warp group g (four warps, one
+    // thread a weight row), which decodes every fourth block into it. The groups' chains
+    // (wait for the codes, decode, wait for the stage, store) overlap; with all sixteen
+    // warps on every block the chain's latency bounded the rate (0.88 us a block, 128 x 64)
+    const int d = tid - 128, row = d & (kTileN - 1), grp = d >> 7;
+    const int q = warp & 3;  // row = 32 q + lane
     int* xe = reinterpret_cast<int*>(sp + kOffXe);
     int* xf = xe + kMaxTileM;
+    float* xs = reinterpret_cast<float*>(xf + kMaxTileM);
     float* red = reinterpret_cast<float*>(sp + kOffRed);
     const uint32_t lane_base = tmem + (static_cast<uint32_t>(32 * q) << 16);
-    const uint32_t tA = lane_base + kTmemA + 16u * r4;
-    const uint32_t myword = 4u * (static_cast<uint32_t>(row >> 2) * kGroupWords + (row & 3)) + 64u * r4;
-    constexpr uint32_t kScalePitch = (kChunkBlocks * kTileK / kG) * 8;  // bytes a row group
-    const uint32_t myscale = static_cast<uint32_t>(row >> 2) * kScalePitch + 2u * (row & 3) + (kG == 32 ? 8u * r4 : 0u);
+    const uint32_t tA = lane_base + kTmemA + 64u * grp;
+    constexpr uint32_t kScales = kTileK / kG;  // scales a block
+    const uint32_t myword = base + kOffRaw + 4u * (static_cast<uint32_t>(row >> 2) * kGroupWords + (row & 3)) + 256u * (grp & 1);
+    const uint32_t myscale = base + kOffScale + static_cast<uint32_t>(row >> 2) * (kChunkBlocks * kScales * 8) +
+                             2u * (row & 3) + 8u * kScales * (grp & 1);
     bool ok = true;
-    int blk = 0, chunk = 0, done_tiles = 0;  // blocks stored, chunks read, epilogues finished
-    int pend = first, pend_last = -1;        // the tile whose epilogue is next, its last block
+    uint32_t done_tiles = 0;       // epilogues finished
+    int pend = first;              // the tile whose epilogue is next
+    int64_t pend_last = -1;        // its last block
 
     auto epilogue = [&](int i) {
-      const Tile t = tile_at(a, pre, ntn, i);
+      const Tile t = tile_at(a, pre, ntn, rank, i);
       const int n = mma_n(t.cnt), nacc = accs_for(n);
       const int nr = t.n0 + 32 * q + lane;
-      bool flagged = false;
+      // the tokens' exponents; special: some token is flagged, or the two powers of two
+      // cannot be multiplied into one normal float
+      bool special = false;
       for (int m = d; m < kMaxTileM; m += kDec) {
         const bool in = m < t.cnt;
-        xe[m] = in ? __ldg(a.xexp + t.m0 + m) : 0;
+        const int e = in ? __ldg(a.xexp + t.m0 + m) : 0;
+        xe[m] = e;
+        xs[m] = __int_as_float((e + 127) << 23);
         xf[m] = in ? __ldg(a.xflag + t.m0 + m) : 0;
-        flagged = flagged || xf[m] != 0;
+        special = special || xf[m] != 0 || e < -85 || e > 115;
       }
       const int we = nr < a.N ? __ldg(a.wexp + static_cast<int64_t>(t.e) * a.groups * 4 + nr) : 0;
-      flagged = named_bar_or(3, kDec, flagged);
-      if (ok) ok = mbar_wait(accum, static_cast<uint32_t>(done_tiles) & 1, a.fault, kFaultEpilogue);
+      const float ws = __int_as_float((127 + we) << 23);  // 2^we (we is in -30 .. 4)
+      special = named_bar_or(3, kDec, special);
+      if (ok) ok = mbar_wait(accum, done_tiles & 1, a.fault, kFaultEpilogue);
       __syncwarp();
       tc_fence_after_sync();
-      float* const part = a.part ? a.part + static_cast<int64_t>(t.split) * a.M * a.N : nullptr;
-      for (int c0 = 16 * grp; c0 < n; c0 += 64) {
-        uint32_t v[16];
+      // this warp's columns 16 grp + 64 c + (0..15), the accumulators summed in order
+      auto read16 = [&](int c0, uint32_t (&v)[16]) {
         tmem_ld16(lane_base + static_cast<uint32_t>(c0), v);
         tmem_ld_wait();
-        for (int j = 1; j < nacc; ++j) {  // accumulators summed in order
+        for (int j = 1; j < nacc; ++j) {
           uint32_t u[16];
           tmem_ld16(lane_base + static_cast<uint32_t>(j * n + c0), u);
           tmem_ld_wait();
 #pragma unroll
           for (int x = 0; x < 16; ++x) v[x] = __float_as_uint(__uint_as_float(v[x]) + __uint_as_float(u[x]));
         }
-        if (c0 + 64 >= n) {  // this warp's last read of the accumulators
-          tc_fence_before_sync();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(dfree);
-        }
-        if (!ok || nr >= a.N) continue;
+      };
+      auto release = [&]() {  // the accumulators may be overwritten
+        tc_fence_before_sync();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cluster(dfree0);
+      };
+      if (!special && !a.part) {
+        // all columns are read, scaled and rounded first, so that the tensor cores wait for
+        // the reads only; the stores run beside the next tile's instructions
+        uint32_t y[4][8];
 #pragma unroll
-        for (int x = 0; x < 16; ++x) {
-          const int m = c0 + x;
-          if (m < t.cnt && !xf[m]) {
-            const float y = scale_pow2(__uint_as_float(v[x]), xe[m] + we);
-            const int64_t o = static_cast<int64_t>(t.m0 + m) * a.N + nr;
-            if (part) part[o] = y;
-            else a.Y[o] = f32_to_bf16_bits(y);
+        for (int c = 0; c < 4; ++c) {
+          const int c0 = 16 * grp + 64 * c;
+          if (c0 >= n) break;
+          uint32_t v[16];
+          read16(c0, v);
+#pragma unroll
+          for (int x = 0; x < 16; x += 2) {
+            const float2 f = *reinterpret_cast<const float2*>(xs + c0 + x);
+            y[c][x / 2] = f32_to_bf16_bits(__uint_as_float(v[x]) * (f.x * ws)) |
+                          static_cast<uint32_t>(f32_to_bf16_bits(__uint_as_float(v[x + 1]) * (f.y * ws))) << 16;
           }
         }
+        release();
+        if (ok && nr < a.N) {
+          uint16_t* yp = a.Y + static_cast<int64_t>(t.m0) * a.N + nr;
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            const int c0 = 16 * grp + 64 * c;
+            if (c0 >= t.cnt) break;
+            uint16_t* yc = yp + static_cast<int64_t>(c0) * a.N;
+#pragma unroll
+            for (int x = 0; x < 16; ++x)
+              if (c0 + x < t.cnt) yc[static_cast<int64_t>(x) * a.N] = static_cast<uint16_t>(y[c][x / 2] >> (16 * (x & 1)));
+          }
+        }
+      } else {
+        float* const part = a.part ? a.part + static_cast<int64_t>(t.split) * a.M * a.N : nullptr;
+        for (int c0 = 16 * grp; c0 < n; c0 += 64) {
+          uint32_t v[16];
+          read16(c0, v);
+          if (!ok || nr >= a.N) continue;
+#pragma unroll
+          for (int x = 0; x < 16; ++x) {
+            const int m = c0 + x;
+            if (m < t.cnt && !xf[m]) {
+              const float y = special ? scale_pow2(__uint_as_float(v[x]), xe[m] + we) : __uint_as_float(v[x]) * (xs[m] * ws);
+              const int64_t o = static_cast<int64_t>(t.m0 + m) * a.N + nr;
+              if (part) part[o] = y;
+              else a.Y[o] = f32_to_bf16_bits(y);
+            }
+          }
+        }
+        release();
+        if (special)
+          fixup_flagged<kG>(a, t, xf, red, d, [&](int m, int r, float y) {
+            if (!ok) return;
+            const int64_t o = static_cast<int64_t>(t.m0 + m) * a.N + t.n0 + r;
+            if (part) part[o] = y;
+            else a.Y[o] = f32_to_bf16_bits(y);
+          });
       }
-      if (16 * grp >= n) {  // nothing to read for this warp
-        __syncwarp();
-        if (lane == 0) mbar_arrive(dfree);
-      }
-      if (flagged)
-        fixup_flagged<kG>(a, t, xf, red, d, [&](int m, int r, float y) {
-          if (!ok) return;
-          const int64_t o = static_cast<int64_t>(t.m0 + m) * a.N + t.n0 + r;
-          if (part) part[o] = y;
-          else a.Y[o] = f32_to_bf16_bits(y);
-        });
-      named_bar_sync(3, kDec);  // xe and xf are free again
+      named_bar_sync(3, kDec);  // the shared arrays are free again
       ++done_tiles;
     };
     // the next tile of this CTA from i on that has rows
     auto skip_empty = [&](int i) {
-      while (i < total && tile_at(a, pre, ntn, i).cnt <= 0) i += step;
+      while (i < total && tile_at(a, pre, ntn, rank, i).cnt <= 0) i += step;
       return i;
     };
-    uint32_t hv[16];
-    auto publish_prev = [&]() {  // the last block's store has landed: hand its stage over
-      tmem_st_wait();
-      tc_fence_before_sync();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(fullA + 8 * ((blk - 1) % kStages));
-    };
     pend = skip_empty(first);
-    if (pend < total) pend_last = tile_at(a, pre, ntn, pend).nkb - 1;
+    if (pend < total) pend_last = (tile_at(a, pre, ntn, rank, pend).nkb + 1) / 2 * 2 - 1;
+    int64_t blk0 = 0;     // blocks and chunks of the tiles before
+    uint32_t chunk0 = 0;
     for (int i = pend; i < total; i = skip_empty(i + step)) {
-      const Tile t = tile_at(a, pre, ntn, i);
+      const Tile t = tile_at(a, pre, ntn, rank, i);
       const int nr = t.n0 + row;
       const int we = nr < a.N ? __ldg(a.wexp + static_cast<int64_t>(t.e) * a.groups * 4 + nr) : 0;
-      const float wf = __int_as_float((127 - we) << 23);  // 2^-we (we is in -35 .. 4)
-      for (int kb = 0; kb < t.nkb; kb += kChunkBlocks, ++chunk) {
-        const int r = chunk % kRawStages;
-        if (ok) ok = mbar_wait(fullR + 8 * r, static_cast<uint32_t>(chunk / kRawStages) & 1, a.fault, kFaultDecode);
+      // 2^-we as two fp16 factors (we is in -30 .. 4)
+      const int we1 = we < -15 ? -15 : we;
+      const __half2 f1 = __half2half2(__ushort_as_half(static_cast<uint16_t>((15 - we1) << 10)));
+      const __half2 f2 = __half2half2(__ushort_as_half(static_cast<uint16_t>((15 - (we - we1)) << 10)));
+      // the tile's blocks are dealt to the groups two by two: chunk c (two blocks) to the
+      // groups 0 and 1 or 2 and 3
+      const uint32_t nch = static_cast<uint32_t>(t.nkb + kChunkBlocks - 1) / kChunkBlocks;
+      for (uint32_t c = ((chunk0 & 1) ^ static_cast<uint32_t>(grp >> 1)); c < nch; c += 2) {
+        const uint32_t r = (chunk0 + c) % kRawStages;
+        if (ok) ok = mbar_wait(fullR + 8 * r, ((chunk0 + c) / kRawStages) & 1, a.fault, kFaultDecode);
         __syncwarp();
-        const uint32_t src = base + kOffRaw + r * kRawBytes + myword;
-        const uint32_t ssrc = base + kOffScale + r * kScaleStage + myscale;
-        uint32_t w[2][4], sc[2];
+        uint32_t w[16];
 #pragma unroll
-        for (int b = 0; b < 2; ++b) {
+        for (int x = 0; x < 16; ++x) w[x] = lds32(myword + r * kRawBytes + 16u * x);
+        uint32_t sc[kScales];
 #pragma unroll
-          for (int x = 0; x < 4; ++x) w[b][x] = lds32(src + 256u * b + 16u * x);
-          sc[b] = lds16(ssrc + (kG == 32 ? 32u : 8u) * b);
-        }
+        for (int x = 0; x < static_cast<int>(kScales); ++x) sc[x] = lds16(myscale + r * kScaleStage + 8u * x);
         __syncwarp();
         if (lane == 0) mbar_arrive(emptyR + 8 * r);
+        // (an odd number of blocks: the last chunk's second one is zeros to its group)
+        const uint32_t use = (chunk0 + c) / 2;  // the stage's uses before this one
+        if (ok) ok = mbar_wait(emptyA + 8 * grp, (use & 1) ^ 1, a.fault, kFaultDecode);
+        __syncwarp();
+        tc_fence_after_sync();
 #pragma unroll
-        for (int b = 0; b < 2; ++b) {
-          if (kb + b >= t.nkb) break;
-          const __half2 s2 = __half2half2(__float2half_rn(f16_bits_to_f32(static_cast<uint16_t>(sc[b])) * wf));
+        for (int x = 0; x < 4; ++x) {  // 32 weights at a time
+          const __half2 sx = __half2half2(__ushort_as_half(static_cast<uint16_t>(sc[kG == 32 ? x : 0])));
+          const __half2 s2 = __hmul2(__hmul2(sx, f1), f2);
+          uint32_t hv[16];
 #pragma unroll
-          for (int x = 0; x < 4; ++x) decode_word(w[b][x], s2, hv + 4 * x);
-          if (blk > 0) publish_prev();
-          // the epilogue of a tile whose last block is kStages back: every stage is full of
-          // later blocks, so the tensor cores go on as soon as the accumulators are read
-          if (blk - 1 == pend_last + kStages) {
-            epilogue(pend);
-            pend = skip_empty(pend + step);
-            pend_last = pend < total ? pend_last + tile_at(a, pre, ntn, pend).nkb : -1;
-          }
-          const int s = blk % kStages;
-          if (ok) ok = mbar_wait(emptyA + 8 * s, (static_cast<uint32_t>(blk / kStages) & 1) ^ 1, a.fault, kFaultDecode);
-          __syncwarp();
-          tc_fence_after_sync();
-          tmem_st16(tA + 64u * s, hv);
-          ++blk;
+          for (int y = 0; y < 4; ++y) decode_word(w[4 * x + y], s2, hv + 4 * y);
+          tmem_st16(tA + 16u * x, hv);
+        }
+        tmem_st_wait();
+        tc_fence_before_sync();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cluster(fullA0 + 8 * grp);
+        // Tiles that ended before this block: their epilogues. The stages then hold later
+        // blocks, so the tensor cores go on as soon as the accumulators are read. (Each
+        // group comes here after its first block behind the tile, which waits only for
+        // blocks of that tile or earlier ones: no circle of waits.)
+        const int64_t b = blk0 + 2 * static_cast<int64_t>(c) + (grp & 1);
+        while (pend < total && pend_last < b) {
+          epilogue(pend);
+          pend = skip_empty(pend + step);
+          if (pend < total) pend_last += (tile_at(a, pre, ntn, rank, pend).nkb + 1) / 2 * 2;
         }
       }
+      blk0 += 2 * static_cast<int64_t>(nch);
+      chunk0 += nch;
     }
-    if (blk > 0) publish_prev();
     for (; pend < total; pend = skip_empty(pend + step)) epilogue(pend);
   }
 
   tc_fence_before_sync();
   __syncthreads();
+  cluster_sync_all();  // neither CTA leaves while the other's MMAs or arrivals reach into it
   if (warp == 1) {
     tc_fence_after_sync();
-    tmem_dealloc(tmem, kTmemCols);
+    tmem_dealloc_pair(tmem, kTmemCols);
   }
 }
 
@@ -662,9 +725,9 @@ Plan plan_for(const lbq_weights* w, int64_t M) {
   p.ntm = static_cast<int>((M + kMaxTileM - 1) / kMaxTileM);
   p.tile_m = static_cast<int>((M + p.ntm - 1) / p.ntm + 15) / 16 * 16;
   p.ntm = static_cast<int>((M + p.tile_m - 1) / p.tile_m);
-  const int64_t tiles = (w->N + kTileN - 1) / kTileN * p.ntm;
+  const int64_t tiles = (w->N + 2 * kTileN - 1) / (2 * kTileN) * p.ntm, pairs = sm_count() / 2;
   const int nkb = static_cast<int>(w->K / kTileK);
-  int splits = tiles < sm_count() ? static_cast<int>(sm_count() / tiles) : 1;
+  int splits = tiles < pairs ? static_cast<int>(pairs / tiles) : 1;
   const int most = (nkb + 3) / 4;  // at least four blocks each
   if (splits > most) splits = most;
   p.kb_split = ((nkb + splits - 1) / splits + kChunkBlocks - 1) / kChunkBlocks * kChunkBlocks;
@@ -778,19 +841,23 @@ cudaError_t launch(const lbq_weights* w, const Plan& plan, const lbq_expert_rows
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   a.kb_split = plan.kb_split;
-  const int64_t ntn = (w->N + kTileN - 1) / kTileN;
+  const int64_t ntn = (w->N + 2 * kTileN - 1) / (2 * kTileN), pairs = sm_count() / 2;
   // experts: at most rows / 256 + E token tiles
   const int64_t most = er ? (rows / kMaxTileM + E) * ntn : static_cast<int64_t>(plan.ntm) * ntn * plan.splits;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(most < sm_count() ? most : sm_count()));
+  cfg.gridDim = dim3(2 * static_cast<unsigned>(most < pairs ? most : pairs));
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = kSmem;
   cfg.stream = s;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = 2;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = 2;
   e = cudaLaunchKernelEx(&cfg, q4_tc_kernel<kG>, tx, tw, ts, a);
   if (e != cudaSuccess || plan.splits == 1) return e;
   const int64_t MN = rows * w->N;
