@@ -38,11 +38,10 @@ namespace {
 using namespace lbq;
 
 constexpr int kTileN = 128, kTileK = 128, kMaxTileM = 256;
-constexpr int kStages = 4;             // weight stages in tensor memory
+constexpr int kStages = 4;             // stages of one 128 x 128 weight block and its activations
 constexpr int kDec = 4 * kTileN;       // decoder threads
 constexpr int kThreads = 128 + kDec;
-constexpr int kSlabs = 8;              // activation slabs (64 K, half the tile's tokens) in shared memory
-constexpr uint32_t kSlabBytes = kMaxTileM / 2 * 128;
+constexpr uint32_t kSlabBytes = kMaxTileM / 2 * 128;  // activations: 64 K of half the tile's tokens
 constexpr int kBoxRows = 32;           // tokens per activation copy
 constexpr uint32_t kBoxBytes = kBoxRows * 128;
 // A weight copy: 32 row groups x (2 blocks = 32 words of four rows, plus one word of
@@ -57,13 +56,13 @@ constexpr uint32_t kScaleStage = 2048;  // bytes reserved for a chunk's scales
 constexpr uint32_t kTmemCols = 512, kTmemA = 256;
 // Shared memory, from a 1 KB boundary.
 constexpr uint32_t kOffSlab = 0;
-constexpr uint32_t kOffRaw = kOffSlab + kSlabs * kSlabBytes;
+constexpr uint32_t kOffRaw = kOffSlab + kStages * 2 * kSlabBytes;
 constexpr uint32_t kOffScale = kOffRaw + kRawStages * kRawBytes;
 constexpr uint32_t kOffXe = kOffScale + kRawStages * kScaleStage;  // exponents, flags, 2^exponent
 constexpr uint32_t kOffRed = kOffXe + 3 * kMaxTileM * 4;           // [512] floats
 constexpr uint32_t kOffPre = kOffRed + kDec * 4;                   // [E + 1] tiles before expert e
 constexpr uint32_t kOffBar = kOffPre + (LBQ_MAX_EXPERTS + 2) * 4;
-constexpr uint32_t kBarBytes = 8 * (2 * kStages + 2 * kSlabs + 2 * kRawStages + 2) + 8;  // and the TMEM slot
+constexpr uint32_t kBarBytes = 8 * (2 * kStages + 2 * kRawStages + 2) + 8;  // and the TMEM slot
 constexpr uint32_t kSmem = kOffBar + kBarBytes + 1024;
 static_assert(kSmem <= 232448, "over the shared-memory limit");
 constexpr unsigned kFaultX = 14, kFaultMma = 15, kFaultW = 16, kFaultDecode = 17, kFaultEpilogue = 18;
@@ -348,19 +347,15 @@ __global__ void __launch_bounds__(kThreads, 1)
   unsigned char* sp = smem_raw + (base - smem_u32(smem_raw));
   int* pre = reinterpret_cast<int*>(sp + kOffPre);
   const uint32_t bars = base + kOffBar;
-  const uint32_t fullA = bars, emptyA = fullA + 8 * kStages, fullB = emptyA + 8 * kStages,
-                 emptyB = fullB + 8 * kSlabs, fullR = emptyB + 8 * kSlabs,
+  const uint32_t full = bars, empty = full + 8 * kStages, fullR = empty + 8 * kStages,
                  emptyR = fullR + 8 * kRawStages, accum = emptyR + 8 * kRawStages, dfree = accum + 8,
                  tslot = dfree + 8;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (tid == 0) {
     for (int s = 0; s < kStages; ++s) {
-      mbar_init(fullA + 8 * s, 2 * kDec / 32 / kStages);  // the stage's four warps of both CTAs
-      mbar_init(emptyA + 8 * s, 1);
-    }
-    for (int s = 0; s < kSlabs; ++s) {
-      mbar_init(fullB + 8 * s, 1);
-      mbar_init(emptyB + 8 * s, 1);
+      // the stage's four decoder warps of both CTAs, and the first CTA's activation lane
+      mbar_init(full + 8 * s, 2 * kDec / 32 / kStages + 1);
+      mbar_init(empty + 8 * s, 1);
     }
     for (int s = 0; s < kRawStages; ++s) {
       mbar_init(fullR + 8 * s, 1);
@@ -402,87 +397,85 @@ __global__ void __launch_bounds__(kThreads, 1)
   cluster_sync_all();  // the other CTA's barriers and tensor memory are ready too
   tc_fence_after_sync();
   total = a.offsets ? pre[a.E] : a.ntm * ntn * a.splits;
-  const uint32_t tmem = lds32(tslot);
+  // All 512 columns are allocated, so the allocation starts at column 0; a constant keeps
+  // the MMA loop's addresses in uniform registers.
+  constexpr uint32_t tmem = 0;
   const int first = static_cast<int>(blockIdx.x >> 1), step = static_cast<int>(gridDim.x >> 1);
   // the barriers the first CTA waits on for both
-  const uint32_t fullA0 = map_to_rank(fullA, 0), fullB0 = map_to_rank(fullB, 0), dfree0 = map_to_rank(dfree, 0);
+  const uint32_t full0 = map_to_rank(full, 0), dfree0 = map_to_rank(dfree, 0);
 
   if (warp == 0) {
     // ---------------- activations
     if (lane == 0) {
       prefetch_tmap(&tm_x);
-      uint32_t slab = 0;  // slabs issued
+      uint32_t blk = 0;  // stages filled
       bool ok = true;
       for (int i = first; i < total && ok; i += step) {
         const Tile t = tile_at(a, pre, ntn, rank, i);
         if (t.cnt <= 0) continue;
         const int half = mma_n(t.cnt) / 2, boxes = (half + kBoxRows - 1) / kBoxRows;
-        for (int h = 0; h < 2 * t.nkb; ++h) {
-          const uint32_t s = slab % kSlabs;
-          if (!mbar_wait(emptyB + 8 * s, ((slab / kSlabs) & 1) ^ 1, a.fault, kFaultX)) {
+        for (int kb = 0; kb < (t.nkb + 1) / 2 * 2; ++kb, ++blk) {
+          const uint32_t s = blk % kStages;
+          if (!mbar_wait(empty + 8 * s, ((blk / kStages) & 1) ^ 1, a.fault, kFaultX)) {
             ok = false;
             break;
           }
-          if (rank == 0) mbar_arrive_expect_tx(fullB + 8 * s, 2 * static_cast<uint32_t>(boxes) * kBoxBytes);
-          for (int b = 0; b < boxes; ++b)
-            tma_load_2d_pair(base + kOffSlab + s * kSlabBytes + b * kBoxBytes, &tm_x, t.kb0 * kTileK + 64 * h,
-                             t.m0 + rank * half + b * kBoxRows, fullB0 + 8 * s);
-          ++slab;
+          if (kb == t.nkb) {  // an odd number of blocks: the last chunk's second stage stays unused
+            if (rank == 0) mbar_arrive(full + 8 * s);
+            continue;
+          }
+          if (rank == 0) mbar_arrive_expect_tx(full + 8 * s, 4 * static_cast<uint32_t>(boxes) * kBoxBytes);
+          for (int h = 0; h < 2; ++h)
+            for (int b = 0; b < boxes; ++b)
+              tma_load_2d_pair(base + kOffSlab + (2 * s + h) * kSlabBytes + b * kBoxBytes, &tm_x,
+                               (t.kb0 + kb) * kTileK + 64 * h, t.m0 + rank * half + b * kBoxRows, full0 + 8 * s);
         }
       }
       // every issued copy lands before the CTAs end (both halves complete on the first's barriers)
       if (rank == 0)
-        for (uint32_t s = slab > kSlabs ? slab - kSlabs : 0; s < slab; ++s)
-          mbar_wait_cluster(fullB + 8 * (s % kSlabs), (s / kSlabs) & 1, a.fault, kFaultX, false);
+        for (uint32_t q = blk > kStages ? blk - kStages : 0; q < blk; ++q)
+          mbar_wait_cluster(full + 8 * (q % kStages), (q / kStages) & 1, a.fault, kFaultX, false);
     }
   } else if (warp == 1) {
-    // ---------------- MMA issue: eight K = 16 steps a weight stage
-    if (lane == 0 && rank == 0) {
-      uint32_t blk = 0, slab = 0, nt = 0;
+    // ---------------- MMA issue: eight K = 16 steps a stage, one wait and one commit. The
+    // whole warp walks the loop and one elected lane issues, so that the loop's values
+    // stay in uniform registers (issued from a branch on lane 0, and with separate
+    // barriers for weights and two activation slabs, a block took 0.74 us at any size).
+    if (rank == 0) {
+      uint32_t blk = 0, nt = 0;
       bool ok = true;
       for (int i = first; i < total && ok; i += step) {
         const Tile t = tile_at(a, pre, ntn, rank, i);
         if (t.cnt <= 0) continue;
         const int n = mma_n(t.cnt), nacc = accs_for(n);
         const uint32_t idesc = idesc_f16_m256(n);
-        uint32_t dcol[8];
-#pragma unroll
-        for (int ks = 0; ks < 8; ++ks) dcol[ks] = tmem + static_cast<uint32_t>((ks & (nacc - 1)) * n);
         // the accumulators are free once the previous tile's have been read
         ok = mbar_wait_cluster(dfree, (nt & 1) ^ 1, a.fault, kFaultMma);
-        for (int kb = 0; kb < t.nkb && ok; ++kb, ++blk) {
+        for (int kb = 0; kb < (t.nkb + 1) / 2 * 2; ++kb, ++blk) {
           const uint32_t s = blk % kStages;
-          ok = mbar_wait_cluster(fullA + 8 * s, (blk / kStages) & 1, a.fault, kFaultMma);
+          if (ok) ok = mbar_wait_cluster(full + 8 * s, (blk / kStages) & 1, a.fault, kFaultMma);
+          ok = __all_sync(0xffffffffu, ok);
           if (!ok) break;
-          const uint32_t ta = tmem + kTmemA + 64u * s;
+          tc_fence_after_sync();
+          if (elect_one()) {
+            if (kb < t.nkb) {
+              const uint32_t ta = tmem + kTmemA + 64u * s;
+              const uint64_t bdesc = sw128_desc(base + kOffSlab + 2 * s * kSlabBytes);
 #pragma unroll
-          for (int h = 0; h < 2; ++h, ++slab) {
-            const uint32_t sb = slab % kSlabs;
-            ok = mbar_wait_cluster(fullB + 8 * sb, (slab / kSlabs) & 1, a.fault, kFaultMma);
-            if (!ok) break;
-            tc_fence_after_sync();
-            const uint64_t bdesc = sw128_desc(base + kOffSlab + sb * kSlabBytes);
-#pragma unroll
-            for (int k4 = 0; k4 < 4; ++k4) {
-              const int ks = 4 * h + k4;
-              mma_f16_ts_pair(dcol[ks], ta + 8u * ks, bdesc + 2u * k4, idesc, (kb > 0 || ks >= nacc) ? 1u : 0u);
+              for (int ks = 0; ks < 8; ++ks)
+                mma_f16_ts_pair(tmem + static_cast<uint32_t>((ks & (nacc - 1)) * n), ta + 8u * ks,
+                                bdesc + (ks >> 2) * (kSlabBytes >> 4) + 2u * (ks & 3), idesc,
+                                (kb > 0 || ks >= nacc) ? 1u : 0u);
             }
-            mma_commit_pair(emptyB + 8 * sb);
+            mma_commit_pair(empty + 8 * s);
           }
-          if (!ok) break;
-          mma_commit_pair(emptyA + 8 * s);
+          __syncwarp();
         }
-        if ((t.nkb & 1) && ok) {  // the last chunk's second stage holds no block of this tile
-          const uint32_t s = blk % kStages;
-          ok = mbar_wait_cluster(fullA + 8 * s, (blk / kStages) & 1, a.fault, kFaultMma);
-          mma_commit_pair(emptyA + 8 * s);
-          ++blk;
-        }
-        mma_commit_pair(accum);
+        if (elect_one()) mma_commit_pair(accum);
+        __syncwarp();
         ++nt;
       }
     }
-    __syncwarp();
   } else if (warp == 2) {
     // ---------------- packed weights and scales
     if (lane == 0) {
@@ -663,7 +656,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) mbar_arrive(emptyR + 8 * r);
         // (an odd number of blocks: the last chunk's second one is zeros to its group)
         const uint32_t use = (chunk0 + c) / 2;  // the stage's uses before this one
-        if (ok) ok = mbar_wait(emptyA + 8 * grp, (use & 1) ^ 1, a.fault, kFaultDecode);
+        if (ok) ok = mbar_wait(empty + 8 * grp, (use & 1) ^ 1, a.fault, kFaultDecode);
         __syncwarp();
         tc_fence_after_sync();
 #pragma unroll
@@ -678,7 +671,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         tmem_st_wait();
         tc_fence_before_sync();
         __syncwarp();
-        if (lane == 0) mbar_arrive_cluster(fullA0 + 8 * grp);
+        if (lane == 0) mbar_arrive_cluster(full0 + 8 * grp);
         // Tiles that ended before this block: their epilogues. The stages then hold later
         // blocks, so the tensor cores go on as soon as the accumulators are read. (Each
         // group comes here after its first block behind the tile, which waits only for
