@@ -275,6 +275,12 @@ __device__ __forceinline__ bool named_bar_or(uint32_t id, uint32_t count, bool v
   return r != 0;
 }
 
+__device__ __forceinline__ uint32_t and_or(uint32_t a, uint32_t b, uint32_t c) {
+  uint32_t d;
+  asm("lop3.b32 %0, %1, %2, %3, 0xea;" : "=r"(d) : "r"(a), "r"(b), "r"(c));  // (a & b) | c
+  return d;
+}
+
 // The eight codes of a word as fp16 pairs s (q - 8), in K order. 0x6400 | q is 1024 + q
 // and 0x6400 | 16 q is 1024 + 16 q: q - 8 exactly after one subtraction or one fused
 // multiply-add; the product with s is rounded to fp16.
@@ -283,8 +289,8 @@ __device__ __forceinline__ void decode_word(uint32_t w, __half2 s, uint32_t* out
   const __half2 c16th = __half2half2(__ushort_as_half(0x2c00));   // 1/16
   const __half2 cm72 = __half2half2(__ushort_as_half(0xd480));    // -72
   const uint32_t w8 = w >> 8;
-  const uint32_t v[4] = {(w & 0x000f000fu) | 0x64006400u, (w & 0x00f000f0u) | 0x64006400u,
-                         (w8 & 0x000f000fu) | 0x64006400u, (w8 & 0x00f000f0u) | 0x64006400u};
+  const uint32_t v[4] = {and_or(w, 0x000f000fu, 0x64006400u), and_or(w, 0x00f000f0u, 0x64006400u),
+                         and_or(w8, 0x000f000fu, 0x64006400u), and_or(w8, 0x00f000f0u, 0x64006400u)};
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
     const __half2 h = *reinterpret_cast<const __half2*>(&v[j]);
@@ -434,7 +440,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // every issued copy lands before the CTAs end (both halves complete on the first's barriers)
       if (rank == 0)
         for (uint32_t q = blk > kStages ? blk - kStages : 0; q < blk; ++q)
-          mbar_wait_cluster(full + 8 * (q % kStages), (q / kStages) & 1, a.fault, kFaultX, false);
+          mbar_wait(full + 8 * (q % kStages), (q / kStages) & 1, a.fault, kFaultX, false);
     }
   } else if (warp == 1) {
     // ---------------- MMA issue: eight K = 16 steps a stage, one wait and one commit. The
@@ -450,10 +456,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int n = mma_n(t.cnt), nacc = accs_for(n);
         const uint32_t idesc = idesc_f16_m256(n);
         // the accumulators are free once the previous tile's have been read
-        ok = mbar_wait_cluster(dfree, (nt & 1) ^ 1, a.fault, kFaultMma);
+        ok = mbar_wait(dfree, (nt & 1) ^ 1, a.fault, kFaultMma);
         for (int kb = 0; kb < (t.nkb + 1) / 2 * 2; ++kb, ++blk) {
           const uint32_t s = blk % kStages;
-          if (ok) ok = mbar_wait_cluster(full + 8 * s, (blk / kStages) & 1, a.fault, kFaultMma);
+          if (ok) ok = mbar_wait(full + 8 * s, (blk / kStages) & 1, a.fault, kFaultMma);
           ok = __all_sync(0xffffffffu, ok);
           if (!ok) break;
           tc_fence_after_sync();

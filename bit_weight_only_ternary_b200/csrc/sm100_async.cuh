@@ -223,36 +223,11 @@ __device__ __forceinline__ uint32_t map_to_rank(uint32_t saddr, uint32_t rank) {
 __device__ __forceinline__ void cluster_sync_all() {
   asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
 }
-// Arrives on a barrier of any CTA of the cluster (address from map_to_rank).
+// Arrives on a barrier of any CTA of the cluster (address from map_to_rank). It orders
+// tensor-memory accesses (with the tcgen05 fences around it), not generic writes: a
+// release at cluster scope costs a memory barrier of several hundred cycles.
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar) {
-  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
-}
-__device__ __forceinline__ bool mbar_try_wait_cluster(uint32_t bar, uint32_t parity, uint32_t ns) {
-  uint32_t ok;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, %3;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(ok)
-      : "r"(bar), "r"(parity), "r"(ns)
-      : "memory");
-  return ok != 0;
-}
-// mbar_wait for a barrier on which the other CTA arrives too.
-__device__ __forceinline__ bool mbar_wait_cluster(uint32_t bar, uint32_t parity, unsigned* fault,
-                                                  unsigned code, bool give_up_after_fault = true) {
-  if (mbar_try_wait_cluster(bar, parity, 1000000u)) return true;
-  const uint64_t t0 = global_ns();
-  for (uint32_t i = 1;; ++i) {
-    if (mbar_try_wait_cluster(bar, parity, 1000000u)) return true;
-    if ((i & 15) == 0) {
-      if (give_up_after_fault && *reinterpret_cast<volatile unsigned*>(fault) != 0) return false;
-      if (global_ns() - t0 > kWaitLimitNs) {
-        atomicExch(fault, code);
-        return false;
-      }
-    }
-  }
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 // 2D tiled TMA load into this CTA's shared memory, completing on a barrier of either CTA
 // of the pair (address from map_to_rank).
