@@ -22,7 +22,8 @@
 // halves: with a CTA on its own every SM fetched all 256 tokens, 64 KB per 128 K and so 17
 // TB/s from L2 at the MMA's own rate, and that bound it (1.42 ms for 4096 x 5120 x 34816).
 // Warp roles:
-//   warp 0   one lane copies activation slabs (64 K x tokens) with 2D TMA, 32 rows a box
+//   warp 0   one lane copies activations (128 K x tokens), one 3D TMA a block: issuing four
+//            or eight boxes of 32 rows a block took longer than the matrix instructions
 //   warp 1   allocates tensor memory; in the pair's first CTA one lane issues the MMAs
 //   warp 2   one lane copies packed weights and scales, 256 K x 128 rows a copy
 //   warps 4-19 decode, four warps a weight stage; then, one block later (the stages are
@@ -42,8 +43,12 @@ constexpr int kStages = 4;             // stages of one 128 x 128 weight block a
 constexpr int kDec = 4 * kTileN;       // decoder threads
 constexpr int kThreads = 128 + kDec;
 constexpr uint32_t kSlabBytes = kMaxTileM / 2 * 128;  // activations: 64 K of half the tile's tokens
-constexpr int kBoxRows = 32;           // tokens per activation copy
-constexpr uint32_t kBoxBytes = kBoxRows * 128;
+// An activation copy brings 128 K (two 128-byte swizzled halves) of a CTA's tokens at once:
+// a tensor map for every multiple of kBoxStep tokens up to 128.
+constexpr int kBoxStep = 16, kBoxes = kMaxTileM / 2 / kBoxStep;
+struct XMaps {
+  CUtensorMap m[kBoxes];
+};
 // A weight copy: 32 row groups x (2 blocks = 32 words of four rows, plus one word of
 // four rows so that a group's row is 33 16-byte units, an odd number: the eight groups a
 // warp decodes then read from different banks).
@@ -346,7 +351,7 @@ __device__ __forceinline__ float scale_pow2(float v, int e) {
 
 template <int kG>
 __global__ void __launch_bounds__(kThreads, 1)
-    q4_tc_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_w,
+    q4_tc_kernel(const __grid_constant__ XMaps tm_x, const __grid_constant__ CUtensorMap tm_w,
                  const __grid_constant__ CUtensorMap tm_s, const __grid_constant__ Args a) {
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
@@ -413,13 +418,13 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == 0) {
     // ---------------- activations
     if (lane == 0) {
-      prefetch_tmap(&tm_x);
       uint32_t blk = 0;  // stages filled
       bool ok = true;
       for (int i = first; i < total && ok; i += step) {
         const Tile t = tile_at(a, pre, ntn, rank, i);
         if (t.cnt <= 0) continue;
-        const int half = mma_n(t.cnt) / 2, boxes = (half + kBoxRows - 1) / kBoxRows;
+        const int half = mma_n(t.cnt) / 2, box = (half + kBoxStep - 1) / kBoxStep;
+        const CUtensorMap* map = &tm_x.m[box - 1];
         for (int kb = 0; kb < (t.nkb + 1) / 2 * 2; ++kb, ++blk) {
           const uint32_t s = blk % kStages;
           if (!mbar_wait(empty + 8 * s, ((blk / kStages) & 1) ^ 1, a.fault, kFaultX)) {
@@ -430,11 +435,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (rank == 0) mbar_arrive(full + 8 * s);
             continue;
           }
-          if (rank == 0) mbar_arrive_expect_tx(full + 8 * s, 4 * static_cast<uint32_t>(boxes) * kBoxBytes);
-          for (int h = 0; h < 2; ++h)
-            for (int b = 0; b < boxes; ++b)
-              tma_load_2d_pair(base + kOffSlab + (2 * s + h) * kSlabBytes + b * kBoxBytes, &tm_x,
-                               (t.kb0 + kb) * kTileK + 64 * h, t.m0 + rank * half + b * kBoxRows, full0 + 8 * s);
+          if (rank == 0) mbar_arrive_expect_tx(full + 8 * s, static_cast<uint32_t>(box) * (2 * 2 * kBoxStep * 128));
+          tma_load_3d_pair(base + kOffSlab + 2 * s * kSlabBytes, map, 0, t.m0 + rank * half, t.kb0 * 2 + 2 * kb, full0 + 8 * s);
         }
       }
       // every issued copy lands before the CTAs end (both halves complete on the first's barriers)
@@ -455,6 +457,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (t.cnt <= 0) continue;
         const int n = mma_n(t.cnt), nacc = accs_for(n);
         const uint32_t idesc = idesc_f16_m256(n);
+        const uint32_t half_k = static_cast<uint32_t>((n / 2 + kBoxStep - 1) / kBoxStep) * (kBoxStep * 128 >> 4);
         // the accumulators are free once the previous tile's have been read
         ok = mbar_wait(dfree, (nt & 1) ^ 1, a.fault, kFaultMma);
         for (int kb = 0; kb < (t.nkb + 1) / 2 * 2; ++kb, ++blk) {
@@ -470,7 +473,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
               for (int ks = 0; ks < 8; ++ks)
                 mma_f16_ts_pair(tmem + static_cast<uint32_t>((ks & (nacc - 1)) * n), ta + 8u * ks,
-                                bdesc + (ks >> 2) * (kSlabBytes >> 4) + 2u * (ks & 3), idesc,
+                                bdesc + (ks >> 2) * half_k + 2u * (ks & 3), idesc,
                                 (kb > 0 || ks >= nacc) ? 1u : 0u);
             }
             mma_commit_pair(empty + 8 * s);
@@ -812,7 +815,8 @@ cudaError_t launch(const lbq_weights* w, const Plan& plan, const lbq_expert_rows
   a.fault = lbq_fault_word();
   if (!a.fault) return cudaErrorInvalidDevicePointer;
 
-  CUtensorMap tx, tw, ts;
+  XMaps tx;
+  CUtensorMap tw, ts;
   const cuuint32_t estr[2] = {1, 1};
   auto map = [&](CUtensorMap* m, CUtensorMapDataType dt, void* p, cuuint64_t cols, cuuint64_t n, cuuint64_t pitch,
                  cuuint32_t bx, cuuint32_t by, CUtensorMapSwizzle sw) {
@@ -824,9 +828,17 @@ cudaError_t launch(const lbq_weights* w, const Plan& plan, const lbq_expert_rows
   };
   const cuuint64_t G = static_cast<cuuint64_t>(E) * ng, cw = static_cast<cuuint64_t>(w->code_stride),
                    se = static_cast<cuuint64_t>(w->scale_stride) * 4;
-  if (!map(&tx, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, Xh, w->K, rows, static_cast<cuuint64_t>(w->K) * 2, 64, kBoxRows,
-           CU_TENSOR_MAP_SWIZZLE_128B) ||
-      !map(&tw, CU_TENSOR_MAP_DATA_TYPE_UINT32, const_cast<void*>(w->codes), cw, G, cw * 4, kGroupWords, kTileN / 4,
+  for (int i = 0; i < kBoxes; ++i) {
+    const cuuint64_t dims[3] = {64, static_cast<cuuint64_t>(rows), static_cast<cuuint64_t>(w->K / 64)};
+    const cuuint64_t strides[2] = {static_cast<cuuint64_t>(w->K) * 2, 128};
+    const cuuint32_t box[3] = {64, static_cast<cuuint32_t>((i + 1) * kBoxStep), 2};
+    const cuuint32_t estr3[3] = {1, 1, 1};
+    if (encode(&tx.m[i], CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, Xh, dims, strides, box, estr3,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+      return cudaErrorInvalidValue;
+  }
+  if (!map(&tw, CU_TENSOR_MAP_DATA_TYPE_UINT32, const_cast<void*>(w->codes), cw, G, cw * 4, kGroupWords, kTileN / 4,
            CU_TENSOR_MAP_SWIZZLE_NONE) ||
       !map(&ts, CU_TENSOR_MAP_DATA_TYPE_UINT16, const_cast<void*>(w->scales), se, G, se * 2,
            (kChunkBlocks * kTileK / kG) * 4, kTileN / 4, CU_TENSOR_MAP_SWIZZLE_NONE))
