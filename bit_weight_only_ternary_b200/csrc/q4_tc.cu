@@ -63,11 +63,14 @@ constexpr uint32_t kTmemCols = 512, kTmemA = 256;
 constexpr uint32_t kOffSlab = 0;
 constexpr uint32_t kOffRaw = kOffSlab + kStages * 2 * kSlabBytes;
 constexpr uint32_t kOffScale = kOffRaw + kRawStages * kRawBytes;
-constexpr uint32_t kOffXe = kOffScale + kRawStages * kScaleStage;  // exponents, flags, 2^exponent
-constexpr uint32_t kOffRed = kOffXe + 3 * kMaxTileM * 4;           // [512] floats
+constexpr int kInfos = 2;  // tiles whose tokens' exponents are in shared memory
+constexpr uint32_t kInfoBytes = (3 * kMaxTileM + 4) * 4;  // exponents, flags, 2^exponent; special
+constexpr uint32_t kOffInfo = kOffScale + kRawStages * kScaleStage;
+constexpr uint32_t kOffRed = kOffInfo + kInfos * kInfoBytes;  // [512] floats
 constexpr uint32_t kOffPre = kOffRed + kDec * 4;                   // [E + 1] tiles before expert e
-constexpr uint32_t kOffBar = kOffPre + (LBQ_MAX_EXPERTS + 2) * 4;
-constexpr uint32_t kBarBytes = 8 * (2 * kStages + 2 * kRawStages + 2) + 8;  // and the TMEM slot
+constexpr uint32_t kOffFirst = kOffPre + (LBQ_MAX_EXPERTS + 2) * 4;  // [E + 1] offsets, clamped
+constexpr uint32_t kOffBar = kOffFirst + (LBQ_MAX_EXPERTS + 2) * 4;
+constexpr uint32_t kBarBytes = 8 * (2 * kStages + 2 * kRawStages + 2 * kInfos + 2) + 8;  // and the TMEM slot
 constexpr uint32_t kSmem = kOffBar + kBarBytes + 1024;
 static_assert(kSmem <= 232448, "over the shared-memory limit");
 constexpr unsigned kFaultX = 14, kFaultMma = 15, kFaultW = 16, kFaultDecode = 17, kFaultEpilogue = 18;
@@ -105,21 +108,27 @@ __device__ __forceinline__ int64_t source_row(const int32_t* slots, int topk, in
 __device__ __forceinline__ int clamp_row(int v, int R) { return v < 0 ? 0 : (v > R ? R : v); }
 
 // ------------------------------------------------------------------- preparation
-// Blocks [0, rows): one activation row each to fp16 (exact power-of-two scaling, flag if
-// not exact). The blocks behind: eight groups of four weight rows each, one a warp; the
-// exponent that brings the row's largest scale to [2^11, 2^12).
+// The first blocks convert activation rows to fp16, kRow threads a row (exact power-of-two
+// scaling, flag if not exact): a whole block for few long rows, where latency counts, a
+// warp for many (a block a row took 107 us for 32768 rows of 2048, most of it launching
+// blocks). The blocks behind take groups of four weight rows, one a warp: the exponent
+// that brings a row's largest scale to [2^11, 2^12).
+template <int kRow>
 __global__ void __launch_bounds__(256)
     q4_prepare_kernel(const Args a, uint16_t* __restrict__ Xh, int* __restrict__ xexp,
-                      int* __restrict__ xflag, int* __restrict__ wexp, int ngroups) {
+                      int* __restrict__ xflag, int* __restrict__ wexp, int ngroups, int group) {
   pdl_launch_dependents();
+  constexpr int kRows = 256 / kRow;  // rows a block
   __shared__ float red[8];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  if (static_cast<int64_t>(blockIdx.x) >= a.M) {
-    const int64_t grp = (static_cast<int64_t>(blockIdx.x) - a.M) * 8 + warp;
+  const int64_t xblocks = (static_cast<int64_t>(a.M) + kRows - 1) / kRows;
+  if (static_cast<int64_t>(blockIdx.x) >= xblocks) {
+    const int64_t grp = (static_cast<int64_t>(blockIdx.x) - xblocks) * 8 + warp;
     if (grp >= ngroups) return;
     const uint2* s = reinterpret_cast<const uint2*>(a.scales + grp * 4 * a.scale_stride);
-    const int ns = static_cast<int>(a.K / a.kb_split);  // (scales a row, passed in kb_split)
+    const int ns = static_cast<int>(a.K / group);
     uint32_t m01 = 0, m23 = 0;
+#pragma unroll 4
     for (int e = lane; e < ns; e += 32) {
       const uint2 v = __ldg(s + e);
       m01 = __vmaxu2(m01, v.x & 0x7fff7fffu);
@@ -137,35 +146,41 @@ __global__ void __launch_bounds__(256)
     }
     return;
   }
-  const int64_t m = blockIdx.x;
+  // this thread's row and its place among the row's threads (kRow = 256: all on one row)
+  const int64_t m = static_cast<int64_t>(blockIdx.x) * kRows + threadIdx.x / kRow;
+  const int u = threadIdx.x % kRow;
+  if (m >= a.M) return;
   int64_t src = m;
   if (a.offsets) {
     if (m >= clamp_row(__ldg(a.offsets + a.E), a.M)) return;
     src = source_row(a.slots, a.topk, a.T, m);
   }
   uint4* hr = reinterpret_cast<uint4*>(Xh + m * a.K);
-  const int64_t K8 = a.K / 8;
+  const int K8 = static_cast<int>(a.K / 8);
   if (src < 0) {  // a slot of no token: zeros
-    for (int64_t k = threadIdx.x; k < K8; k += blockDim.x) hr[k] = make_uint4(0, 0, 0, 0);
-    if (threadIdx.x == 0) xexp[m] = xflag[m] = 0;
+    for (int k = u; k < K8; k += kRow) hr[k] = make_uint4(0, 0, 0, 0);
+    if (u == 0) xexp[m] = xflag[m] = 0;
     return;
   }
   const uint4* xr = reinterpret_cast<const uint4*>(a.X + src * a.K);
   auto lo = [](uint32_t w) { return __uint_as_float(w << 16); };
   auto hi = [](uint32_t w) { return __uint_as_float(w & 0xffff0000u); };
-  float mx = 0.0f;
-  for (int64_t k = threadIdx.x; k < K8; k += blockDim.x) {
+  uint32_t mb = 0;  // largest magnitude, as bf16 bits in both halves
+#pragma unroll 8
+  for (int k = u; k < K8; k += kRow) {
     const uint4 v = xr[k];
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-    for (int q = 0; q < 4; ++q) mx = fmaxf(mx, fmaxf(fabsf(lo(w[q])), fabsf(hi(w[q]))));
+    mb = __vmaxu2(mb, __vmaxu2(__vmaxu2(v.x & 0x7fff7fffu, v.y & 0x7fff7fffu),
+                               __vmaxu2(v.z & 0x7fff7fffu, v.w & 0x7fff7fffu)));
   }
+  float mx = fmaxf(lo(mb), hi(mb));
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-  if (lane == 0) red[warp] = mx;
-  __syncthreads();
-  mx = red[0];
-  for (int i = 1; i < 8; ++i) mx = fmaxf(mx, red[i]);
+  if (kRow == 256) {
+    if (lane == 0) red[warp] = mx;
+    __syncthreads();
+    mx = red[0];
+    for (int i = 1; i < 8; ++i) mx = fmaxf(mx, red[i]);
+  }
   const int e = mx > 0.0f ? ilogbf(mx) - 14 : 0;  // max |x| 2^-e in [2^14, 2^15)
   bool inexact = false;
   auto pack = [&inexact](float a0, float a1) {
@@ -175,21 +190,22 @@ __global__ void __launch_bounds__(256)
   };
   if (-e >= -126 && -e <= 127) {
     const float f = __int_as_float((127 - e) << 23);
-    for (int64_t k = threadIdx.x; k < K8; k += blockDim.x) {
+#pragma unroll 4
+    for (int k = u; k < K8; k += kRow) {
       const uint4 v = xr[k];
       hr[k] = make_uint4(pack(lo(v.x) * f, hi(v.x) * f), pack(lo(v.y) * f, hi(v.y) * f),
                          pack(lo(v.z) * f, hi(v.z) * f), pack(lo(v.w) * f, hi(v.w) * f));
     }
   } else {
-    for (int64_t k = threadIdx.x; k < K8; k += blockDim.x) {
+    for (int k = u; k < K8; k += kRow) {
       const uint4 v = xr[k];
       auto sc = [&](float x) { return ldexpf(x, -e); };
       hr[k] = make_uint4(pack(sc(lo(v.x)), sc(hi(v.x))), pack(sc(lo(v.y)), sc(hi(v.y))),
                          pack(sc(lo(v.z)), sc(hi(v.z))), pack(sc(lo(v.w)), sc(hi(v.w))));
     }
   }
-  const int any = __syncthreads_or(inexact ? 1 : 0);
-  if (threadIdx.x == 0) {
+  const bool any = kRow == 256 ? __syncthreads_or(inexact ? 1 : 0) != 0 : __any_sync(0xffffffffu, inexact);
+  if (u == 0) {
     xexp[m] = e;
     xflag[m] = any ? 1 : 0;
   }
@@ -202,13 +218,14 @@ struct Tile {
   int split, kb0, nkb;
 };
 
-// Token tiles of `cnt` rows: as few as fit, all alike up to 16 rows.
+// Token tiles of `cnt` rows: as few as fit, all alike up to 16 rows (none is empty: all
+// but the last hold at most 256 rows each, and cnt is more than they can hold).
 __device__ __forceinline__ int tiles_for(int cnt) { return (cnt + kMaxTileM - 1) / kMaxTileM; }
 __device__ __forceinline__ int tile_rows(int cnt, int nt) { return ((cnt + nt - 1) / nt + 15) / 16 * 16; }
 
 // Tile `i` of the walk. Token tiles run fastest: the CTAs at work share weight tiles
 // (read from HBM once), and all activations stay in L2.
-__device__ __forceinline__ Tile tile_at(const Args& a, const int* pre, int ntn, int rank, int i) {
+__device__ __forceinline__ Tile tile_at(const Args& a, const int* pre, const int* off, int ntn, int rank, int i) {
   Tile t;
   const int nkb = static_cast<int>(a.K / kTileK);
   if (!a.offsets) {
@@ -227,12 +244,12 @@ __device__ __forceinline__ Tile tile_at(const Args& a, const int* pre, int ntn, 
     const int mid = (lo + hi) >> 1;
     if (pre[mid] <= i) lo = mid; else hi = mid;
   }
-  const int r0 = clamp_row(__ldg(a.offsets + lo), a.M), r1 = clamp_row(__ldg(a.offsets + lo + 1), a.M);
+  const int r0 = off[lo], r1 = off[lo + 1];
   const int nt = tiles_for(r1 - r0), rows = tile_rows(r1 - r0, nt), l = i - pre[lo];
   t.e = lo;
   t.n0 = (2 * (l / nt) + rank) * kTileN;
   t.m0 = r0 + (l % nt) * rows;
-  t.cnt = r1 - t.m0 < rows ? r1 - t.m0 : rows;  // (rounding up may leave the last tile empty: 0 or less)
+  t.cnt = r1 - t.m0 < rows ? r1 - t.m0 : rows;
   t.split = 0;
   t.kb0 = 0;
   t.nkb = nkb;
@@ -357,10 +374,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
   unsigned char* sp = smem_raw + (base - smem_u32(smem_raw));
   int* pre = reinterpret_cast<int*>(sp + kOffPre);
+  int* off = reinterpret_cast<int*>(sp + kOffFirst);
   const uint32_t bars = base + kOffBar;
   const uint32_t full = bars, empty = full + 8 * kStages, fullR = empty + 8 * kStages,
                  emptyR = fullR + 8 * kRawStages, accum = emptyR + 8 * kRawStages, dfree = accum + 8,
-                 tslot = dfree + 8;
+                 fullI = dfree + 8, emptyI = fullI + 8 * kInfos, tslot = emptyI + 8 * kInfos;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (tid == 0) {
     for (int s = 0; s < kStages; ++s) {
@@ -371,6 +389,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int s = 0; s < kRawStages; ++s) {
       mbar_init(fullR + 8 * s, 1);
       mbar_init(emptyR + 8 * s, kChunkBlocks * kDec / 32 / kStages);
+    }
+    for (int s = 0; s < kInfos; ++s) {
+      mbar_init(fullI + 8 * s, 1);
+      mbar_init(emptyI + 8 * s, kDec / 32);
     }
     mbar_init(accum, 1);
     mbar_init(dfree, 2 * kDec / 32);
@@ -388,7 +410,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int e = e0 + lane;
         int c = 0;
         if (e < a.E) {
-          const int rows = clamp_row(__ldg(a.offsets + e + 1), a.M) - clamp_row(__ldg(a.offsets + e), a.M);
+          const int r0 = clamp_row(__ldg(a.offsets + e), a.M), r1 = clamp_row(__ldg(a.offsets + e + 1), a.M);
+          const int rows = r1 - r0;
+          off[e] = r0;
+          if (e == a.E - 1) off[a.E] = r1;
           c = rows > 0 ? tiles_for(rows) * ntn : 0;
         }
         int inc = c;
@@ -421,8 +446,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint32_t blk = 0;  // stages filled
       bool ok = true;
       for (int i = first; i < total && ok; i += step) {
-        const Tile t = tile_at(a, pre, ntn, rank, i);
-        if (t.cnt <= 0) continue;
+        const Tile t = tile_at(a, pre, off, ntn, rank, i);
         const int half = mma_n(t.cnt) / 2, box = (half + kBoxStep - 1) / kBoxStep;
         const CUtensorMap* map = &tm_x.m[box - 1];
         for (int kb = 0; kb < (t.nkb + 1) / 2 * 2; ++kb, ++blk) {
@@ -453,8 +477,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint32_t blk = 0, nt = 0;
       bool ok = true;
       for (int i = first; i < total && ok; i += step) {
-        const Tile t = tile_at(a, pre, ntn, rank, i);
-        if (t.cnt <= 0) continue;
+        const Tile t = tile_at(a, pre, off, ntn, rank, i);
         const int n = mma_n(t.cnt), nacc = accs_for(n);
         const uint32_t idesc = idesc_f16_m256(n);
         const uint32_t half_k = static_cast<uint32_t>((n / 2 + kBoxStep - 1) / kBoxStep) * (kBoxStep * 128 >> 4);
@@ -494,8 +517,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint32_t c = 0;
       bool ok = true;
       for (int i = first; i < total && ok; i += step) {
-        const Tile t = tile_at(a, pre, ntn, rank, i);
-        if (t.cnt <= 0) continue;
+        const Tile t = tile_at(a, pre, off, ntn, rank, i);
         const int g0 = t.e * a.groups + t.n0 / 4;
         for (int kb = t.kb0; kb < t.kb0 + t.nkb; kb += kChunkBlocks) {
           const uint32_t r = c % kRawStages;
@@ -512,6 +534,41 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (uint32_t q = c > kRawStages ? c - kRawStages : 0; q < c; ++q)
         mbar_wait(fullR + 8 * (q % kRawStages), (q / kRawStages) & 1, a.fault, kFaultW, false);
     }
+  } else if (warp == 3) {
+    // ---------------- the tiles' tokens' exponents and flags, ahead of the epilogues
+    uint32_t k = 0;
+    for (int i = first; i < total; i += step, ++k) {
+      const Tile t = tile_at(a, pre, off, ntn, rank, i);
+      const uint32_t s = k % kInfos;
+      int* xe = reinterpret_cast<int*>(sp + kOffInfo + s * kInfoBytes);
+      int e[kMaxTileM / 32], f[kMaxTileM / 32];
+#pragma unroll
+      for (int x = 0; x < kMaxTileM / 32; ++x) {
+        const int m = 32 * x + lane;
+        e[x] = m < t.cnt ? __ldg(a.xexp + t.m0 + m) : 0;
+        f[x] = m < t.cnt ? __ldg(a.xflag + t.m0 + m) : 0;
+      }
+      bool ok = mbar_wait(emptyI + 8 * s, ((k / kInfos) & 1) ^ 1, a.fault, kFaultEpilogue);
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) break;
+      // special: some token is flagged, or the two powers of two of an output cannot be
+      // multiplied into one normal float
+      bool special = false;
+#pragma unroll
+      for (int x = 0; x < kMaxTileM / 32; ++x) {
+        const int m = 32 * x + lane;
+        xe[m] = e[x];
+        xe[kMaxTileM + m] = f[x];
+        xe[2 * kMaxTileM + m] = (e[x] + 127) << 23;
+        special = special || f[x] != 0 || e[x] < -85 || e[x] > 115;
+      }
+      special = __any_sync(0xffffffffu, special);
+      if (lane == 0) {
+        xe[3 * kMaxTileM] = special;
+        mbar_arrive(fullI + 8 * s);
+      }
+      __syncwarp();
+    }
   } else if (warp >= 4) {
     // ---------------- decode: weight stage g belongs to warp group g (four warps, one
     // thread a weight row), which decodes every fourth block into it. The groups' chains
@@ -519,9 +576,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     // warps on every block the chain's latency bounded the rate (0.88 us a block, 128 x 64)
     const int d = tid - 128, row = d & (kTileN - 1), grp = d >> 7;
     const int q = warp & 3;  // row = 32 q + lane
-    int* xe = reinterpret_cast<int*>(sp + kOffXe);
-    int* xf = xe + kMaxTileM;
-    float* xs = reinterpret_cast<float*>(xf + kMaxTileM);
     float* red = reinterpret_cast<float*>(sp + kOffRed);
     const uint32_t lane_base = tmem + (static_cast<uint32_t>(32 * q) << 16);
     const uint32_t tA = lane_base + kTmemA + 64u * grp;
@@ -530,28 +584,20 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t myscale = base + kOffScale + static_cast<uint32_t>(row >> 2) * (kChunkBlocks * kScales * 8) +
                              2u * (row & 3) + 8u * kScales * (grp & 1);
     bool ok = true;
-    uint32_t done_tiles = 0;       // epilogues finished
-    int pend = first;              // the tile whose epilogue is next
-    int64_t pend_last = -1;        // its last block
+    uint32_t done_tiles = 0;  // epilogues finished
 
-    auto epilogue = [&](int i) {
-      const Tile t = tile_at(a, pre, ntn, rank, i);
+    auto epilogue = [&](const Tile& t) {
       const int n = mma_n(t.cnt), nacc = accs_for(n);
       const int nr = t.n0 + 32 * q + lane;
-      // the tokens' exponents; special: some token is flagged, or the two powers of two
-      // cannot be multiplied into one normal float
-      bool special = false;
-      for (int m = d; m < kMaxTileM; m += kDec) {
-        const bool in = m < t.cnt;
-        const int e = in ? __ldg(a.xexp + t.m0 + m) : 0;
-        xe[m] = e;
-        xs[m] = __int_as_float((e + 127) << 23);
-        xf[m] = in ? __ldg(a.xflag + t.m0 + m) : 0;
-        special = special || xf[m] != 0 || e < -85 || e > 115;
-      }
       const int we = nr < a.N ? __ldg(a.wexp + static_cast<int64_t>(t.e) * a.groups * 4 + nr) : 0;
       const float ws = __int_as_float((127 + we) << 23);  // 2^we (we is in -30 .. 4)
-      special = named_bar_or(3, kDec, special);
+      const uint32_t si = done_tiles % kInfos;
+      const int* xe = reinterpret_cast<const int*>(sp + kOffInfo + si * kInfoBytes);
+      const int* xf = xe + kMaxTileM;
+      const float* xs = reinterpret_cast<const float*>(xf + kMaxTileM);
+      if (ok) ok = mbar_wait(fullI + 8 * si, (done_tiles / kInfos) & 1, a.fault, kFaultEpilogue);
+      // (one answer for all: the recomputation below has barriers)
+      const bool special = named_bar_or(3, kDec, ok && xe[3 * kMaxTileM] != 0);
       if (ok) ok = mbar_wait(accum, done_tiles & 1, a.fault, kFaultEpilogue);
       __syncwarp();
       tc_fence_after_sync();
@@ -628,29 +674,40 @@ __global__ void __launch_bounds__(kThreads, 1)
             else a.Y[o] = f32_to_bf16_bits(y);
           });
       }
-      named_bar_sync(3, kDec);  // the shared arrays are free again
+      __syncwarp();
+      if (lane == 0) mbar_arrive(emptyI + 8 * si);
       ++done_tiles;
     };
-    // the next tile of this CTA from i on that has rows
-    auto skip_empty = [&](int i) {
-      while (i < total && tile_at(a, pre, ntn, rank, i).cnt <= 0) i += step;
-      return i;
+    int pend = first;  // the tile whose epilogue is next, and its last block
+    Tile pt = {};
+    int64_t pend_last = -1;
+    auto next_pend = [&]() {
+      if (pend >= total) return;
+      pt = tile_at(a, pre, off, ntn, rank, pend);
+      pend_last += (pt.nkb + 1) / 2 * 2;
     };
-    pend = skip_empty(first);
-    if (pend < total) pend_last = (tile_at(a, pre, ntn, rank, pend).nkb + 1) / 2 * 2 - 1;
+    auto weight_exp = [&](const Tile& t) {
+      return t.n0 + row < a.N ? __ldg(a.wexp + static_cast<int64_t>(t.e) * a.groups * 4 + t.n0 + row) : 0;
+    };
+    next_pend();
     int64_t blk0 = 0;     // blocks and chunks of the tiles before
     uint32_t chunk0 = 0;
-    for (int i = pend; i < total; i = skip_empty(i + step)) {
-      const Tile t = tile_at(a, pre, ntn, rank, i);
-      const int nr = t.n0 + row;
-      const int we = nr < a.N ? __ldg(a.wexp + static_cast<int64_t>(t.e) * a.groups * 4 + nr) : 0;
+    Tile t = pt;
+    int we_next = pend < total ? weight_exp(t) : 0;
+    for (int i = first; i < total; i += step) {
+      const int we = we_next;
+      const int nkb = t.nkb;
+      if (i + step < total) {  // the next tile and its row's exponent, before this one's blocks
+        t = tile_at(a, pre, off, ntn, rank, i + step);
+        we_next = weight_exp(t);
+      }
       // 2^-we as two fp16 factors (we is in -30 .. 4)
       const int we1 = we < -15 ? -15 : we;
       const __half2 f1 = __half2half2(__ushort_as_half(static_cast<uint16_t>((15 - we1) << 10)));
       const __half2 f2 = __half2half2(__ushort_as_half(static_cast<uint16_t>((15 - (we - we1)) << 10)));
       // the tile's blocks are dealt to the groups two by two: chunk c (two blocks) to the
       // groups 0 and 1 or 2 and 3
-      const uint32_t nch = static_cast<uint32_t>(t.nkb + kChunkBlocks - 1) / kChunkBlocks;
+      const uint32_t nch = static_cast<uint32_t>(nkb + kChunkBlocks - 1) / kChunkBlocks;
       for (uint32_t c = ((chunk0 & 1) ^ static_cast<uint32_t>(grp >> 1)); c < nch; c += 2) {
         const uint32_t r = (chunk0 + c) % kRawStages;
         if (ok) ok = mbar_wait(fullR + 8 * r, ((chunk0 + c) / kRawStages) & 1, a.fault, kFaultDecode);
@@ -687,15 +744,19 @@ __global__ void __launch_bounds__(kThreads, 1)
         // blocks of that tile or earlier ones: no circle of waits.)
         const int64_t b = blk0 + 2 * static_cast<int64_t>(c) + (grp & 1);
         while (pend < total && pend_last < b) {
-          epilogue(pend);
-          pend = skip_empty(pend + step);
-          if (pend < total) pend_last += (tile_at(a, pre, ntn, rank, pend).nkb + 1) / 2 * 2;
+          epilogue(pt);
+          pend += step;
+          next_pend();
         }
       }
       blk0 += 2 * static_cast<int64_t>(nch);
       chunk0 += nch;
     }
-    for (; pend < total; pend = skip_empty(pend + step)) epilogue(pend);
+    while (pend < total) {
+      epilogue(pt);
+      pend += step;
+      next_pend();
+    }
   }
 
   tc_fence_before_sync();
@@ -844,14 +905,15 @@ cudaError_t launch(const lbq_weights* w, const Plan& plan, const lbq_expert_rows
            (kChunkBlocks * kTileK / kG) * 4, kTileN / 4, CU_TENSOR_MAP_SWIZZLE_NONE))
     return cudaErrorInvalidValue;
 
-  Args prep = a;
-  prep.kb_split = kG;  // weights a scale
-  const int64_t wblocks = (static_cast<int64_t>(E) * ng + 7) / 8;
-  q4_prepare_kernel<<<static_cast<unsigned>(rows + wblocks), 256, 0, s>>>(prep, Xh, xexp, xflag, wexp,
-                                                                          static_cast<int>(E * ng));
+  a.kb_split = plan.kb_split;
+  const unsigned wblocks = static_cast<unsigned>((static_cast<int64_t>(E) * ng + 7) / 8);
+  const int ngroups = static_cast<int>(E * ng);
+  if (rows >= 8 * sm_count())  // enough rows for every SM at eight a block
+    q4_prepare_kernel<32><<<static_cast<unsigned>((rows + 7) / 8) + wblocks, 256, 0, s>>>(a, Xh, xexp, xflag, wexp, ngroups, kG);
+  else
+    q4_prepare_kernel<256><<<static_cast<unsigned>(rows) + wblocks, 256, 0, s>>>(a, Xh, xexp, xflag, wexp, ngroups, kG);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  a.kb_split = plan.kb_split;
   const int64_t ntn = (w->N + 2 * kTileN - 1) / (2 * kTileN), pairs = sm_count() / 2;
   // experts: at most rows / 256 + E token tiles
   const int64_t most = er ? (rows / kMaxTileM + E) * ntn : static_cast<int64_t>(plan.ntm) * ntn * plan.splits;
