@@ -67,7 +67,7 @@ lbq_status check_operands(const lbq_weights* w, const void* x, int64_t M, const 
     if (!D) return LBQ_ERR_ARG;
     if (!aligned(D, 16)) return LBQ_ERR_ALIGN;
   }
-  if (M == 1 && lbq_gemv_workspace(w) && w->N > lbq::kMaxSplitRows) return LBQ_ERR_SHAPE;
+  if (M == 1 && !lbq::is_q4(w->fmt) && lbq_gemv_workspace(w) && w->N > lbq::kMaxSplitRows) return LBQ_ERR_SHAPE;
   return LBQ_OK;
 }
 
@@ -350,7 +350,7 @@ lbq_status lbq_gemm(const lbq_weights* w, const uint16_t* X, int64_t M, const in
   lbq_status st = check_product(w, X, M, D, Y, workspace, workspace_bytes, &L);
   if (st != LBQ_OK) return st;
   if (per_token(w, M)) {
-    if (lbq_gemv_workspace(w) && w->N > lbq::kMaxSplitRows) return LBQ_ERR_SHAPE;
+    if (!lbq::is_q4(w->fmt) && lbq_gemv_workspace(w) && w->N > lbq::kMaxSplitRows) return LBQ_ERR_SHAPE;
     // one batch-1 product per token, in stream order (they share the workspace)
     for (int64_t m = 0; m < M; ++m) {
       const cudaError_t e =
@@ -416,7 +416,7 @@ lbq_status lbq_expert_combine_grad(const uint16_t* dout, const uint16_t* Y, int6
 size_t lbq_expert_workspace_bytes(const lbq_weights* w, int32_t E, int64_t R) {
   Layout L;
   if (check_expert_weights(w, E, &L) != LBQ_OK || R < 1 || R > kMaxSlots) return 0;
-  return expert_few(E, R) ? 0 : lbq_q4_expert_tc_workspace(w, E, R);
+  return expert_few(E, R) ? lbq_q4_few_workspace(8) : lbq_q4_expert_tc_workspace(w, E, R);
 }
 
 lbq_status lbq_expert_gemm(const lbq_weights* w, int32_t E, const uint16_t* X, int64_t T,
@@ -436,7 +436,7 @@ lbq_status lbq_expert_gemm(const lbq_weights* w, int32_t E, const uint16_t* X, i
     if (!aligned(workspace, 16)) return LBQ_ERR_ALIGN;
   }
   const lbq_expert_rows rows = {X, offsets, slots, Y, T, R, topk, E};
-  return from_cuda(expert_few(E, R) ? lbq_launch_q4_expert_few(w, rows, as_stream(stream))
+  return from_cuda(expert_few(E, R) ? lbq_launch_q4_expert_few(w, rows, workspace, as_stream(stream))
                                     : lbq_launch_q4_expert_tc(w, rows, workspace, as_stream(stream)));
 }
 

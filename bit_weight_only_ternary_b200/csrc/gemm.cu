@@ -101,7 +101,7 @@ __global__ void __launch_bounds__(256) gemm_rowwarp(const uint8_t* __restrict__ 
 
 size_t lbq_gemm_workspace(const lbq_weights* w, int64_t M) {
   if (w->fmt == LBQ_TERN5) return lbq_gemm_tc_workspace(w, M);
-  if (is_q4(w->fmt)) return M <= kQ4FewTokens ? 0 : lbq_q4_tc_workspace(w, M);
+  if (is_q4(w->fmt)) return M <= kQ4FewTokens ? lbq_q4_few_workspace(M) : lbq_q4_tc_workspace(w, M);
   return w->fmt == LBQ_Q2RHT
              ? kWsCounterBytes + static_cast<size_t>(w->K) * static_cast<size_t>(M) * sizeof(float)
              : 0;
@@ -117,7 +117,7 @@ cudaError_t lbq_launch_gemm(const lbq_weights* w, const uint16_t* X, int64_t M, 
   switch (w->fmt) {
     case LBQ_Q4G32:
     case LBQ_Q4G128:
-      return M <= kQ4FewTokens ? lbq_launch_q4_few(w, X, M, Y, s) : lbq_launch_q4_tc(w, X, M, Y, ws, s);
+      return M <= kQ4FewTokens ? lbq_launch_q4_few(w, X, M, Y, ws, s) : lbq_launch_q4_tc(w, X, M, Y, ws, s);
     case LBQ_TERN5:  // tensor-core path (gemm_tc.cu)
       return lbq_launch_gemm_tc(w, X, M, Y, ws, s);
     case LBQ_SIGN1:

@@ -517,7 +517,7 @@ unsigned* lbq_fault_word() {
 }
 
 size_t lbq_gemv_workspace(const lbq_weights* w) {
-  if (is_q4(w->fmt)) return 0;
+  if (is_q4(w->fmt)) return lbq_q4_few_workspace(1);
   const int KS = slices_of(w);
   if (KS <= 1) return 0;
   return kWsCounterBytes + static_cast<size_t>(KS) * static_cast<size_t>(w->N) * sizeof(float);
@@ -531,7 +531,7 @@ cudaError_t lbq_launch_gemv(const lbq_weights* w, const uint16_t* x, const int8_
     case LBQ_Q4G32:
     case LBQ_Q4G128: {
       const lbq_product p = {*w, x, nullptr, y};
-      return lbq_launch_q4_list(&p, 1, y32, s);
+      return lbq_launch_q4_list(&p, 1, y32, ws, s);
     }
     default: return launch<LBQ_Q2RHT>(w, x, D, y, y32, ws, s);
   }

@@ -645,7 +645,7 @@ int64_t lbq_gemv_batch_plan_list(const lbq_product* ps, int32_t n, int ctas, int
 
 // [64 KB kept zero (the counter rule of every workspace)][piece sums]
 size_t lbq_gemv_batch_ws(const lbq_product* ps, int32_t n) {
-  if (is_q4(ps[0].w.fmt)) return kWsCounterBytes;  // whole rows per CTA: no piece sums
+  if (is_q4(ps[0].w.fmt)) return lbq_q4_few_workspace(1);
   const Plan pl = plan_list(ps, n, sm_count(), nullptr);
   return kWsCounterBytes + pl.partial_floats * sizeof(float);
 }
@@ -708,7 +708,7 @@ cudaError_t lbq_launch_gemv_batch(const lbq_product* ps, int32_t n, void* ws, cu
     case LBQ_SIGN1: return launch_list<LBQ_SIGN1>(ps, n, ws, s);
     case LBQ_Q2RHT: return launch_list<LBQ_Q2RHT>(ps, n, ws, s);
     case LBQ_Q4G32:
-    case LBQ_Q4G128: return lbq_launch_q4_list(ps, n, nullptr, s);
+    case LBQ_Q4G128: return lbq_launch_q4_list(ps, n, nullptr, ws, s);
     default: return cudaErrorInvalidValue;
   }
 }

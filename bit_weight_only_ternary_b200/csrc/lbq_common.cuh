@@ -191,8 +191,10 @@ cudaError_t lbq_launch_gemm(const lbq_weights* w, const uint16_t* X, int64_t M, 
                             uint16_t* Y, void* ws, cudaStream_t s);
 // The 4-bit products (q4_gemv.cu): a list of batch-1 products (y32: fp32 outputs, only
 // for a list of one), and one matrix times a few tokens.
-cudaError_t lbq_launch_q4_list(const lbq_product* ps, int32_t n, float* y32, cudaStream_t s);
-cudaError_t lbq_launch_q4_few(const lbq_weights* w, const uint16_t* X, int64_t M, uint16_t* Y,
+// All share one workspace (counters zero before and after, then scratch).
+size_t lbq_q4_few_workspace(int64_t M);
+cudaError_t lbq_launch_q4_list(const lbq_product* ps, int32_t n, float* y32, void* ws, cudaStream_t s);
+cudaError_t lbq_launch_q4_few(const lbq_weights* w, const uint16_t* X, int64_t M, uint16_t* Y, void* ws,
                               cudaStream_t s);
 // Rows of sorted order by their experts' matrices: row r in [offsets[e], offsets[e + 1])
 // reads X row slots[r] / topk (r itself when slots is null).
@@ -210,7 +212,7 @@ cudaError_t lbq_launch_q4_tc(const lbq_weights* w, const uint16_t* X, int64_t M,
                              cudaStream_t s);
 size_t lbq_q4_expert_tc_workspace(const lbq_weights* w, int32_t E, int64_t R);
 cudaError_t lbq_launch_q4_expert_tc(const lbq_weights* w, const lbq_expert_rows& r, void* ws, cudaStream_t s);
-cudaError_t lbq_launch_q4_expert_few(const lbq_weights* w, const lbq_expert_rows& r, cudaStream_t s);
+cudaError_t lbq_launch_q4_expert_few(const lbq_weights* w, const lbq_expert_rows& r, void* ws, cudaStream_t s);
 // Slots sorted by expert and the rows' way there and back (expert.cu).
 cudaError_t lbq_launch_expert_sort(const void* ids, int id_bytes, int64_t R, int32_t E,
                                    int32_t* offsets, int32_t* rows, int32_t* slots, cudaStream_t s);

@@ -1,20 +1,30 @@
-// q4_gemv.cu -- 4-bit products for few tokens: y[m][n] = sum_k s[n][k/g] (q[n][k] - 8) x[m][k].
+// q4_gemv.cu -- 4-bit products of few tokens: y[m][n] = sum_k s[n][k/g] (q[n][k] - 8) x[m][k],
+// for a list of products (one token), one matrix and a few tokens, or a matrix per expert. Bound: the bytes of the packed weights, with the decoding close behind.
 //
-// One CTA computes 32 weight rows (eight groups of four) over all of K for up to eight
-// tokens; its eight warps take the 128-weight chunks of K in turn and their fp32 sums are
-// added in warp order, so the result does not depend on timing. Bound: the bytes of the
-// packed weights.
+// Work. A tile is 32 weight rows (eight groups of four) x up to 8 tokens over all of K;
+// its chunks are 128 of K (2 KB of codes). All tiles' chunks lie in one line, cut into
+// equal runs, one a warp: however many rows a product has, every SM streams until the end,
+// and a warp adds up its stretch of K alone. It streams through two slots of shared memory
+// of its own that asynchronous copies fill ahead, across tiles. A tile that lies in one
+// warp's run is stored by the warp; the parts of a tile that several warps share are
+// joined in K order, once, when the CTA's runs are done; where the CTA's runs end inside a
+// tile, its part goes to the workspace and the last of the tile's CTAs to get there adds
+// the parts in K order. Every order of sums is fixed, so results do not depend on timing.
+// (A CTA a tile, its warps taking chunks in turn and two chunks ahead in registers, took
+// 50 us for a 27B layer; the warps of a persistent CTA joined at every tile 47 us.)
 //
-// A 16-byte load brings one 32-bit word (eight neighbouring weights) of four rows. Lane
-// (g, t) = (lane / 4, lane % 4) reads word 4 s + t of row group g, which is, up to the
-// order of rows and of K, the weight operand of m16n8k16 matrix instructions: rows 4g and
-// 4g+1 are rows g and g+8 of a first tile, 4g+2 and 4g+3 of a second, and a word's eight
-// weights are the lane's K values of two instructions. The activations need only the same
-// order of K: lane (g, t) reads the eight activations of its word for token g with one
-// 16-byte load. A code becomes a bf16 integer without a conversion: 0x4300 | q is 128 + q,
-// minus 136 is q - 8, both exact. Products of these integers with bf16 activations are
-// exact in fp32, sums are fp32, and the group's scale multiplies the group's sum in fp32:
-// nothing is rounded to fewer bits before the final bf16 (or fp32) store.
+// Arithmetic. A 16-byte load brings one 32-bit word (eight neighbouring weights) of four
+// rows. Lane (g, t) = (lane / 4, lane % 4) reads word 4 s + t of row group g, which is, up
+// to the order of rows and of K, the weight operand of m16n8k16 matrix instructions: rows
+// 4g and 4g+1 are rows g and g+8 of a first tile, 4g+2 and 4g+3 of a second, and a word's
+// eight weights are the lane's K values of two instructions. The activations need only
+// the same order of K: lane (g, t) reads the eight activations of its word for token g. A
+// code becomes a bf16 integer without a conversion: 0x4300 | q is 128 + q, minus 136 is
+// q - 8, both exact. Products of these integers with bf16 activations are exact in fp32,
+// sums are fp32, and the group's scale multiplies the group's sum in fp32: nothing is
+// rounded to fewer bits before the final bf16 (or fp32) store. (Summing 128 + q and
+// taking 136 sum x off at the end would save the subtractions, but an activation on a
+// zero weight would then leave its rounding error behind.)
 #include <algorithm>
 
 #include "lbq_common.cuh"
@@ -27,300 +37,563 @@ using namespace lbq;
 constexpr int kWarps = 8;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kRowTile = 32;
-constexpr int kMaxTokens = 8;  // columns of one matrix instruction
+// CTAs an SM: what the slots leave room for.
+constexpr int ctas_per_sm(int tok) { return tok == 8 ? 2 : 3; }
+
+// Asynchronous copies global -> shared of this thread's own bytes (L1 is bypassed for 16).
+__device__ __forceinline__ void cp16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp8(uint32_t dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int kLeft>
+__device__ __forceinline__ void cp_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(kLeft) : "memory");
+}
+__device__ __forceinline__ uint4 lds128(uint32_t a) {
+  uint4 v;
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));
+  return v;
+}
+__device__ __forceinline__ uint2 lds64(uint32_t a) {
+  uint2 v;
+  asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a));
+  return v;
+}
+
+// Pair j of a word's codes (weights 2j, 2j+1) as two bf16 integers q - 8.
+__device__ __forceinline__ uint32_t q4_pair(uint32_t w, int j) {
+  uint32_t v, r;
+  // ((w >> 4 j) & 0x000f000f) | 0x43004300, 128 + q twice, as one three-input operation
+  // (left to the compiler it became two, with an immediate each)
+  asm("lop3.b32 %0, %1, %2, %3, 0xea;" : "=r"(v) : "r"(w >> (4 * j)), "r"(0x000f000fu), "r"(0x43004300u));
+  asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(v), "r"(0x43084308u));  // - 136
+  return r;
+}
+
+__device__ __forceinline__ void mma_bf16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+      "{%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+// d = a b: the first instruction of a group's sum.
+__device__ __forceinline__ void mma_bf16_first(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+      "{%8, %9}, {%10, %10, %10, %10};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.0f));
+}
+
+// ---------------------------------------------------------------- where the tiles are
+// A source gives the tiles of its products (or experts): tiles and chunks of product p,
+// the lane's pointers into tile i, and where its outputs go.
+struct LanePtr {
+  const uint8_t* w;        // the lane's word of its row group, chunk 0
+  const uint16_t* s;       // its row group's scales
+  const uint16_t* x;       // its token's activations + 8 t; null: no token, or (zero) zeros
+  bool zero;
+};
 
 struct Q4Prod {
   const uint8_t* codes;
   const uint16_t* scales;
   const uint16_t* x;   // [M][K]
   void* y;             // bf16 (or fp32) [M][N]
+  int64_t q0;          // chunks of the products before
   int64_t gcode;       // code bytes per group of four rows
   int32_t gscale;      // scales per group of four rows
-  int32_t N, nc;       // rows; 128-weight chunks of K
-  int32_t tile0;       // first CTA of this product
+  int32_t N, nc;       // rows; chunks of a tile
 };
 
 template <int kCap>
 struct Q4List {
+  int64_t chunks;
+  float* part;         // workspace: parts of tiles cut by a run's end
+  unsigned* count;     // arrivals on such a tile (zero before and after)
   int32_t n, M;
   Q4Prod p[kCap];
 };
 
-// 16 bytes of packed weights: streamed, not kept in L1.
-__device__ __forceinline__ uint4 ldg_w(const void* p) {
-  uint4 v;
-  asm volatile("ld.global.nc.L1::no_allocate.v4.b32 {%0, %1, %2, %3}, [%4];"
-               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-               : "l"(p));
-  return v;
-}
-// Activations: plain loads (they may have been written just before this kernel).
-__device__ __forceinline__ uint4 ldg_x(const void* p) {
-  uint4 v;
-  asm volatile("ld.global.v4.b32 {%0, %1, %2, %3}, [%4];"
-               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-               : "l"(p));
-  return v;
-}
-
-// Pair j of a word's codes (weights 2j, 2j+1) as two bf16 integers q - 8.
-__device__ __forceinline__ uint32_t q4_pair(uint32_t w, int j) {
-  const uint32_t v = ((w >> (4 * j)) & 0x000f000fu) | 0x43004300u;  // 128 + q
-  uint32_t r;
-  asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(v), "r"(0x43084308u));  // - 136
-  return r;
-}
-
-__device__ __forceinline__ void mma_bf16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
-                                         uint32_t a3, uint32_t b0, uint32_t b1) {
-  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
-      "{%8, %9}, {%0, %1, %2, %3};"
-      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
-
-// One chunk of K in flight: 4 x 16 bytes of codes, the scales and the activations.
-template <int kG>
-struct Chunk {
-  uint4 w[4];
-  uint2 s[kG == 32 ? 4 : 1];  // fp16 of rows 4g .. 4g+3 per group of K
-  uint4 x[4];
-};
-
-// acc[tile][..] += this warp's chunks of the 32-row tile; xrow: this lane's token's
-// activations (null: zeros).
-template <int kG>
-__device__ __forceinline__ void warp_sum_tile(const uint8_t* codes, const uint16_t* scales, int nc,
-                                              const uint16_t* xrow, int warp, int lane,
-                                              float (&acc)[2][4]) {
-  const int t = lane & 3;
-  const uint8_t* wp = codes + 16 * t;
-  Chunk<kG> buf[2];
-  auto load = [&](Chunk<kG>& b, int c) {
-    if (c >= nc) return;
-#pragma unroll
-    for (int s = 0; s < 4; ++s) b.w[s] = ldg_w(wp + static_cast<int64_t>(c) * 256 + 64 * s);
-    constexpr int kS = kG == 32 ? 4 : 1;
-#pragma unroll
-    for (int s = 0; s < kS; ++s)
-      b.s[s] = __ldg(reinterpret_cast<const uint2*>(scales + 4 * (static_cast<int64_t>(c) * kS + s)));
-#pragma unroll
-    for (int s = 0; s < 4; ++s)
-      b.x[s] = xrow ? ldg_x(xrow + static_cast<int64_t>(c) * kQ4Chunk + 32 * s + 8 * t) : make_uint4(0, 0, 0, 0);
-  };
-  auto use = [&](const Chunk<kG>& b) {
-    float part[2][4];
-#pragma unroll
-    for (int s = 0; s < 4; ++s) {
-      if (kG == 32 || s == 0) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) part[i >> 2][i & 3] = 0.0f;
-      }
-      const uint4 w = b.w[s], x = b.x[s];
-      mma_bf16(part[0], q4_pair(w.x, 0), q4_pair(w.y, 0), q4_pair(w.x, 1), q4_pair(w.y, 1), x.x, x.y);
-      mma_bf16(part[1], q4_pair(w.z, 0), q4_pair(w.w, 0), q4_pair(w.z, 1), q4_pair(w.w, 1), x.x, x.y);
-      mma_bf16(part[0], q4_pair(w.x, 2), q4_pair(w.y, 2), q4_pair(w.x, 3), q4_pair(w.y, 3), x.z, x.w);
-      mma_bf16(part[1], q4_pair(w.z, 2), q4_pair(w.w, 2), q4_pair(w.z, 3), q4_pair(w.w, 3), x.z, x.w);
-      if (kG == 32 || s == 3) {
-        const uint2 sc = b.s[kG == 32 ? s : 0];
-        const float2 s01 = __half22float2(*reinterpret_cast<const __half2*>(&sc.x));
-        const float2 s23 = __half22float2(*reinterpret_cast<const __half2*>(&sc.y));
-        acc[0][0] += s01.x * part[0][0];
-        acc[0][1] += s01.x * part[0][1];
-        acc[0][2] += s01.y * part[0][2];
-        acc[0][3] += s01.y * part[0][3];
-        acc[1][0] += s23.x * part[1][0];
-        acc[1][1] += s23.x * part[1][1];
-        acc[1][2] += s23.y * part[1][2];
-        acc[1][3] += s23.y * part[1][3];
+template <int kCap, int kTok, bool kF32>
+struct ListSource {
+  static constexpr bool kZeros = false;
+  const Q4List<kCap>& a;
+  __device__ __forceinline__ int64_t chunks() const { return a.chunks; }
+  __device__ __forceinline__ int64_t start(int p) const { return a.p[p].q0; }
+  __device__ __forceinline__ int nc(int p) const { return a.p[p].nc; }
+  __device__ __forceinline__ int ntok() const { return kTok == 1 ? 1 : (a.M + kTok - 1) / kTok; }
+  __device__ __forceinline__ int tiles(int p) const { return (a.p[p].N + kRowTile - 1) / kRowTile * ntok(); }
+  __device__ __forceinline__ int next(int p) const { return p + 1; }
+  __device__ __forceinline__ int find(int64_t q) const {
+    int lo = 0;
+    if (kCap > 1) {
+      int hi = a.n;
+      while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (a.p[mid].q0 <= q) lo = mid; else hi = mid;
       }
     }
-  };
-  load(buf[0], warp);
-  load(buf[1], warp + kWarps);
-  for (int c = warp; c < nc; c += 2 * kWarps) {
-    use(buf[0]);
-    load(buf[0], c + 2 * kWarps);
-    if (c + kWarps >= nc) break;
-    use(buf[1]);
-    load(buf[1], c + 3 * kWarps);
+    return lo;
   }
-}
-
-// The warps' sums added in warp order; put(token, row in tile, value).
-template <typename Put>
-__device__ __forceinline__ void join_warps(float (*red)[kRowTile * kMaxTokens], const float (&acc)[2][4],
-                                           int warp, int lane, Put put) {
-  const int g = lane >> 2, t = lane & 3;
-#pragma unroll
-  for (int i = 0; i < 2; ++i)
-#pragma unroll
-    for (int h = 0; h < 2; ++h)
-#pragma unroll
-      for (int c = 0; c < 2; ++c)  // token 2t + c, row 4g + 2i + h
-        red[warp][(2 * t + c) * kRowTile + 4 * g + 2 * i + h] = acc[i][2 * h + c];
-  __syncthreads();
-  const int o = threadIdx.x;
-  float v = red[0][o];
-#pragma unroll
-  for (int w = 1; w < kWarps; ++w) v += red[w][o];
-  put(o / kRowTile, o % kRowTile, v);
-}
-
-template <int kG, int kCap, bool kF32>
-__global__ void __launch_bounds__(kThreads, 2)
-    q4_list_kernel(const __grid_constant__ Q4List<kCap> a) {
-  __shared__ float red[kWarps][kRowTile * kMaxTokens];
-  const int tile = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2;
-  int lo = 0;
-  if (kCap > 1) {  // the last product whose first tile is at most this one
-    int hi = a.n;
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      if (a.p[mid].tile0 <= tile) lo = mid; else hi = mid;
-    }
+  __device__ __forceinline__ void point(int p, int i, int lane, LanePtr& l) const {
+    const Q4Prod& P = a.p[p];
+    const int g = lane >> 2, t = lane & 3, ng = (P.N + 3) >> 2;
+    const int rt = kTok == 1 ? i : i / ntok(), m = (i - rt * ntok()) * kTok + g;  // token tiles run fastest
+    int64_t grp = rt * (kRowTile / 4) + g;
+    if (grp >= ng) grp = ng - 1;  // rows behind the last: read it again, store nothing
+    l.w = P.codes + grp * P.gcode + 16 * t;
+    l.s = P.scales + grp * P.gscale;
+    const int64_t K = static_cast<int64_t>(P.nc) * kQ4Chunk;
+    l.x = g < kTok && m < a.M ? P.x + m * K + 8 * t : nullptr;
+    l.zero = false;
   }
-  const Q4Prod& P = a.p[lo];
-  pdl_launch_dependents();
-  const int row0 = (tile - P.tile0) * kRowTile;
-  const int ng = (P.N + 3) >> 2;
-  int64_t grp = (row0 >> 2) + g;
-  if (grp >= ng) grp = ng - 1;  // rows behind the last: read it again, store nothing
-  const int m0 = blockIdx.y * kMaxTokens, K = P.nc * kQ4Chunk;
-  pdl_wait();
-  float acc[2][4] = {};
-  const uint16_t* xrow = m0 + g < a.M ? P.x + static_cast<int64_t>(m0 + g) * K : nullptr;
-  warp_sum_tile<kG>(P.codes + grp * P.gcode, P.scales + grp * P.gscale, P.nc, xrow, warp, lane, acc);
-  join_warps(red, acc, warp, lane, [&](int m, int r, float v) {
-    if (m0 + m >= a.M || row0 + r >= P.N) return;
-    const int64_t o = static_cast<int64_t>(m0 + m) * P.N + row0 + r;
+  __device__ __forceinline__ void store(int p, int i, int m, int r, float v) const {
+    const Q4Prod& P = a.p[p];
+    const int rt = kTok == 1 ? i : i / ntok(), row = rt * kRowTile + r;
+    m += (i - rt * ntok()) * kTok;
+    if (m >= a.M || row >= P.N) return;
+    const int64_t o = static_cast<int64_t>(m) * P.N + row;
     if (kF32) static_cast<float*>(P.y)[o] = v;
     else static_cast<uint16_t*>(P.y)[o] = f32_to_bf16_bits(v);
-  });
-}
+  }
+};
 
-struct Q4ExpertArgs {
+struct Q4Experts {
   const uint8_t* codes;
   const uint16_t* scales;
   int64_t gcode, ecode, escale;  // code bytes per group, per expert; scales per expert
   int32_t gscale, N, nc;
   lbq_expert_rows r;
+  float* part;
+  unsigned* count;
 };
 
-template <int kG>
-__global__ void __launch_bounds__(kThreads, 2) q4_expert_kernel(const __grid_constant__ Q4ExpertArgs a) {
-  __shared__ float red[kWarps][kRowTile * kMaxTokens];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2;
-  const int e = blockIdx.y, row0 = blockIdx.x * kRowTile;
+// Tiles of expert e: its token tiles, each with all row tiles behind one another (so the
+// lanes' token rows, found through the slots, change rarely).
+template <int kTok>
+struct ExpertSource {
+  static constexpr bool kZeros = true;  // slots may name no token
+  const Q4Experts& a;
+  const int* off;  // [E + 1] first rows, clamped (shared memory)
+  const int* pre;  // [E + 1] tiles of the experts before
+  __device__ __forceinline__ int ntn() const { return (a.N + kRowTile - 1) / kRowTile; }
+  __device__ __forceinline__ int64_t chunks() const { return static_cast<int64_t>(pre[a.r.E]) * a.nc; }
+  __device__ __forceinline__ int64_t start(int e) const { return static_cast<int64_t>(pre[e]) * a.nc; }
+  __device__ __forceinline__ int nc(int) const { return a.nc; }
+  __device__ __forceinline__ int tiles(int e) const { return pre[e + 1] - pre[e]; }
+  __device__ __forceinline__ int next(int e) const {
+    do ++e; while (e < a.r.E && pre[e + 1] == pre[e]);
+    return e;
+  }
+  __device__ __forceinline__ int find(int64_t q) const {
+    const int tile = static_cast<int>(q / a.nc);
+    int lo = 0, hi = a.r.E;  // the last expert with pre[e] <= tile (the ones before it may be empty)
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (pre[mid] <= tile) lo = mid; else hi = mid;
+    }
+    return lo;
+  }
+  __device__ __forceinline__ void point(int e, int i, int lane, LanePtr& l) const {
+    const int g = lane >> 2, t = lane & 3, ng = (a.N + 3) >> 2, nt = i / ntn(), rt = i - nt * ntn();
+    int64_t grp = rt * (kRowTile / 4) + g;
+    if (grp >= ng) grp = ng - 1;
+    l.w = a.codes + e * a.ecode + grp * a.gcode + 16 * t;
+    l.s = a.scales + e * a.escale + grp * a.gscale;
+    {
+      const int row = off[e] + nt * kTok + g;
+      l.x = nullptr;
+      l.zero = false;
+      if (g < kTok && row < off[e + 1]) {
+        int64_t src = row;
+        if (a.r.slots) {
+          const int slot = __ldcg(a.r.slots + row);
+          src = slot < 0 ? -1 : slot / a.r.topk;
+        }
+        l.zero = src < 0 || src >= a.r.T;  // a slot of no token: a row of zeros
+        if (!l.zero) l.x = a.r.X + src * (static_cast<int64_t>(a.nc) * kQ4Chunk) + 8 * t;
+      }
+    }
+  }
+  __device__ __forceinline__ void store(int e, int i, int m, int r, float v) const {
+    const int nt = i / ntn(), row = (i - nt * ntn()) * kRowTile + r, y = off[e] + nt * kTok + m;
+    if (y < off[e + 1] && row < a.N) a.r.Y[static_cast<int64_t>(y) * a.N + row] = f32_to_bf16_bits(v);
+  }
+};
+
+// -------------------------------------------------------------------- the stream
+// A slot: 4 x 512 bytes of codes, 8 bytes of scales a row group and group of K, 256 bytes
+// of activations a token. Every lane copies the codes it will read itself; the scales of a
+// row group serve four lanes, and lanes of columns behind the last token read any bytes:
+// a column of the product depends on its own token only, and theirs are not stored.
+template <int kG, int kTok>
+struct Slot {  // (two a warp)
+  static constexpr uint32_t kScale = 2048;
+  static constexpr uint32_t kX = kScale + (kG == 32 ? 256 : 64);
+  static constexpr uint32_t kXStep = 64 * kTok;  // a lane's next 16 bytes
+  static constexpr uint32_t kBytes = kX + kTok * 256;
+};
+
+// A place in the line of chunks: chunk c of tile i of product p.
+struct Place {
+  int p, i, c;
+};
+template <typename Src>
+__device__ __forceinline__ Place place_of(const Src& src, int64_t q) {
+  Place a;
+  a.p = src.find(q);
+  const int64_t r = q - src.start(a.p);
+  a.i = static_cast<int>(r / src.nc(a.p));
+  a.c = static_cast<int>(r - static_cast<int64_t>(a.i) * src.nc(a.p));
+  return a;
+}
+
+template <int kG, int kTok, typename Src>
+__device__ __forceinline__ void stream_tiles(const Src& src, float* part, unsigned* count, int grid) {
+  using S = Slot<kG, kTok>;
+  constexpr int kOut = kRowTile * kTok;  // outputs of a tile
+  extern __shared__ __align__(128) unsigned char slots[];
+  // Of every warp's run: the end of a tile that began in an earlier run (0), the start of
+  // one that goes on in the next (1).
+  __shared__ float ends[kWarps][2][kOut];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+  const int64_t W = src.chunks();
+  const int b = static_cast<int>(blockIdx.x);
+  if (b >= grid) return;
+  auto run_start = [&](int w) { return W * (b * kWarps + w) / (static_cast<int64_t>(grid) * kWarps); };
+
+  // --- fetching: chunks 0 .. n - 1 of this warp's run
+  const int64_t q0 = run_start(warp);
+  const int n = static_cast<int>(run_start(warp + 1) - q0);
+  const uint32_t slot0 = smem_u32(slots) + warp * (2 * S::kBytes), flip = slot0 ^ (slot0 + S::kBytes);
+  Place u = {0, 0, 0};
+  if (n > 0) u = place_of(src, q0);
+  Place f = u;
+  LanePtr l = {};
+  int left = 0, qf = 0;  // chunks left of the tile being fetched; of the run, those fetched
+  auto point = [&]() {   // the pointers to chunk f.c
+    src.point(f.p, f.i, lane, l);
+    l.w += static_cast<int64_t>(f.c) * 256;
+    l.s += static_cast<int64_t>(f.c) * (kG == 32 ? 16 : 4) + (kG == 32 ? 4 * t : 0);
+    if (l.x) l.x += static_cast<int64_t>(f.c) * kQ4Chunk;
+    left = src.nc(f.p) - f.c;
+  };
+  if (n > 0) point();
+  uint32_t fslot = slot0;
+  auto fetch = [&]() {
+    if (qf < n) {
+#pragma unroll
+      for (int s = 0; s < 4; ++s) cp16(fslot + 512u * s + 16u * lane, l.w + 64 * s);
+      if (kG == 32) cp8(fslot + S::kScale + 8u * lane, l.s);
+      else if (t == 0) cp8(fslot + S::kScale + 8u * g, l.s);
+      const uint32_t d = fslot + S::kX + 16u * lane;
+      if (l.x) {
+#pragma unroll
+        for (int s = 0; s < 4; ++s) cp16(d + S::kXStep * s, l.x + 32 * s);
+        l.x += kQ4Chunk;
+      } else if (Src::kZeros && l.zero) {
+#pragma unroll
+        for (int s = 0; s < 4; ++s)
+          asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(d + S::kXStep * s), "r"(0u) : "memory");
+      }
+      l.w += 256;
+      l.s += kG == 32 ? 16 : 4;
+      if (++qf < n && --left == 0) {
+        f.c = 0;
+        if (++f.i == src.tiles(f.p)) {
+          f.i = 0;
+          f.p = src.next(f.p);
+        }
+        point();
+      }
+    }
+    cp_commit();
+    fslot ^= flip;
+  };
+  fetch();
+  fetch();
+
+  // --- the run's tiles, whole or in part
+  uint32_t cslot = slot0;
+  const uint32_t xoff = S::kX + 16u * (lane & (4 * kTok - 1));
+  Place head = {-1, 0, 0}, tail = {-1, 0, 0};  // the tiles of this run's ends
+  int64_t tail_q = 0;                          // where the second begins
+  const int head_c = u.c;
+  for (int q = 0; q < n;) {
+    const int nc = src.nc(u.p);
+    const int qe = nc - u.c < n - q ? q + (nc - u.c) : n;
+    float acc[2][4] = {};
+    const int part_c = u.c, part_q = q;
+    for (; q < qe; ++q) {
+      cp_wait<1>();
+      __syncwarp();  // (the other lanes' scales)
+      float sum[2][4];
+#pragma unroll
+      for (int s = 0; s < 4; ++s) {
+        const uint4 w = lds128(cslot + 512u * s + 16u * lane);
+        const uint4 x = lds128(cslot + xoff + S::kXStep * s);
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const uint32_t a0[4] = {q4_pair(w.x, 2 * j), q4_pair(w.y, 2 * j), q4_pair(w.x, 2 * j + 1), q4_pair(w.y, 2 * j + 1)};
+          const uint32_t a1[4] = {q4_pair(w.z, 2 * j), q4_pair(w.w, 2 * j), q4_pair(w.z, 2 * j + 1), q4_pair(w.w, 2 * j + 1)};
+          const uint32_t b0 = j ? x.z : x.x, b1 = j ? x.w : x.y;
+          if (j == 0 && (kG == 32 || s == 0)) {
+            mma_bf16_first(sum[0], a0, b0, b1);
+            mma_bf16_first(sum[1], a1, b0, b1);
+          } else {
+            mma_bf16(sum[0], a0, b0, b1);
+            mma_bf16(sum[1], a1, b0, b1);
+          }
+        }
+        if (kG == 32 || s == 3) {
+          const uint2 sc = lds64(cslot + S::kScale + (kG == 32 ? 32u * g + 8u * s : 8u * g));
+          const float2 s01 = __half22float2(*reinterpret_cast<const __half2*>(&sc.x));
+          const float2 s23 = __half22float2(*reinterpret_cast<const __half2*>(&sc.y));
+#pragma unroll
+          for (int c = 0; c < (kTok == 1 ? 1 : 2); ++c) {  // tokens 2t, 2t + 1
+            acc[0][c] += s01.x * sum[0][c];
+            acc[0][2 + c] += s01.y * sum[0][2 + c];
+            acc[1][c] += s23.x * sum[1][c];
+            acc[1][2 + c] += s23.y * sum[1][2 + c];
+          }
+        }
+      }
+      __syncwarp();  // every lane has read the slot
+      fetch();
+      cslot ^= flip;
+    }
+    const bool whole = part_c == 0 && qe - part_q == nc;
+    float* const to = ends[warp][part_c == 0 ? 1 : 0];
+    if (part_c > 0) head = u;
+    else if (!whole) tail = u, tail_q = q0 + part_q;
+#pragma unroll
+    for (int c = 0; c < (kTok == 1 ? 1 : 2); ++c)
+      if (2 * t + c < kTok)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {  // row 4g + r of token 2t + c
+          const float v = acc[r >> 1][2 * (r & 1) + c];
+          if (whole) src.store(u.p, u.i, 2 * t + c, 4 * g + r, v);
+          else to[(2 * t + c) * kRowTile + 4 * g + r] = v;
+        }
+    u.c = 0;
+    if (q < n && ++u.i == src.tiles(u.p)) {
+      u.i = 0;
+      u.p = src.next(u.p);
+    }
+  }
+  cp_wait<0>();
+  __syncthreads();
+
+  // --- tiles that several warps share: joined by the warp in whose run the tile (or the
+  // CTA's part of it) begins
+  const int64_t c1 = run_start(kWarps);
+  auto join = [&](const Place& at, int64_t qt, int which) {
+    const int nc = src.nc(at.p);
+    const int64_t qn = qt + nc;
+    float v[kTok];  // row `lane` of every token
+#pragma unroll
+    for (int m = 0; m < kTok; ++m) v[m] = ends[warp][which][m * kRowTile + lane];
+    for (int w = warp + 1; w < kWarps; ++w) {
+      const int64_t s0 = run_start(w);
+      if (s0 >= qn) break;
+      if (s0 == run_start(w + 1)) continue;  // an empty run
+#pragma unroll
+      for (int m = 0; m < kTok; ++m) v[m] += ends[w][0][m * kRowTile + lane];
+    }
+    if (which == 1 && qn <= c1) {
+#pragma unroll
+      for (int m = 0; m < kTok; ++m) src.store(at.p, at.i, m, lane, v[m]);
+      return;
+    }
+    // shared with other CTAs
+#pragma unroll
+    for (int m = 0; m < kTok; ++m) __stcg(part + static_cast<int64_t>(2 * b + which) * kOut + m * kRowTile + lane, v[m]);
+    __threadfence();
+    __syncwarp();
+    auto cta_of = [&](int64_t q) { return static_cast<int>(((q + 1) * grid - 1) / W); };
+    const int first = cta_of(qt), parts = cta_of(qn - 1) - first + 1;
+    unsigned before = 0;
+    if (lane == 0) before = atomicAdd(count + first, 1u);
+    before = __shfl_sync(0xffffffffu, before, 0);
+    if (before != static_cast<unsigned>(parts - 1)) return;
+    __threadfence();
+#pragma unroll
+    for (int m = 0; m < kTok; ++m) {
+      float y = __ldcg(part + static_cast<int64_t>(2 * first + 1) * kOut + m * kRowTile + lane);
+      for (int k = 1; k < parts; ++k) y += __ldcg(part + static_cast<int64_t>(2 * (first + k)) * kOut + m * kRowTile + lane);
+      src.store(at.p, at.i, m, lane, y);
+    }
+    if (lane == 0) count[first] = 0;  // as it was found
+  };
+  if (head.p >= 0 && q0 == run_start(0)) join(head, q0 - head_c, 0);
+  if (tail.p >= 0) join(tail, tail_q, 1);
+}
+
+// Enough CTAs to fill the GPU, but at least a chunk for every warp of each.
+__device__ __forceinline__ int runs_for(int64_t chunks, int most) {
+  const int64_t n = (chunks + kWarps - 1) / kWarps;
+  return static_cast<int>(n < most ? n : most);
+}
+
+template <int kG, int kTok, int kCap, bool kF32>
+__global__ void __launch_bounds__(kThreads, ctas_per_sm(kTok))
+    q4_list_kernel(const __grid_constant__ Q4List<kCap> a) {
   pdl_launch_dependents();
   pdl_wait();
-  const int R = static_cast<int>(a.r.R);
-  int lo = __ldcg(a.r.offsets + e), hi = __ldcg(a.r.offsets + e + 1);
-  lo = lo < 0 ? 0 : lo;
-  hi = hi > R ? R : hi;
-  if (lo >= hi) return;
-  const int ng = (a.N + 3) >> 2, K = a.nc * kQ4Chunk;
-  int64_t grp = (row0 >> 2) + g;
-  if (grp >= ng) grp = ng - 1;
-  const uint8_t* codes = a.codes + e * a.ecode + grp * a.gcode;
-  const uint16_t* scales = a.scales + e * a.escale + grp * a.gscale;
-  for (int m0 = lo; m0 < hi; m0 += kMaxTokens) {
-    const uint16_t* xrow = nullptr;
-    if (m0 + g < hi) {
-      int64_t src = m0 + g;
-      if (a.r.slots) {
-        const int slot = __ldcg(a.r.slots + src);
-        src = slot < 0 ? -1 : slot / a.r.topk;
-      }
-      if (src >= 0 && src < a.r.T) xrow = a.r.X + src * K;
-    }
-    float acc[2][4] = {};
-    warp_sum_tile<kG>(codes, scales, a.nc, xrow, warp, lane, acc);
-    join_warps(red, acc, warp, lane, [&](int m, int r, float v) {
-      if (m0 + m < hi && row0 + r < a.N)
-        a.r.Y[static_cast<int64_t>(m0 + m) * a.N + row0 + r] = f32_to_bf16_bits(v);
-    });
-    __syncthreads();  // red is read before the next tokens' sums
+  const ListSource<kCap, kTok, kF32> src = {a};
+  stream_tiles<kG, kTok>(src, a.part, a.count, static_cast<int>(gridDim.x));
+}
+
+template <int kG, int kTok>
+__global__ void __launch_bounds__(kThreads, ctas_per_sm(kTok))
+    q4_expert_kernel(const __grid_constant__ Q4Experts a) {
+  __shared__ int off[LBQ_MAX_EXPERTS + 1], pre[LBQ_MAX_EXPERTS + 1];
+  pdl_launch_dependents();
+  pdl_wait();
+  const int R = static_cast<int>(a.r.R), E = a.r.E;
+  for (int e = threadIdx.x; e <= E; e += kThreads) {
+    const int v = __ldcg(a.r.offsets + e);
+    off[e] = v < 0 ? 0 : (v > R ? R : v);
   }
+  __syncthreads();
+  if (threadIdx.x < 32) {  // tiles before each expert: a running sum, 32 experts at a time
+    const int lane = threadIdx.x, ntn = (a.N + kRowTile - 1) / kRowTile;
+    int run = 0;
+    for (int e0 = 0; e0 < E; e0 += 32) {
+      const int e = e0 + lane, rows = e < E ? off[e + 1] - off[e] : 0;
+      const int c = rows > 0 ? (rows + kTok - 1) / kTok * ntn : 0;
+      int inc = c;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int v = __shfl_up_sync(0xffffffffu, inc, o);
+        if (lane >= o) inc += v;
+      }
+      if (e < E) pre[e] = run + inc - c;
+      run += __shfl_sync(0xffffffffu, inc, 31);
+    }
+    if (lane == 0) pre[E] = run;
+  }
+  __syncthreads();
+  if (pre[E] == 0) return;
+  const ExpertSource<kTok> src = {a, off, pre};
+  stream_tiles<kG, kTok>(src, a.part, a.count, runs_for(src.chunks(), static_cast<int>(gridDim.x)));
 }
 
 // Programmatic dependent launch on stream s: the kernel starts early and waits itself.
-template <typename... KArgs, typename... Args>
-cudaError_t launch_pdl(void (*k)(KArgs...), dim3 grid, dim3 block, cudaStream_t s, const Args&... args) {
+template <typename A>
+cudaError_t launch_pdl(void (*k)(A), size_t smem, unsigned grid, cudaStream_t s, const A& args) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = grid;
-  cfg.blockDim = block;
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, k, args...);
+  return cudaLaunchKernelEx(&cfg, k, args);
 }
 
-Q4Prod make_prod(const lbq_weights& w, const uint16_t* x, void* y) {
+// The kernel's shared-memory limit, set once per device.
+template <auto kKernel>
+cudaError_t allow_smem(size_t bytes) {
+  static PerDevice<bool> configured;
+  bool done = false;
+  return configured.get(
+      [&](int, bool* v) {
+        *v = true;
+        return cudaFuncSetAttribute(kKernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(bytes));
+      },
+      &done);
+}
+
+int most_runs(int tok) { return ctas_per_sm(tok) * sm_count(); }
+
+// Tokens a tile of the experts' products: by the average rows of an expert.
+int few_tok(int32_t E, int64_t R) { return R <= 2 * static_cast<int64_t>(E) ? 4 : 8; }
+
+// Workspace: the counters' 64 KB (one for every run), then two parts of a tile a run.
+float* part_of(void* ws) { return reinterpret_cast<float*>(static_cast<char*>(ws) + kWsCounterBytes); }
+
+template <int kG, int kTok, int kCap, bool kF32>
+cudaError_t launch_list(Q4List<kCap>& a, void* ws, cudaStream_t s) {
+  constexpr size_t smem = kWarps * 2 * Slot<kG, kTok>::kBytes;
+  a.part = part_of(ws);
+  a.count = static_cast<unsigned*>(ws);
+  const int64_t runs = (a.chunks + kWarps - 1) / kWarps;
+  const unsigned grid = static_cast<unsigned>(runs < most_runs(kTok) ? runs : most_runs(kTok));
+  const cudaError_t e = allow_smem<q4_list_kernel<kG, kTok, kCap, kF32>>(smem);
+  return e != cudaSuccess ? e : launch_pdl(q4_list_kernel<kG, kTok, kCap, kF32>, smem, grid, s, a);
+}
+
+template <int kG, int kTok>
+cudaError_t launch_experts(const Q4Experts& a, cudaStream_t s) {
+  constexpr size_t smem = kWarps * 2 * Slot<kG, kTok>::kBytes;
+  const cudaError_t e = allow_smem<q4_expert_kernel<kG, kTok>>(smem);
+  return e != cudaSuccess ? e : launch_pdl(q4_expert_kernel<kG, kTok>, smem, static_cast<unsigned>(most_runs(kTok)), s, a);
+}
+
+// Product p of a list, each row tile with `ntok` token tiles: q0 chunks lie before it.
+Q4Prod make_prod(const lbq_weights& w, const uint16_t* x, void* y, int64_t* q0, int64_t ntok = 1) {
   Q4Prod p;
   p.codes = static_cast<const uint8_t*>(w.codes);
   p.scales = static_cast<const uint16_t*>(w.scales);
   p.x = x;
   p.y = y;
+  p.q0 = *q0;
   p.gcode = 4 * w.code_stride;
   p.gscale = static_cast<int32_t>(4 * w.scale_stride);
   p.N = static_cast<int32_t>(w.N);
   p.nc = static_cast<int32_t>(w.K / kQ4Chunk);
-  p.tile0 = 0;
+  *q0 += (w.N + kRowTile - 1) / kRowTile * ntok * p.nc;
   return p;
 }
 
-unsigned tiles_of(int64_t N) { return static_cast<unsigned>((N + kRowTile - 1) / kRowTile); }
-
 }  // namespace
 
-cudaError_t lbq_launch_q4_list(const lbq_product* ps, int32_t n, float* y32, cudaStream_t s) {
+size_t lbq_q4_few_workspace(int64_t M) {
+  const int tok = M == 1 ? 1 : (M <= 4 ? 4 : 8);
+  return kWsCounterBytes + static_cast<size_t>(most_runs(tok)) * 2 * kRowTile * tok * sizeof(float);
+}
+
+cudaError_t lbq_launch_q4_list(const lbq_product* ps, int32_t n, float* y32, void* ws, cudaStream_t s) {
   const bool g32 = ps[0].w.fmt == LBQ_Q4G32;
   if (n == 1) {
     Q4List<1> a;
     a.n = 1;
     a.M = 1;
-    a.p[0] = make_prod(ps[0].w, ps[0].x, y32 ? static_cast<void*>(y32) : ps[0].y);
-    const dim3 grid(tiles_of(ps[0].w.N));
-    if (y32) return launch_pdl(g32 ? q4_list_kernel<32, 1, true> : q4_list_kernel<128, 1, true>, grid, kThreads, s, a);
-    return launch_pdl(g32 ? q4_list_kernel<32, 1, false> : q4_list_kernel<128, 1, false>, grid, kThreads, s, a);
+    a.chunks = 0;
+    a.p[0] = make_prod(ps[0].w, ps[0].x, y32 ? static_cast<void*>(y32) : ps[0].y, &a.chunks);
+    if (y32) return g32 ? launch_list<32, 1, 1, true>(a, ws, s) : launch_list<128, 1, 1, true>(a, ws, s);
+    return g32 ? launch_list<32, 1, 1, false>(a, ws, s) : launch_list<128, 1, 1, false>(a, ws, s);
   }
   static thread_local Q4List<LBQ_BATCH_MAX> a;  // 18 KB: off the stack
   a.n = n;
   a.M = 1;
-  // longest K first: its CTAs take longest, so they should not be the last to start
-  int32_t order[LBQ_BATCH_MAX];
-  for (int32_t i = 0; i < n; ++i) order[i] = i;
-  std::stable_sort(order, order + n, [&](int32_t i, int32_t k) { return ps[i].w.K > ps[k].w.K; });
-  int64_t tiles = 0;
-  for (int32_t i = 0; i < n; ++i) {
-    const lbq_product& q = ps[order[i]];
-    a.p[i] = make_prod(q.w, q.x, q.y);
-    a.p[i].tile0 = static_cast<int32_t>(tiles);
-    tiles += tiles_of(q.w.N);
-  }
-  if (tiles > INT32_MAX) return cudaErrorInvalidValue;
-  return launch_pdl(g32 ? q4_list_kernel<32, LBQ_BATCH_MAX, false> : q4_list_kernel<128, LBQ_BATCH_MAX, false>,
-                    dim3(static_cast<unsigned>(tiles)), kThreads, s, a);
+  a.chunks = 0;
+  for (int32_t i = 0; i < n; ++i) a.p[i] = make_prod(ps[i].w, ps[i].x, ps[i].y, &a.chunks);
+  return g32 ? launch_list<32, 1, LBQ_BATCH_MAX, false>(a, ws, s) : launch_list<128, 1, LBQ_BATCH_MAX, false>(a, ws, s);
 }
 
-cudaError_t lbq_launch_q4_few(const lbq_weights* w, const uint16_t* X, int64_t M, uint16_t* Y,
+cudaError_t lbq_launch_q4_few(const lbq_weights* w, const uint16_t* X, int64_t M, uint16_t* Y, void* ws,
                               cudaStream_t s) {
-  if (M > static_cast<int64_t>(65535) * kMaxTokens) return cudaErrorInvalidValue;
+  const bool g32 = w->fmt == LBQ_Q4G32;
+  const int tok = M <= 4 ? 4 : 8;
   Q4List<1> a;
   a.n = 1;
   a.M = static_cast<int32_t>(M);
-  a.p[0] = make_prod(*w, X, Y);
-  const dim3 grid(tiles_of(w->N), static_cast<unsigned>((M + kMaxTokens - 1) / kMaxTokens));
-  return launch_pdl(w->fmt == LBQ_Q4G32 ? q4_list_kernel<32, 1, false> : q4_list_kernel<128, 1, false>, grid,
-                    kThreads, s, a);
+  a.chunks = 0;
+  a.p[0] = make_prod(*w, X, Y, &a.chunks, (M + tok - 1) / tok);
+  if (tok == 4) return g32 ? launch_list<32, 4, 1, false>(a, ws, s) : launch_list<128, 4, 1, false>(a, ws, s);
+  return g32 ? launch_list<32, 8, 1, false>(a, ws, s) : launch_list<128, 8, 1, false>(a, ws, s);
 }
 
-cudaError_t lbq_launch_q4_expert_few(const lbq_weights* w, const lbq_expert_rows& r, cudaStream_t s) {
-  Q4ExpertArgs a;
+cudaError_t lbq_launch_q4_expert_few(const lbq_weights* w, const lbq_expert_rows& r, void* ws, cudaStream_t s) {
+  Q4Experts a;
   a.codes = static_cast<const uint8_t*>(w->codes);
   a.scales = static_cast<const uint16_t*>(w->scales);
   a.gcode = 4 * w->code_stride;
@@ -331,6 +604,9 @@ cudaError_t lbq_launch_q4_expert_few(const lbq_weights* w, const lbq_expert_rows
   a.N = static_cast<int32_t>(w->N);
   a.nc = static_cast<int32_t>(w->K / kQ4Chunk);
   a.r = r;
-  const dim3 grid(tiles_of(w->N), static_cast<unsigned>(r.E));
-  return launch_pdl(w->fmt == LBQ_Q4G32 ? q4_expert_kernel<32> : q4_expert_kernel<128>, grid, kThreads, s, a);
+  a.part = part_of(ws);
+  a.count = static_cast<unsigned*>(ws);
+  const bool g32 = w->fmt == LBQ_Q4G32;
+  if (few_tok(r.E, r.R) == 4) return g32 ? launch_experts<32, 4>(a, s) : launch_experts<128, 4>(a, s);
+  return g32 ? launch_experts<32, 8>(a, s) : launch_experts<128, 8>(a, s);
 }

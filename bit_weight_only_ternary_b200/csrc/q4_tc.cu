@@ -956,12 +956,12 @@ cudaError_t lbq_launch_q4_tc(const lbq_weights* w, const uint16_t* X, int64_t M,
 }
 
 size_t lbq_q4_expert_tc_workspace(const lbq_weights* w, int32_t E, int64_t R) {
-  return scratch_for(w, R, E, 0).total;
+  return kWsCounterBytes + scratch_for(w, R, E, 0).total;
 }
 
 cudaError_t lbq_launch_q4_expert_tc(const lbq_weights* w, const lbq_expert_rows& r, void* ws, cudaStream_t s) {
   const Plan p = {kMaxTileM, 1, 1, static_cast<int>(w->K / kTileK)};
-  char* base = static_cast<char*>(ws);
+  char* base = static_cast<char*>(ws) + kWsCounterBytes;
   return w->fmt == LBQ_Q4G32 ? launch<32>(w, p, &r, r.X, r.R, r.Y, base, s)
                              : launch<128>(w, p, &r, r.X, r.R, r.Y, base, s);
 }

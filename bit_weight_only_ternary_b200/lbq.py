@@ -462,11 +462,11 @@ def lbq_expert_workspace_bytes(ew: ExpertWeights, R: int) -> int:
 
 
 def workspace_for_experts(ew: ExpertWeights, R: int, device=None) -> torch.Tensor | None:
-    """A workspace of lbq_expert_workspace_bytes(ew, R) bytes (None if 0)."""
+    """A zero-filled workspace of lbq_expert_workspace_bytes(ew, R) bytes (None if 0)."""
     n = lbq_expert_workspace_bytes(ew, R)
     if n == 0:
         return None
-    return torch.empty(((n + 15) // 16) * 16, dtype=torch.uint8, device=device or ew.codes.device)
+    return torch.zeros(((n + 15) // 16) * 16, dtype=torch.uint8, device=device or ew.codes.device)
 
 
 def lbq_expert_gemm(ew: ExpertWeights, X: torch.Tensor, offsets: torch.Tensor, slots=None,

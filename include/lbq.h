@@ -347,8 +347,9 @@ lbq_status lbq_expert_combine_grad(const uint16_t* dout, const uint16_t* Y, int6
                                    const int32_t* rows, int64_t T, int32_t topk, const float* weights,
                                    uint16_t* dY, float* dweights, void* stream);
 
-/* Bytes of workspace lbq_expert_gemm needs for R rows (0: none, or bad arguments). The
- * counter rule of lbq_workspace_bytes does not apply: it is scratch only. */
+/* Bytes of workspace lbq_expert_gemm needs for R rows (0 on bad arguments), under the
+ * counter rule of lbq_workspace_bytes: its first 64 KB are zero when it is first used
+ * and zero again after every completed call. */
 size_t lbq_expert_workspace_bytes(const lbq_weights* w, int32_t E, int64_t R);
 
 /* Y[r] = W_hat_e x_r for every row r in [offsets[e], offsets[e+1]), x_r = X[slots[r] /

@@ -250,11 +250,16 @@ def test_batch_of_many_shapes_and_formats(L, orc):
         items.append((L.lbq_pack(fmt, W.cuda()), x[0].cuda(), D, y))
         want.append((Y[0], S[0]))
     plist = L.ProductList(items)
-    L.lbq_gemv_batch(plist, L.workspace_for_batch(plist))
+    ws = L.workspace_for_batch(plist)
+    L.lbq_gemv_batch(plist, ws)
+    first = [y.clone() for _, _, _, y in items]
+    L.lbq_gemv_batch(plist, ws)
+    assert all(torch.equal(y, f) for (_, _, _, y), f in zip(items, first))  # the same bits
+    assert not ws[:65536].any()  # the counters are left at zero
     for (pw, x, D, y), (Y, S) in zip(items, want):
         if pw.fmt in Q4:
+            # (sums may run in another order than in lbq_gemv, inside the same bound)
             _inside(y, Y, S, f"{pw.N}x{pw.K}")
-            assert torch.equal(y, L.lbq_gemv(pw, x))
         else:
             assert np.all(np.abs(y.double().cpu().numpy() - Y) <= 2.0 ** -8 * S)
     assert L.lbq_device_fault() == 0
