@@ -91,8 +91,11 @@ __device__ __forceinline__ void mma_bf16_first(float (&d)[4], const uint32_t (&a
 // A source gives the tiles of its products (or experts): tiles and chunks of product p,
 // the lane's pointers into tile i, and where its outputs go.
 struct LanePtr {
-  const uint8_t* w;        // the lane's word of its row group, chunk 0
-  const uint16_t* s;       // its row group's scales
+  const uint8_t* w;        // the tile's first row group's codes
+  const uint16_t* s;       // and scales
+  int64_t gcode;           // from one row group to the next
+  int32_t gscale;
+  int groups;              // row groups of the tile that exist (of 8)
   const uint16_t* x;       // its token's activations + 8 t; null: no token, or (zero) zeros
   bool zero;
 };
@@ -120,6 +123,7 @@ struct Q4List {
 template <int kCap, int kTok, bool kF32>
 struct ListSource {
   static constexpr bool kZeros = false;
+  static constexpr bool kEarly = true;  // the list and the weights are known before the previous kernel ends
   const Q4List<kCap>& a;
   __device__ __forceinline__ int64_t chunks() const { return a.chunks; }
   __device__ __forceinline__ int64_t start(int p) const { return a.p[p].q0; }
@@ -142,12 +146,14 @@ struct ListSource {
     const Q4Prod& P = a.p[p];
     const int g = lane >> 2, t = lane & 3, ng = (P.N + 3) >> 2;
     const int rt = kTok == 1 ? i : i / ntok(), m = (i - rt * ntok()) * kTok + g;  // token tiles run fastest
-    int64_t grp = rt * (kRowTile / 4) + g;
-    if (grp >= ng) grp = ng - 1;  // rows behind the last: read it again, store nothing
-    l.w = P.codes + grp * P.gcode + 16 * t;
+    const int64_t grp = rt * (kRowTile / 4);
+    l.w = P.codes + grp * P.gcode;
     l.s = P.scales + grp * P.gscale;
+    l.gcode = P.gcode;
+    l.gscale = P.gscale;
+    l.groups = ng - static_cast<int>(grp);
     const int64_t K = static_cast<int64_t>(P.nc) * kQ4Chunk;
-    l.x = g < kTok && m < a.M ? P.x + m * K + 8 * t : nullptr;
+    l.x = kTok == 1 ? P.x + 8 * lane : (g < kTok && m < a.M ? P.x + m * K + 8 * t : nullptr);
     l.zero = false;
   }
   __device__ __forceinline__ void store(int p, int i, int m, int r, float v) const {
@@ -176,6 +182,7 @@ struct Q4Experts {
 template <int kTok>
 struct ExpertSource {
   static constexpr bool kZeros = true;  // slots may name no token
+  static constexpr bool kEarly = false;
   const Q4Experts& a;
   const int* off;  // [E + 1] first rows, clamped (shared memory)
   const int* pre;  // [E + 1] tiles of the experts before
@@ -199,10 +206,12 @@ struct ExpertSource {
   }
   __device__ __forceinline__ void point(int e, int i, int lane, LanePtr& l) const {
     const int g = lane >> 2, t = lane & 3, ng = (a.N + 3) >> 2, nt = i / ntn(), rt = i - nt * ntn();
-    int64_t grp = rt * (kRowTile / 4) + g;
-    if (grp >= ng) grp = ng - 1;
-    l.w = a.codes + e * a.ecode + grp * a.gcode + 16 * t;
+    const int64_t grp = rt * (kRowTile / 4);
+    l.w = a.codes + e * a.ecode + grp * a.gcode;
     l.s = a.scales + e * a.escale + grp * a.gscale;
+    l.gcode = a.gcode;
+    l.gscale = a.gscale;
+    l.groups = ng - static_cast<int>(grp);
     {
       const int row = off[e] + nt * kTok + g;
       l.x = nullptr;
@@ -274,50 +283,84 @@ __device__ __forceinline__ void stream_tiles(const Src& src, float* part, unsign
   Place f = u;
   LanePtr l = {};
   int left = 0, qf = 0;  // chunks left of the tile being fetched; of the run, those fetched
+  // A copy instruction brings 256 bytes of two row groups (lanes 0-15 and 16-31); row groups
+  // behind the last are left out, and the rows computed from what is there are not stored.
+  const int hi = lane >> 4, lo = lane & 15;
+  const uint32_t wdst = 512u * (lo >> 2) + 16u * (lo & 3) + 64u * hi;
   auto point = [&]() {   // the pointers to chunk f.c
     src.point(f.p, f.i, lane, l);
-    l.w += static_cast<int64_t>(f.c) * 256;
-    l.s += static_cast<int64_t>(f.c) * (kG == 32 ? 16 : 4) + (kG == 32 ? 4 * t : 0);
+    l.w += static_cast<int64_t>(f.c) * 256 + hi * l.gcode + 16 * lo;
+    if (kG == 32) l.s += static_cast<int64_t>(f.c) * 16 + (lo >> 1) * static_cast<int64_t>(l.gscale) + 8 * (lo & 1);
+    else l.s += static_cast<int64_t>(f.c) * 4 + (lane & 7) * static_cast<int64_t>(l.gscale);
     if (l.x) l.x += static_cast<int64_t>(f.c) * kQ4Chunk;
     left = src.nc(f.p) - f.c;
   };
   if (n > 0) point();
-  uint32_t fslot = slot0;
-  auto fetch = [&]() {
+  auto fetch_w = [&](uint32_t d) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (2 * i + hi < l.groups) cp16(d + wdst + 128u * i, l.w + 2 * i * l.gcode);
+    if (kG == 32) {
+      if (lane < 16 && (lane >> 1) < l.groups) cp16(d + S::kScale + 16u * lane, l.s);
+    } else if (lane < 8 && lane < l.groups) {
+      cp8(d + S::kScale + 8u * lane, l.s);
+    }
+  };
+  auto fetch_x = [&](uint32_t d, const uint16_t* x, bool zero) {
+    d += S::kX + 16u * lane;
+    if (kTok == 1) {  // 128 activations: 16 lanes
+      if (lane < 16) cp16(d, x);
+    } else if (x) {
+#pragma unroll
+      for (int s = 0; s < 4; ++s) cp16(d + S::kXStep * s, x + 32 * s);
+    } else if (Src::kZeros && zero) {
+#pragma unroll
+      for (int s = 0; s < 4; ++s)
+        asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(d + S::kXStep * s), "r"(0u) : "memory");
+    }
+  };
+  auto advance = [&]() {  // to the next chunk of the run
+    l.w += 256;
+    l.s += kG == 32 ? 16 : 4;
+    if (kTok == 1 || l.x) l.x += kQ4Chunk;
+    if (++qf < n && --left == 0) {
+      f.c = 0;
+      if (++f.i == src.tiles(f.p)) {
+        f.i = 0;
+        f.p = src.next(f.p);
+      }
+      point();
+    }
+  };
+  // The first two chunks: their codes and scales before the previous kernel has finished
+  // (where that kernel decides nothing about them), the activations after it.
+  const uint16_t* x0[2] = {nullptr, nullptr};
+  bool z0[2] = {false, false};
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+    if (i < n) {
+      fetch_w(slot0 + i * S::kBytes);
+      x0[i] = l.x;
+      z0[i] = l.zero;
+      advance();
+    }
+  if (Src::kEarly) pdl_wait();
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    if (i < n) fetch_x(slot0 + i * S::kBytes, x0[i], z0[i]);
+    cp_commit();
+  }
+  uint32_t cslot = slot0;
+  auto fetch = [&]() {  // the next chunk into the slot just read
     if (qf < n) {
-#pragma unroll
-      for (int s = 0; s < 4; ++s) cp16(fslot + 512u * s + 16u * lane, l.w + 64 * s);
-      if (kG == 32) cp8(fslot + S::kScale + 8u * lane, l.s);
-      else if (t == 0) cp8(fslot + S::kScale + 8u * g, l.s);
-      const uint32_t d = fslot + S::kX + 16u * lane;
-      if (l.x) {
-#pragma unroll
-        for (int s = 0; s < 4; ++s) cp16(d + S::kXStep * s, l.x + 32 * s);
-        l.x += kQ4Chunk;
-      } else if (Src::kZeros && l.zero) {
-#pragma unroll
-        for (int s = 0; s < 4; ++s)
-          asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(d + S::kXStep * s), "r"(0u) : "memory");
-      }
-      l.w += 256;
-      l.s += kG == 32 ? 16 : 4;
-      if (++qf < n && --left == 0) {
-        f.c = 0;
-        if (++f.i == src.tiles(f.p)) {
-          f.i = 0;
-          f.p = src.next(f.p);
-        }
-        point();
-      }
+      fetch_w(cslot);
+      fetch_x(cslot, l.x, l.zero);
+      advance();
     }
     cp_commit();
-    fslot ^= flip;
   };
-  fetch();
-  fetch();
 
   // --- the run's tiles, whole or in part
-  uint32_t cslot = slot0;
   const uint32_t xoff = S::kX + 16u * (lane & (4 * kTok - 1));
   Place head = {-1, 0, 0}, tail = {-1, 0, 0};  // the tiles of this run's ends
   int64_t tail_q = 0;                          // where the second begins
@@ -442,7 +485,6 @@ template <int kG, int kTok, int kCap, bool kF32>
 __global__ void __launch_bounds__(kThreads, ctas_per_sm(kTok))
     q4_list_kernel(const __grid_constant__ Q4List<kCap> a) {
   pdl_launch_dependents();
-  pdl_wait();
   const ListSource<kCap, kTok, kF32> src = {a};
   stream_tiles<kG, kTok>(src, a.part, a.count, static_cast<int>(gridDim.x));
 }
