@@ -4,7 +4,7 @@
 // Work. A tile is 32 weight rows (eight groups of four) x up to 8 tokens over all of K;
 // its chunks are 128 of K (2 KB of codes). All tiles' chunks lie in one line, cut into
 // equal runs, one a warp: however many rows a product has, every SM streams until the end,
-// and a warp adds up its stretch of K alone. It streams through two slots of shared memory
+// and a warp adds up its stretch of K alone. It streams through slots of shared memory
 // of its own that asynchronous copies fill ahead, across tiles. A tile that lies in one
 // warp's run is stored by the warp; the parts of a tile that several warps share are
 // joined in K order, once, when the CTA's runs are done; where the CTA's runs end inside a
@@ -30,6 +30,12 @@
 #include "lbq_common.cuh"
 #include "sm100_async.cuh"
 
+#ifndef DEPTHS
+#define DEPTHS (kTok == 8 ? 3 : 2)
+#endif
+#ifndef CTAS
+#define CTAS (tok == 8 ? 2 : 3)
+#endif
 namespace {
 
 using namespace lbq;
@@ -38,7 +44,7 @@ constexpr int kWarps = 8;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kRowTile = 32;
 // CTAs an SM: what the slots leave room for.
-constexpr int ctas_per_sm(int tok) { return tok == 8 ? 2 : 3; }
+constexpr int ctas_per_sm(int tok) { return CTAS; }
 
 // Asynchronous copies global -> shared of this thread's own bytes (L1 is bypassed for 16).
 __device__ __forceinline__ void cp16(uint32_t dst, const void* src) {
@@ -239,12 +245,20 @@ struct ExpertSource {
 // row group serve four lanes, and lanes of columns behind the last token read any bytes:
 // a column of the product depends on its own token only, and theirs are not stored.
 template <int kG, int kTok>
-struct Slot {  // (two a warp)
+struct Slot {  // (kDepth a warp)
   static constexpr uint32_t kScale = 2048;
   static constexpr uint32_t kX = kScale + (kG == 32 ? 256 : 64);
   static constexpr uint32_t kXStep = 64 * kTok;  // a lane's next 16 bytes
   static constexpr uint32_t kBytes = kX + kTok * 256;
+  static constexpr int kDepth = DEPTHS;
 };
+
+// a / b for a >= 0, b > 0: in 32 bits where they fit (a 64-bit division takes some hundred
+// instructions, and a run's start and end have a dozen).
+__device__ __forceinline__ int64_t quot(int64_t a, int64_t b) {
+  if (((a | b) >> 32) == 0) return static_cast<uint32_t>(a) / static_cast<uint32_t>(b);
+  return a / b;
+}
 
 // A place in the line of chunks: chunk c of tile i of product p.
 struct Place {
@@ -255,7 +269,7 @@ __device__ __forceinline__ Place place_of(const Src& src, int64_t q) {
   Place a;
   a.p = src.find(q);
   const int64_t r = q - src.start(a.p);
-  a.i = static_cast<int>(r / src.nc(a.p));
+  a.i = static_cast<int>(quot(r, src.nc(a.p)));
   a.c = static_cast<int>(r - static_cast<int64_t>(a.i) * src.nc(a.p));
   return a;
 }
@@ -266,18 +280,20 @@ __device__ __forceinline__ void stream_tiles(const Src& src, float* part, unsign
   constexpr int kOut = kRowTile * kTok;  // outputs of a tile
   extern __shared__ __align__(128) unsigned char slots[];
   // Of every warp's run: the end of a tile that began in an earlier run (0), the start of
-  // one that goes on in the next (1).
-  __shared__ float ends[kWarps][2][kOut];
+  // one that goes on in the next (1). Kept in registers while the runs last, then in the
+  // slots' place.
+  float (*ends)[2][kOut] = reinterpret_cast<float (*)[2][kOut]>(slots);
+  static_assert(2 * kOut * sizeof(float) <= S::kDepth * S::kBytes, "ends do not fit");
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   const int64_t W = src.chunks();
   const int b = static_cast<int>(blockIdx.x);
   if (b >= grid) return;
-  auto run_start = [&](int w) { return W * (b * kWarps + w) / (static_cast<int64_t>(grid) * kWarps); };
+  auto run_start = [&](int w) { return quot(W * (b * kWarps + w), static_cast<int64_t>(grid) * kWarps); };
 
   // --- fetching: chunks 0 .. n - 1 of this warp's run
   const int64_t q0 = run_start(warp);
   const int n = static_cast<int>(run_start(warp + 1) - q0);
-  const uint32_t slot0 = smem_u32(slots) + warp * (2 * S::kBytes), flip = slot0 ^ (slot0 + S::kBytes);
+  const uint32_t slot0 = smem_u32(slots) + warp * (S::kDepth * S::kBytes);
   Place u = {0, 0, 0};
   if (n > 0) u = place_of(src, q0);
   Place f = u;
@@ -332,12 +348,12 @@ __device__ __forceinline__ void stream_tiles(const Src& src, float* part, unsign
       point();
     }
   };
-  // The first two chunks: their codes and scales before the previous kernel has finished
+  // The first chunks: their codes and scales before the previous kernel has finished
   // (where that kernel decides nothing about them), the activations after it.
-  const uint16_t* x0[2] = {nullptr, nullptr};
-  bool z0[2] = {false, false};
+  const uint16_t* x0[S::kDepth] = {};
+  bool z0[S::kDepth] = {};
 #pragma unroll
-  for (int i = 0; i < 2; ++i)
+  for (int i = 0; i < S::kDepth; ++i)
     if (i < n) {
       fetch_w(slot0 + i * S::kBytes);
       x0[i] = l.x;
@@ -346,7 +362,7 @@ __device__ __forceinline__ void stream_tiles(const Src& src, float* part, unsign
     }
   if (Src::kEarly) pdl_wait();
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
+  for (int i = 0; i < S::kDepth; ++i) {
     if (i < n) fetch_x(slot0 + i * S::kBytes, x0[i], z0[i]);
     cp_commit();
   }
@@ -365,13 +381,15 @@ __device__ __forceinline__ void stream_tiles(const Src& src, float* part, unsign
   Place head = {-1, 0, 0}, tail = {-1, 0, 0};  // the tiles of this run's ends
   int64_t tail_q = 0;                          // where the second begins
   const int head_c = u.c;
+  float acc[2][4], first[2][4];  // first: the sums of place 0
   for (int q = 0; q < n;) {
     const int nc = src.nc(u.p);
     const int qe = nc - u.c < n - q ? q + (nc - u.c) : n;
-    float acc[2][4] = {};
+#pragma unroll
+    for (int i = 0; i < 8; ++i) acc[i >> 2][i & 3] = 0.0f;
     const int part_c = u.c, part_q = q;
     for (; q < qe; ++q) {
-      cp_wait<1>();
+      cp_wait<S::kDepth - 1>();
       __syncwarp();  // (the other lanes' scales)
       float sum[2][4];
 #pragma unroll
@@ -406,21 +424,25 @@ __device__ __forceinline__ void stream_tiles(const Src& src, float* part, unsign
       }
       __syncwarp();  // every lane has read the slot
       fetch();
-      cslot ^= flip;
+      cslot = cslot == slot0 + (S::kDepth - 1) * S::kBytes ? slot0 : cslot + S::kBytes;
     }
     const bool whole = part_c == 0 && qe - part_q == nc;
-    float* const to = ends[warp][part_c == 0 ? 1 : 0];
-    if (part_c > 0) head = u;
-    else if (!whole) tail = u, tail_q = q0 + part_q;
+    if (part_c > 0) {
+      head = u;
 #pragma unroll
-    for (int c = 0; c < (kTok == 1 ? 1 : 2); ++c)
-      if (2 * t + c < kTok)
+      for (int i = 0; i < 8; ++i) first[i >> 2][i & 3] = acc[i >> 2][i & 3];
+    } else if (!whole) {
+      tail = u;
+      tail_q = q0 + part_q;
+    }
+    if (whole) {
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {  // row 4g + r of token 2t + c
-          const float v = acc[r >> 1][2 * (r & 1) + c];
-          if (whole) src.store(u.p, u.i, 2 * t + c, 4 * g + r, v);
-          else to[(2 * t + c) * kRowTile + 4 * g + r] = v;
-        }
+      for (int c = 0; c < (kTok == 1 ? 1 : 2); ++c)
+        if (2 * t + c < kTok)
+#pragma unroll
+          for (int r = 0; r < 4; ++r)  // row 4g + r of token 2t + c
+            src.store(u.p, u.i, 2 * t + c, 4 * g + r, acc[r >> 1][2 * (r & 1) + c]);
+    }
     u.c = 0;
     if (q < n && ++u.i == src.tiles(u.p)) {
       u.i = 0;
@@ -428,11 +450,24 @@ __device__ __forceinline__ void stream_tiles(const Src& src, float* part, unsign
     }
   }
   cp_wait<0>();
+  __shared__ int64_t starts[kWarps + 1];  // of the runs
+  if (lane == 0) starts[warp] = q0;
+  if (threadIdx.x == 0) starts[kWarps] = run_start(kWarps);
+  __syncthreads();  // every warp has left its slots
+#pragma unroll
+  for (int c = 0; c < (kTok == 1 ? 1 : 2); ++c)
+    if (2 * t + c < kTok)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const int o = (2 * t + c) * kRowTile + 4 * g + r;
+        if (head.p >= 0) ends[warp][0][o] = first[r >> 1][2 * (r & 1) + c];
+        if (tail.p >= 0) ends[warp][1][o] = acc[r >> 1][2 * (r & 1) + c];
+      }
   __syncthreads();
 
   // --- tiles that several warps share: joined by the warp in whose run the tile (or the
   // CTA's part of it) begins
-  const int64_t c1 = run_start(kWarps);
+  const int64_t c1 = starts[kWarps];
   auto join = [&](const Place& at, int64_t qt, int which) {
     const int nc = src.nc(at.p);
     const int64_t qn = qt + nc;
@@ -440,9 +475,9 @@ __device__ __forceinline__ void stream_tiles(const Src& src, float* part, unsign
 #pragma unroll
     for (int m = 0; m < kTok; ++m) v[m] = ends[warp][which][m * kRowTile + lane];
     for (int w = warp + 1; w < kWarps; ++w) {
-      const int64_t s0 = run_start(w);
+      const int64_t s0 = starts[w];
       if (s0 >= qn) break;
-      if (s0 == run_start(w + 1)) continue;  // an empty run
+      if (s0 == starts[w + 1]) continue;  // an empty run
 #pragma unroll
       for (int m = 0; m < kTok; ++m) v[m] += ends[w][0][m * kRowTile + lane];
     }
@@ -454,15 +489,15 @@ __device__ __forceinline__ void stream_tiles(const Src& src, float* part, unsign
     // shared with other CTAs
 #pragma unroll
     for (int m = 0; m < kTok; ++m) __stcg(part + static_cast<int64_t>(2 * b + which) * kOut + m * kRowTile + lane, v[m]);
-    __threadfence();
     __syncwarp();
-    auto cta_of = [&](int64_t q) { return static_cast<int>(((q + 1) * grid - 1) / W); };
+    auto cta_of = [&](int64_t q) { return static_cast<int>(quot((q + 1) * grid - 1, W)); };
     const int first = cta_of(qt), parts = cta_of(qn - 1) - first + 1;
     unsigned before = 0;
-    if (lane == 0) before = atomicAdd(count + first, 1u);
+    // (one atomic that releases this warp's stores and acquires the others')
+    if (lane == 0)
+      asm volatile("atom.acq_rel.gpu.global.add.u32 %0, [%1], 1;" : "=r"(before) : "l"(count + first) : "memory");
     before = __shfl_sync(0xffffffffu, before, 0);
     if (before != static_cast<unsigned>(parts - 1)) return;
-    __threadfence();
 #pragma unroll
     for (int m = 0; m < kTok; ++m) {
       float y = __ldcg(part + static_cast<int64_t>(2 * first + 1) * kOut + m * kRowTile + lane);
@@ -471,7 +506,7 @@ __device__ __forceinline__ void stream_tiles(const Src& src, float* part, unsign
     }
     if (lane == 0) count[first] = 0;  // as it was found
   };
-  if (head.p >= 0 && q0 == run_start(0)) join(head, q0 - head_c, 0);
+  if (head.p >= 0 && q0 == starts[0]) join(head, q0 - head_c, 0);
   if (tail.p >= 0) join(tail, tail_q, 1);
 }
 
@@ -492,7 +527,9 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(kTok))
 template <int kG, int kTok>
 __global__ void __launch_bounds__(kThreads, ctas_per_sm(kTok))
     q4_expert_kernel(const __grid_constant__ Q4Experts a) {
-  __shared__ int off[LBQ_MAX_EXPERTS + 1], pre[LBQ_MAX_EXPERTS + 1];
+  extern __shared__ __align__(128) unsigned char slots[];
+  int* const off = reinterpret_cast<int*>(slots + kWarps * Slot<kG, kTok>::kDepth * Slot<kG, kTok>::kBytes);  // [E + 1]
+  int* const pre = off + a.r.E + 1;                                                                           // [E + 1]
   pdl_launch_dependents();
   pdl_wait();
   const int R = static_cast<int>(a.r.R), E = a.r.E;
@@ -563,7 +600,7 @@ float* part_of(void* ws) { return reinterpret_cast<float*>(static_cast<char*>(ws
 
 template <int kG, int kTok, int kCap, bool kF32>
 cudaError_t launch_list(Q4List<kCap>& a, void* ws, cudaStream_t s) {
-  constexpr size_t smem = kWarps * 2 * Slot<kG, kTok>::kBytes;
+  constexpr size_t smem = kWarps * Slot<kG, kTok>::kDepth * Slot<kG, kTok>::kBytes;
   a.part = part_of(ws);
   a.count = static_cast<unsigned*>(ws);
   const int64_t runs = (a.chunks + kWarps - 1) / kWarps;
@@ -574,9 +611,10 @@ cudaError_t launch_list(Q4List<kCap>& a, void* ws, cudaStream_t s) {
 
 template <int kG, int kTok>
 cudaError_t launch_experts(const Q4Experts& a, cudaStream_t s) {
-  constexpr size_t smem = kWarps * 2 * Slot<kG, kTok>::kBytes;
-  const cudaError_t e = allow_smem<q4_expert_kernel<kG, kTok>>(smem);
-  return e != cudaSuccess ? e : launch_pdl(q4_expert_kernel<kG, kTok>, smem, static_cast<unsigned>(most_runs(kTok)), s, a);
+  constexpr size_t slots = kWarps * Slot<kG, kTok>::kDepth * Slot<kG, kTok>::kBytes;
+  const cudaError_t e = allow_smem<q4_expert_kernel<kG, kTok>>(slots + 8 * (LBQ_MAX_EXPERTS + 1));
+  return e != cudaSuccess ? e : launch_pdl(q4_expert_kernel<kG, kTok>, slots + 8 * static_cast<size_t>(a.r.E + 1),
+                                           static_cast<unsigned>(most_runs(kTok)), s, a);
 }
 
 // Product p of a list, each row tile with `ntok` token tiles: q0 chunks lie before it.
