@@ -30,22 +30,16 @@
 #include "lbq_common.cuh"
 #include "sm100_async.cuh"
 
-#ifndef DEPTHS
-#define DEPTHS (kTok == 8 ? 3 : 2)
-#endif
-#ifndef CTAS
-#define CTAS (tok == 8 ? 2 : 3)
-#endif
 namespace {
 
 using namespace lbq;
 
-constexpr int kWarps = 8;
+// One CTA an SM. Twenty-four warps in three CTAs took 43 us for a 27B layer (the CTAs of an
+// SM advanced unevenly, 24 to 37 us), 24 in one CTA 41, 12 in one 40.5, 16 in one 39: more
+// bytes in flight fill longer at the start and drain longer at the end.
+constexpr int kWarps = 16;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kRowTile = 32;
-// CTAs an SM: what the slots leave room for.
-constexpr int ctas_per_sm(int tok) { return CTAS; }
-
 // Asynchronous copies global -> shared of this thread's own bytes (L1 is bypassed for 16).
 __device__ __forceinline__ void cp16(uint32_t dst, const void* src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
@@ -250,7 +244,7 @@ struct Slot {  // (kDepth a warp)
   static constexpr uint32_t kX = kScale + (kG == 32 ? 256 : 64);
   static constexpr uint32_t kXStep = 64 * kTok;  // a lane's next 16 bytes
   static constexpr uint32_t kBytes = kX + kTok * 256;
-  static constexpr int kDepth = DEPTHS;
+  static constexpr int kDepth = 2;
 };
 
 // a / b for a >= 0, b > 0: in 32 bits where they fit (a 64-bit division takes some hundred
@@ -517,7 +511,7 @@ __device__ __forceinline__ int runs_for(int64_t chunks, int most) {
 }
 
 template <int kG, int kTok, int kCap, bool kF32>
-__global__ void __launch_bounds__(kThreads, ctas_per_sm(kTok))
+__global__ void __launch_bounds__(kThreads, 1)
     q4_list_kernel(const __grid_constant__ Q4List<kCap> a) {
   pdl_launch_dependents();
   const ListSource<kCap, kTok, kF32> src = {a};
@@ -525,7 +519,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(kTok))
 }
 
 template <int kG, int kTok>
-__global__ void __launch_bounds__(kThreads, ctas_per_sm(kTok))
+__global__ void __launch_bounds__(kThreads, 1)
     q4_expert_kernel(const __grid_constant__ Q4Experts a) {
   extern __shared__ __align__(128) unsigned char slots[];
   int* const off = reinterpret_cast<int*>(slots + kWarps * Slot<kG, kTok>::kDepth * Slot<kG, kTok>::kBytes);  // [E + 1]
@@ -590,7 +584,7 @@ cudaError_t allow_smem(size_t bytes) {
       &done);
 }
 
-int most_runs(int tok) { return ctas_per_sm(tok) * sm_count(); }
+int most_runs() { return sm_count(); }
 
 // Tokens a tile of the experts' products: by the average rows of an expert.
 int few_tok(int32_t E, int64_t R) { return R <= 2 * static_cast<int64_t>(E) ? 4 : 8; }
@@ -604,7 +598,7 @@ cudaError_t launch_list(Q4List<kCap>& a, void* ws, cudaStream_t s) {
   a.part = part_of(ws);
   a.count = static_cast<unsigned*>(ws);
   const int64_t runs = (a.chunks + kWarps - 1) / kWarps;
-  const unsigned grid = static_cast<unsigned>(runs < most_runs(kTok) ? runs : most_runs(kTok));
+  const unsigned grid = static_cast<unsigned>(runs < most_runs() ? runs : most_runs());
   const cudaError_t e = allow_smem<q4_list_kernel<kG, kTok, kCap, kF32>>(smem);
   return e != cudaSuccess ? e : launch_pdl(q4_list_kernel<kG, kTok, kCap, kF32>, smem, grid, s, a);
 }
@@ -614,7 +608,7 @@ cudaError_t launch_experts(const Q4Experts& a, cudaStream_t s) {
   constexpr size_t slots = kWarps * Slot<kG, kTok>::kDepth * Slot<kG, kTok>::kBytes;
   const cudaError_t e = allow_smem<q4_expert_kernel<kG, kTok>>(slots + 8 * (LBQ_MAX_EXPERTS + 1));
   return e != cudaSuccess ? e : launch_pdl(q4_expert_kernel<kG, kTok>, slots + 8 * static_cast<size_t>(a.r.E + 1),
-                                           static_cast<unsigned>(most_runs(kTok)), s, a);
+                                           static_cast<unsigned>(most_runs()), s, a);
 }
 
 // Product p of a list, each row tile with `ntok` token tiles: q0 chunks lie before it.
@@ -637,7 +631,7 @@ Q4Prod make_prod(const lbq_weights& w, const uint16_t* x, void* y, int64_t* q0, 
 
 size_t lbq_q4_few_workspace(int64_t M) {
   const int tok = M == 1 ? 1 : (M <= 4 ? 4 : 8);
-  return kWsCounterBytes + static_cast<size_t>(most_runs(tok)) * 2 * kRowTile * tok * sizeof(float);
+  return kWsCounterBytes + static_cast<size_t>(most_runs()) * 2 * kRowTile * tok * sizeof(float);
 }
 
 cudaError_t lbq_launch_q4_list(const lbq_product* ps, int32_t n, float* y32, void* ws, cudaStream_t s) {
