@@ -97,6 +97,7 @@ struct LanePtr {
   int32_t gscale;
   int groups;              // row groups of the tile that exist (of 8)
   const uint16_t* x;       // its token's activations + 8 t; null: no token, or (zero) zeros
+  const uint16_t* x0;      // where x stood at chunk 0 of the tile
   bool zero;
 };
 
@@ -142,7 +143,7 @@ struct ListSource {
     }
     return lo;
   }
-  __device__ __forceinline__ void point(int p, int i, int lane, LanePtr& l) const {
+  __device__ __forceinline__ void point(int p, int i, int lane, bool, LanePtr& l) const {
     const Q4Prod& P = a.p[p];
     const int g = lane >> 2, t = lane & 3, ng = (P.N + 3) >> 2;
     const int rt = kTok == 1 ? i : i / ntok(), m = (i - rt * ntok()) * kTok + g;  // token tiles run fastest
@@ -153,7 +154,7 @@ struct ListSource {
     l.gscale = P.gscale;
     l.groups = ng - static_cast<int>(grp);
     const int64_t K = static_cast<int64_t>(P.nc) * kQ4Chunk;
-    l.x = kTok == 1 ? P.x + 8 * lane : (g < kTok && m < a.M ? P.x + m * K + 8 * t : nullptr);
+    l.x0 = kTok == 1 ? P.x + 8 * lane : (g < kTok && m < a.M ? P.x + m * K + 8 * t : nullptr);
     l.zero = false;
   }
   __device__ __forceinline__ void store(int p, int i, int m, int r, float v) const {
@@ -204,7 +205,8 @@ struct ExpertSource {
     }
     return lo;
   }
-  __device__ __forceinline__ void point(int e, int i, int lane, LanePtr& l) const {
+  // (next: the lane stood in the tile before this one, which mostly has the same tokens)
+  __device__ __forceinline__ void point(int e, int i, int lane, bool next, LanePtr& l) const {
     const int g = lane >> 2, t = lane & 3, ng = (a.N + 3) >> 2, nt = i / ntn(), rt = i - nt * ntn();
     const int64_t grp = rt * (kRowTile / 4);
     l.w = a.codes + e * a.ecode + grp * a.gcode;
@@ -212,19 +214,18 @@ struct ExpertSource {
     l.gcode = a.gcode;
     l.gscale = a.gscale;
     l.groups = ng - static_cast<int>(grp);
-    {
-      const int row = off[e] + nt * kTok + g;
-      l.x = nullptr;
-      l.zero = false;
-      if (g < kTok && row < off[e + 1]) {
-        int64_t src = row;
-        if (a.r.slots) {
-          const int slot = __ldcg(a.r.slots + row);
-          src = slot < 0 ? -1 : slot / a.r.topk;
-        }
-        l.zero = src < 0 || src >= a.r.T;  // a slot of no token: a row of zeros
-        if (!l.zero) l.x = a.r.X + src * (static_cast<int64_t>(a.nc) * kQ4Chunk) + 8 * t;
+    if (next && rt > 0) return;
+    const int row = off[e] + nt * kTok + g;
+    l.x0 = nullptr;
+    l.zero = false;
+    if (g < kTok && row < off[e + 1]) {
+      int64_t src = row;
+      if (a.r.slots) {
+        const int slot = __ldcg(a.r.slots + row);
+        src = slot < 0 ? -1 : slot / a.r.topk;
       }
+      l.zero = src < 0 || src >= a.r.T;  // a slot of no token: a row of zeros
+      if (!l.zero) l.x0 = a.r.X + src * (static_cast<int64_t>(a.nc) * kQ4Chunk) + 8 * t;
     }
   }
   __device__ __forceinline__ void store(int e, int i, int m, int r, float v) const {
@@ -297,15 +298,16 @@ __device__ __forceinline__ void stream_tiles(const Src& src, float* part, unsign
   // behind the last are left out, and the rows computed from what is there are not stored.
   const int hi = lane >> 4, lo = lane & 15;
   const uint32_t wdst = 512u * (lo >> 2) + 16u * (lo & 3) + 64u * hi;
-  auto point = [&]() {   // the pointers to chunk f.c
-    src.point(f.p, f.i, lane, l);
+  auto point = [&](bool next) {   // the pointers to chunk f.c
+    src.point(f.p, f.i, lane, next, l);
+    l.x = l.x0;
     l.w += static_cast<int64_t>(f.c) * 256 + hi * l.gcode + 16 * lo;
     if (kG == 32) l.s += static_cast<int64_t>(f.c) * 16 + (lo >> 1) * static_cast<int64_t>(l.gscale) + 8 * (lo & 1);
     else l.s += static_cast<int64_t>(f.c) * 4 + (lane & 7) * static_cast<int64_t>(l.gscale);
     if (l.x) l.x += static_cast<int64_t>(f.c) * kQ4Chunk;
     left = src.nc(f.p) - f.c;
   };
-  if (n > 0) point();
+  if (n > 0) point(false);
   auto fetch_w = [&](uint32_t d) {
 #pragma unroll
     for (int i = 0; i < 4; ++i)
@@ -339,7 +341,7 @@ __device__ __forceinline__ void stream_tiles(const Src& src, float* part, unsign
         f.i = 0;
         f.p = src.next(f.p);
       }
-      point();
+      point(true);
     }
   };
   // The first chunks: their codes and scales before the previous kernel has finished
