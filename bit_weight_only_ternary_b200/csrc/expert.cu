@@ -16,14 +16,28 @@ namespace {
 using namespace lbq;
 namespace cg = cooperative_groups;
 
-constexpr int kSortThreads = 1024, kSortWarps = kSortThreads / 32;
+constexpr int kSortThreads = 512, kSortWarps = kSortThreads / 32;
 constexpr int kSortCluster = 8;
+// Slots of a warp's run that stay in registers, 32 at a time (a run of more is read twice).
+constexpr int kSortKeep = 8;
 
 template <typename Id>
 __device__ __forceinline__ int expert_of(const Id* ids, int64_t i, int64_t end, int E) {
   if (i >= end) return E;
   const Id v = ids[i];
   return v >= 0 && v < static_cast<Id>(E) ? static_cast<int>(v) : E;
+}
+
+// The lanes with this lane's value (bits 0 .. bits-1): one ballot a bit. (A match
+// instruction costs more.)
+__device__ __forceinline__ unsigned peers_of(int v, int bits) {
+  unsigned peers = 0xffffffffu;
+  for (int b = 0; b < bits; ++b) {
+    const bool set = (v >> b) & 1;
+    const unsigned m = __ballot_sync(0xffffffffu, set);
+    peers &= set ? m : ~m;
+  }
+  return peers;
 }
 
 // Shared memory: hist [warps][E], tot [E], base [E].
@@ -45,58 +59,75 @@ __global__ void __launch_bounds__(kSortThreads, 1)
   const int64_t w0 = (static_cast<int64_t>(rank) * kSortWarps + warp) * per_warp;
   const int64_t w1 = w0 + per_warp < R ? w0 + per_warp : R;
   int32_t* mine = hist + warp * E;
-  for (int64_t i = w0; i < w1; i += 32) {
-    const int e = expert_of(ids, i + lane, w1, E);
-    const unsigned peers = __match_any_sync(0xffffffffu, e);
+  const int bits = 32 - __clz(E);  // of the values 0 .. E
+  // the warp's first ids, all loads at once
+  int kept[kSortKeep];
+#pragma unroll
+  for (int k = 0; k < kSortKeep; ++k) kept[k] = w0 + 32 * k < w1 ? expert_of(ids, w0 + 32 * k + lane, w1, E) : E;
+  auto count = [&](int e) {
+    const unsigned peers = peers_of(e, bits);
     if (e < E && lane == __ffs(peers) - 1) mine[e] += __popc(peers);
     __syncwarp();
-  }
+  };
+#pragma unroll
+  for (int k = 0; k < kSortKeep; ++k)
+    if (w0 + 32 * k < w1) count(kept[k]);
+  for (int64_t i = w0 + 32 * kSortKeep; i < w1; i += 32) count(expert_of(ids, i + lane, w1, E));
   __syncthreads();
   // each expert's counts of the warps before, and the CTA's total
   for (int e = tid; e < E; e += kSortThreads) {
-    int32_t run = 0;
+    int32_t c[kSortWarps], run = 0;
+#pragma unroll
+    for (int w = 0; w < kSortWarps; ++w) c[w] = hist[w * E + e];
+#pragma unroll
     for (int w = 0; w < kSortWarps; ++w) {
-      const int32_t c = hist[w * E + e];
       hist[w * E + e] = run;
-      run += c;
+      run += c[w];
     }
     tot[e] = run;
   }
   cluster.sync();
-  // thread e (E <= kSortThreads): totals of all CTAs, those of the CTAs before this one
-  int32_t all = 0, before = 0;
-  if (tid < E) {
-    for (int c = 0; c < C; ++c) {
-      const int32_t v = *cluster.map_shared_rank(tot + tid, c);
-      all += v;
-      if (c < rank) before += v;
-    }
-  }
-  cluster.sync();  // no CTA leaves while another still reads its totals
-  int32_t scan = all;  // inclusive over the warp, then over the CTA
+  // thread e: totals of all CTAs and of those before this one, and their running sum over
+  // the experts (kSortThreads at a time)
+  int32_t total = 0;
+  for (int e0 = 0; e0 < E; e0 += kSortThreads) {
+    const int e = e0 + tid;
+    int32_t all = 0, before = 0;
+    if (e < E) {
+      int32_t v[kSortCluster];
 #pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int32_t v = __shfl_up_sync(0xffffffffu, scan, o);
-    if (lane >= o) scan += v;
-  }
-  if (lane == 31) wsum[warp] = scan;
-  __syncthreads();
-  int32_t ahead = 0, total = 0;
-  for (int w = 0; w < kSortWarps; ++w) {
-    if (w < warp) ahead += wsum[w];
-    total += wsum[w];
-  }
-  if (tid < E) {
-    const int32_t first = ahead + scan - all;
-    base[tid] = first + before;
-    if (rank == 0) offsets[tid] = first;
+      for (int c = 0; c < kSortCluster; ++c) v[c] = c < C ? *cluster.map_shared_rank(tot + e, c) : 0;
+#pragma unroll
+      for (int c = 0; c < kSortCluster; ++c) {
+        all += v[c];
+        if (c < rank) before += v[c];
+      }
+    }
+    int32_t scan = all;  // inclusive over the warp, then over the CTA
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int32_t v = __shfl_up_sync(0xffffffffu, scan, o);
+      if (lane >= o) scan += v;
+    }
+    if (lane == 31) wsum[warp] = scan;
+    __syncthreads();
+    int32_t ahead = total;
+    for (int w = 0; w < kSortWarps; ++w) {
+      if (w < warp) ahead += wsum[w];
+      total += wsum[w];
+    }
+    if (e < E) {
+      const int32_t first = ahead + scan - all;
+      base[e] = first + before;
+      if (rank == 0) offsets[e] = first;
+    }
+    __syncthreads();
   }
   if (rank == 0 && tid == 0) offsets[E] = total;
-  __syncthreads();
+  cluster.sync();  // no CTA leaves while another still reads its totals
   const unsigned below = (1u << lane) - 1u;
-  for (int64_t i = w0; i < w1; i += 32) {
-    const int e = expert_of(ids, i + lane, w1, E);
-    const unsigned peers = __match_any_sync(0xffffffffu, e);
+  auto place = [&](int e, int64_t i) {
+    const unsigned peers = peers_of(e, bits);
     int32_t row = -1;
     if (e < E) row = base[e] + mine[e] + __popc(peers & below);
     __syncwarp();
@@ -106,7 +137,11 @@ __global__ void __launch_bounds__(kSortThreads, 1)
       rows[i + lane] = row;
       if (row >= 0) slots[row] = static_cast<int32_t>(i + lane);
     }
-  }
+  };
+#pragma unroll
+  for (int k = 0; k < kSortKeep; ++k)
+    if (w0 + 32 * k < w1) place(kept[k], w0 + 32 * k);
+  for (int64_t i = w0 + 32 * kSortKeep; i < w1; i += 32) place(expert_of(ids, i + lane, w1, E), i);
   for (int64_t r = total + static_cast<int64_t>(rank) * kSortThreads + tid; r < R; r += static_cast<int64_t>(C) * kSortThreads)
     slots[r] = -1;
 }
@@ -163,7 +198,7 @@ template <int kVec, bool kWeighted>
 __global__ void __launch_bounds__(kRowThreads)
     dispatch_kernel(const uint16_t* __restrict__ X, const RouteArgs a, uint16_t* __restrict__ out) {
   const int64_t t = blockIdx.x;
-  for (int64_t n = static_cast<int64_t>(threadIdx.x) * kVec; n < a.N; n += kRowThreads * kVec) {
+  for (int64_t n = static_cast<int64_t>(threadIdx.x) * kVec; n < a.N; n += static_cast<int64_t>(blockDim.x) * kVec) {
     Vec<kVec> v;
     v.load(X + t * a.N + n);
     float f[kVec];
@@ -186,83 +221,124 @@ __global__ void __launch_bounds__(kRowThreads)
   }
 }
 
-template <int kVec, bool kWeighted>
-__global__ void __launch_bounds__(kRowThreads)
-    combine_kernel(const uint16_t* __restrict__ Y, const RouteArgs a, uint16_t* __restrict__ out) {
-  const int64_t t = blockIdx.x;
-  for (int64_t n = static_cast<int64_t>(threadIdx.x) * kVec; n < a.N; n += kRowThreads * kVec) {
-    float acc[kVec] = {};
-#pragma unroll 4
-    for (int j = 0; j < a.topk; ++j) {
-      const int64_t r = row_of(a, t * a.topk + j);
-      if (r < 0) continue;
-      const float w = kWeighted ? __ldg(a.weights + t * a.topk + j) : 1.0f;
-      Vec<kVec> v;
-      v.load(Y + r * a.N + n);
-      float f[kVec];
-      v.get(f);
+// Slots of a token taken together: their rows' loads are all in flight at once.
+constexpr int kSlotsAtOnce = 8;
+
+// The rows (and weights) of up to eight slots of a token. CTAs walk over the tokens and
+// read the next token's ahead: looked up when they were needed, they put a second memory
+// latency before every token's rows (32768 rows of 2048: 27 us to add up).
+template <bool kWeighted>
+struct Slots {
+  int32_t r[kSlotsAtOnce];
+  float w[kSlotsAtOnce];
+  __device__ __forceinline__ void load(const RouteArgs& a, int64_t t, int64_t T, int j0) {
 #pragma unroll
-      for (int i = 0; i < kVec; ++i) acc[i] += kWeighted ? w * f[i] : f[i];
+    for (int j = 0; j < kSlotsAtOnce; ++j) {
+      const bool in = t < T && j0 + j < a.topk;
+      r[j] = in ? __ldg(a.rows + t * a.topk + j0 + j) : -1;
+      w[j] = kWeighted && in ? __ldg(a.weights + t * a.topk + j0 + j) : 1.0f;
+      if (r[j] >= a.R) r[j] = -1;
     }
-    Vec<kVec> o;
-    o.set(acc);
-    o.store(out + t * a.N + n);
+  }
+};
+
+template <int kVec, bool kWeighted>
+__global__ void __launch_bounds__(kRowThreads, 4)
+    combine_kernel(const uint16_t* __restrict__ Y, const RouteArgs a, int64_t T, uint16_t* __restrict__ out) {
+  Slots<kWeighted> next;
+  next.load(a, blockIdx.x, T, 0);
+  for (int64_t t = blockIdx.x; t < T; t += gridDim.x) {
+    const Slots<kWeighted> first = next;
+    next.load(a, t + gridDim.x, T, 0);
+    for (int64_t n = static_cast<int64_t>(threadIdx.x) * kVec; n < a.N; n += static_cast<int64_t>(blockDim.x) * kVec) {
+      float acc[kVec] = {};
+      for (int j0 = 0; j0 < a.topk; j0 += kSlotsAtOnce) {
+        Slots<kWeighted> s = first;
+        if (j0) s.load(a, t, T, j0);
+        Vec<kVec> v[kSlotsAtOnce];
+#pragma unroll
+        for (int j = 0; j < kSlotsAtOnce; ++j)
+          if (s.r[j] >= 0) v[j].load(Y + s.r[j] * a.N + n);
+#pragma unroll
+        for (int j = 0; j < kSlotsAtOnce; ++j) {
+          if (s.r[j] < 0) continue;
+          float f[kVec];
+          v[j].get(f);
+#pragma unroll
+          for (int i = 0; i < kVec; ++i) acc[i] += kWeighted ? s.w[j] * f[i] : f[i];
+        }
+      }
+      Vec<kVec> o;
+      o.set(acc);
+      o.store(out + t * a.N + n);
+    }
   }
 }
 
-// Slots of a token taken together in one walk over its columns.
-constexpr int kSlotsAtOnce = 8;
-
 template <int kVec>
-__global__ void __launch_bounds__(kRowThreads)
+__global__ void __launch_bounds__(kRowThreads, 3)
     combine_grad_kernel(const uint16_t* __restrict__ dout, const uint16_t* __restrict__ Y,
-                        const RouteArgs a, uint16_t* __restrict__ dY, float* __restrict__ dweights) {
-  __shared__ float red[kRowThreads / 32][kSlotsAtOnce];
-  const int64_t t = blockIdx.x;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  for (int j0 = 0; j0 < a.topk; j0 += kSlotsAtOnce) {
-    int64_t r[kSlotsAtOnce];
-    float w[kSlotsAtOnce], dot[kSlotsAtOnce] = {};
+                        const RouteArgs a, int64_t T, uint16_t* __restrict__ dY, float* __restrict__ dweights) {
+  __shared__ float red[2][kRowThreads / 32][kSlotsAtOnce];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = static_cast<int>(blockDim.x) >> 5;
+  int buf = 0;
+  Slots<true> next;
+  next.load(a, blockIdx.x, T, 0);
+  for (int64_t t = blockIdx.x; t < T; t += gridDim.x) {
+    for (int j0 = 0; j0 < a.topk; j0 += kSlotsAtOnce, buf ^= 1) {
+      const Slots<true> s = next;
+      const bool more = j0 + kSlotsAtOnce < a.topk;
+      next.load(a, more ? t : t + gridDim.x, T, more ? j0 + kSlotsAtOnce : 0);
+      float dot[kSlotsAtOnce] = {};
+      for (int64_t n = static_cast<int64_t>(threadIdx.x) * kVec; n < a.N; n += static_cast<int64_t>(blockDim.x) * kVec) {
+        Vec<kVec> v, y[kSlotsAtOnce];
+        v.load(dout + t * a.N + n);
 #pragma unroll
-    for (int j = 0; j < kSlotsAtOnce; ++j) {
-      r[j] = j0 + j < a.topk ? row_of(a, t * a.topk + j0 + j) : -1;
-      w[j] = r[j] >= 0 ? __ldg(a.weights + t * a.topk + j0 + j) : 0.0f;
-    }
-    for (int64_t n = static_cast<int64_t>(threadIdx.x) * kVec; n < a.N; n += kRowThreads * kVec) {
-      Vec<kVec> v;
-      v.load(dout + t * a.N + n);
-      float g[kVec];
-      v.get(g);
+        for (int j = 0; j < kSlotsAtOnce; ++j)
+          if (s.r[j] >= 0) y[j].load(Y + s.r[j] * a.N + n);
+        float g[kVec];
+        v.get(g);
+#pragma unroll
+        for (int j = 0; j < kSlotsAtOnce; ++j) {
+          if (s.r[j] < 0) continue;
+          float f[kVec], p[kVec];
+          y[j].get(f);
+#pragma unroll
+          for (int i = 0; i < kVec; ++i) {
+            dot[j] += g[i] * f[i];
+            p[i] = s.w[j] * g[i];
+          }
+          Vec<kVec> d;
+          d.set(p);
+          d.store(dY + s.r[j] * a.N + n);
+        }
+      }
+      // lanes by a fixed tree, then warps in order (two buffers: one barrier a round)
 #pragma unroll
       for (int j = 0; j < kSlotsAtOnce; ++j) {
-        if (r[j] < 0) continue;
-        Vec<kVec> y, d;
-        y.load(Y + r[j] * a.N + n);
-        float f[kVec], p[kVec];
-        y.get(f);
-#pragma unroll
-        for (int i = 0; i < kVec; ++i) {
-          dot[j] += g[i] * f[i];
-          p[i] = w[j] * g[i];
-        }
-        d.set(p);
-        d.store(dY + r[j] * a.N + n);
+        const float v = warp_sum(dot[j]);
+        if (lane == 0) red[buf][warp][j] = v;
+      }
+      __syncthreads();
+      if (threadIdx.x < kSlotsAtOnce && j0 + static_cast<int>(threadIdx.x) < a.topk) {
+        float v = 0.0f;
+        for (int q = 0; q < warps; ++q) v += red[buf][q][threadIdx.x];
+        dweights[t * a.topk + j0 + threadIdx.x] = v;
       }
     }
-    // lanes by a fixed tree, then warps in order
-#pragma unroll
-    for (int j = 0; j < kSlotsAtOnce; ++j) {
-      const float s = warp_sum(dot[j]);
-      if (lane == 0) red[warp][j] = s;
-    }
-    __syncthreads();
-    if (threadIdx.x < kSlotsAtOnce && j0 + static_cast<int>(threadIdx.x) < a.topk) {
-      float s = 0.0f;
-      for (int q = 0; q < kRowThreads / 32; ++q) s += red[q][threadIdx.x];
-      dweights[t * a.topk + j0 + threadIdx.x] = s;
-    }
-    __syncthreads();
   }
+}
+
+// Threads a token: one 16-byte (or single) column each, whole warps.
+int threads_for(int64_t N, int vec) {
+  const int64_t n = ((N + vec - 1) / vec + 31) / 32 * 32;
+  return n < kRowThreads ? static_cast<int>(n) : kRowThreads;
+}
+
+// CTAs that walk over T tokens: as many as are resident, at `full` CTAs of kRowThreads an SM.
+unsigned walkers(int64_t T, int threads, int full) {
+  const int64_t most = static_cast<int64_t>(sm_count()) * (full * kRowThreads / threads < 16 ? full * kRowThreads / threads : 16);
+  return static_cast<unsigned>(T < most ? T : most);
 }
 
 bool vec8(int64_t N, const void* a, const void* b, const void* c = nullptr, const void* d = nullptr) {
@@ -284,7 +360,7 @@ cudaError_t launch_sort(const Id* ids, int64_t R, int32_t E, int32_t* offsets, i
       },
       &done);
   if (e != cudaSuccess) return e;
-  const int C = R <= 4 * kSortThreads ? 1 : kSortCluster;
+  const int C = R <= 8 * kSortThreads ? 1 : kSortCluster;
   const int64_t warps = static_cast<int64_t>(C) * kSortWarps;
   const int64_t per_warp = ((R + warps - 1) / warps + 31) / 32 * 32;
   cudaLaunchConfig_t cfg = {};
@@ -316,11 +392,11 @@ cudaError_t lbq_launch_expert_dispatch(const uint16_t* X, const int32_t* rows, c
   const RouteArgs a = {rows, weights, R, K, topk};
   const unsigned grid = static_cast<unsigned>(T);
   if (vec8(K, X, out)) {
-    if (weights) dispatch_kernel<8, true><<<grid, kRowThreads, 0, s>>>(X, a, out);
-    else dispatch_kernel<8, false><<<grid, kRowThreads, 0, s>>>(X, a, out);
+    if (weights) dispatch_kernel<8, true><<<grid, threads_for(K, 8), 0, s>>>(X, a, out);
+    else dispatch_kernel<8, false><<<grid, threads_for(K, 8), 0, s>>>(X, a, out);
   } else {
-    if (weights) dispatch_kernel<1, true><<<grid, kRowThreads, 0, s>>>(X, a, out);
-    else dispatch_kernel<1, false><<<grid, kRowThreads, 0, s>>>(X, a, out);
+    if (weights) dispatch_kernel<1, true><<<grid, threads_for(K, 1), 0, s>>>(X, a, out);
+    else dispatch_kernel<1, false><<<grid, threads_for(K, 1), 0, s>>>(X, a, out);
   }
   return cudaGetLastError();
 }
@@ -329,13 +405,13 @@ cudaError_t lbq_launch_expert_combine(const uint16_t* Y, const int32_t* rows, co
                                       int64_t T, int32_t topk, int64_t N, int64_t R, uint16_t* out,
                                       cudaStream_t s) {
   const RouteArgs a = {rows, weights, R, N, topk};
-  const unsigned grid = static_cast<unsigned>(T);
+  const unsigned grid = walkers(T, threads_for(N, vec8(N, Y, out) ? 8 : 1), 4);
   if (vec8(N, Y, out)) {
-    if (weights) combine_kernel<8, true><<<grid, kRowThreads, 0, s>>>(Y, a, out);
-    else combine_kernel<8, false><<<grid, kRowThreads, 0, s>>>(Y, a, out);
+    if (weights) combine_kernel<8, true><<<grid, threads_for(N, 8), 0, s>>>(Y, a, T, out);
+    else combine_kernel<8, false><<<grid, threads_for(N, 8), 0, s>>>(Y, a, T, out);
   } else {
-    if (weights) combine_kernel<1, true><<<grid, kRowThreads, 0, s>>>(Y, a, out);
-    else combine_kernel<1, false><<<grid, kRowThreads, 0, s>>>(Y, a, out);
+    if (weights) combine_kernel<1, true><<<grid, threads_for(N, 1), 0, s>>>(Y, a, T, out);
+    else combine_kernel<1, false><<<grid, threads_for(N, 1), 0, s>>>(Y, a, T, out);
   }
   return cudaGetLastError();
 }
@@ -345,10 +421,10 @@ cudaError_t lbq_launch_expert_combine_grad(const uint16_t* dout, const uint16_t*
                                            int32_t topk, int64_t N, int64_t R, uint16_t* dY,
                                            float* dweights, cudaStream_t s) {
   const RouteArgs a = {rows, weights, R, N, topk};
-  const unsigned grid = static_cast<unsigned>(T);
+  const unsigned grid = walkers(T, threads_for(N, vec8(N, dout, Y, dY) ? 8 : 1), 3);
   if (vec8(N, dout, Y, dY))
-    combine_grad_kernel<8><<<grid, kRowThreads, 0, s>>>(dout, Y, a, dY, dweights);
+    combine_grad_kernel<8><<<grid, threads_for(N, 8), 0, s>>>(dout, Y, a, T, dY, dweights);
   else
-    combine_grad_kernel<1><<<grid, kRowThreads, 0, s>>>(dout, Y, a, dY, dweights);
+    combine_grad_kernel<1><<<grid, threads_for(N, 1), 0, s>>>(dout, Y, a, T, dY, dweights);
   return cudaGetLastError();
 }

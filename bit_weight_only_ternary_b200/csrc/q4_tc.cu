@@ -889,7 +889,11 @@ cudaError_t launch(const lbq_weights* w, const Plan& plan, const lbq_expert_rows
   };
   const cuuint64_t G = static_cast<cuuint64_t>(E) * ng, cw = static_cast<cuuint64_t>(w->code_stride),
                    se = static_cast<cuuint64_t>(w->scale_stride) * 4;
+  // (dense: only the boxes of the full and the last token tile are used)
+  const int64_t last = rows - static_cast<int64_t>(plan.ntm - 1) * plan.tile_m;
+  auto box_of = [](int64_t cnt) { return static_cast<int>((((cnt + 15) / 16 * 16) / 2 + kBoxStep - 1) / kBoxStep) - 1; };
   for (int i = 0; i < kBoxes; ++i) {
+    if (!er && i != box_of(plan.tile_m) && i != box_of(last)) continue;
     const cuuint64_t dims[3] = {64, static_cast<cuuint64_t>(rows), static_cast<cuuint64_t>(w->K / 64)};
     const cuuint64_t strides[2] = {static_cast<cuuint64_t>(w->K) * 2, 128};
     const cuuint32_t box[3] = {64, static_cast<cuuint32_t>((i + 1) * kBoxStep), 2};

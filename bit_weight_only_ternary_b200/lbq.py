@@ -110,13 +110,20 @@ def _check(status: int, where: str):
 
 
 def _ptr(t):
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr()
+
+
+def _current_raw_stream() -> int:
+    """The handle of torch's current stream (without building a Stream object, which takes
+    longer than the launch of a small product, where this torch allows it)."""
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    return raw(torch.cuda.current_device()) if raw else torch.cuda.current_stream().cuda_stream
 
 
 def _stream(stream):
     if stream is None:
-        stream = torch.cuda.current_stream()
-    return ctypes.c_void_p(stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream))
+        return _current_raw_stream()
+    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
 def lbq_packed_layout(fmt: int, K: int, N: int):
@@ -338,11 +345,10 @@ def _arg(where: str, t, dtype, shape=None):
     else is refused here (the C call sees pointers only)."""
     if t is None:
         return
-    dtypes = dtype if isinstance(dtype, tuple) else (dtype,)
-    if t.dtype not in dtypes or not t.is_contiguous() or not t.is_cuda \
-            or t.device.index != torch.cuda.current_device():
+    if t.dtype is not dtype or not t.is_cuda or not t.is_contiguous() \
+            or t.get_device() != torch.cuda.current_device():
         _check(LBQ_ERR_ARG, where)
-    if shape is not None and tuple(t.shape) != tuple(shape):
+    if shape is not None and t.shape != shape:
         _check(LBQ_ERR_SHAPE, where)
 
 
@@ -384,14 +390,16 @@ def lbq_expert_sort(expert: torch.Tensor, E: int, offsets=None, rows=None, slots
     int32 [T*topk]): a stable sort of the slots by expert (ids outside 0..E-1 left out)."""
     T, topk = expert.shape
     w = "lbq_expert_sort"
-    _arg(w, expert, (torch.int32, torch.int64))
+    _arg(w, expert, torch.int64 if expert.dtype is torch.int64 else torch.int32)
     _arg(w, offsets, torch.int32, (E + 1,))
     _arg(w, rows, torch.int32, (T, topk))
     _arg(w, slots, torch.int32, (T * topk,))
-    new = lambda *shape: torch.empty(shape, dtype=torch.int32, device=expert.device)  # noqa: E731
-    offsets = new(E + 1) if offsets is None else offsets
-    rows = new(T, topk) if rows is None else rows
-    slots = new(T * topk) if slots is None else slots
+    if offsets is None:
+        offsets = torch.empty(E + 1, dtype=torch.int32, device=expert.device)
+    if rows is None:
+        rows = torch.empty((T, topk), dtype=torch.int32, device=expert.device)
+    if slots is None:
+        slots = torch.empty(T * topk, dtype=torch.int32, device=expert.device)
     _check(_lib.lbq_expert_sort(_ptr(expert), expert.element_size(), T, topk, E, _ptr(offsets),
                                 _ptr(rows), _ptr(slots), _stream(stream)), "lbq_expert_sort")
     return offsets, rows, slots
