@@ -43,9 +43,11 @@ __device__ __forceinline__ unsigned peers_of(int v, int bits) {
 // Shared memory: hist [warps][E], tot [E], base [E].
 template <typename Id>
 __global__ void __launch_bounds__(kSortThreads, 1)
-    expert_sort_kernel(const Id* __restrict__ ids, int64_t R, int E, int64_t per_warp,
+    expert_sort_kernel(const Id* ids, int64_t R, int E, int64_t per_warp,
                        int32_t* __restrict__ offsets, int32_t* __restrict__ rows,
                        int32_t* __restrict__ slots) {
+  pdl_launch_dependents();
+  pdl_wait();
   extern __shared__ int32_t sm[];
   __shared__ int32_t wsum[kSortWarps];
   int32_t* hist = sm;
@@ -190,13 +192,15 @@ struct RouteArgs {
 
 // The row of slot i, or -1 when it names none.
 __device__ __forceinline__ int64_t row_of(const RouteArgs& a, int64_t i) {
-  const int32_t r = __ldg(a.rows + i);
+  const int32_t r = a.rows[i];
   return r >= 0 && r < a.R ? r : -1;
 }
 
 template <int kVec, bool kWeighted>
 __global__ void __launch_bounds__(kRowThreads)
-    dispatch_kernel(const uint16_t* __restrict__ X, const RouteArgs a, uint16_t* __restrict__ out) {
+    dispatch_kernel(const uint16_t* X, const RouteArgs a, uint16_t* out) {
+  pdl_launch_dependents();
+  pdl_wait();
   const int64_t t = blockIdx.x;
   for (int64_t n = static_cast<int64_t>(threadIdx.x) * kVec; n < a.N; n += static_cast<int64_t>(blockDim.x) * kVec) {
     Vec<kVec> v;
@@ -207,7 +211,7 @@ __global__ void __launch_bounds__(kRowThreads)
       const int64_t r = row_of(a, t * a.topk + j);
       if (r < 0) continue;
       if (kWeighted) {
-        const float w = __ldg(a.weights + t * a.topk + j);
+        const float w = a.weights[t * a.topk + j];
         float p[kVec];
 #pragma unroll
         for (int i = 0; i < kVec; ++i) p[i] = w * f[i];
@@ -235,8 +239,8 @@ struct Slots {
 #pragma unroll
     for (int j = 0; j < kSlotsAtOnce; ++j) {
       const bool in = t < T && j0 + j < a.topk;
-      r[j] = in ? __ldg(a.rows + t * a.topk + j0 + j) : -1;
-      w[j] = kWeighted && in ? __ldg(a.weights + t * a.topk + j0 + j) : 1.0f;
+      r[j] = in ? a.rows[t * a.topk + j0 + j] : -1;
+      w[j] = kWeighted && in ? a.weights[t * a.topk + j0 + j] : 1.0f;
       if (r[j] >= a.R) r[j] = -1;
     }
   }
@@ -244,7 +248,9 @@ struct Slots {
 
 template <int kVec, bool kWeighted>
 __global__ void __launch_bounds__(kRowThreads, 4)
-    combine_kernel(const uint16_t* __restrict__ Y, const RouteArgs a, int64_t T, uint16_t* __restrict__ out) {
+    combine_kernel(const uint16_t* Y, const RouteArgs a, int64_t T, uint16_t* out) {
+  pdl_launch_dependents();
+  pdl_wait();
   Slots<kWeighted> next;
   next.load(a, blockIdx.x, T, 0);
   for (int64_t t = blockIdx.x; t < T; t += gridDim.x) {
@@ -277,8 +283,10 @@ __global__ void __launch_bounds__(kRowThreads, 4)
 
 template <int kVec>
 __global__ void __launch_bounds__(kRowThreads, 3)
-    combine_grad_kernel(const uint16_t* __restrict__ dout, const uint16_t* __restrict__ Y,
-                        const RouteArgs a, int64_t T, uint16_t* __restrict__ dY, float* __restrict__ dweights) {
+    combine_grad_kernel(const uint16_t* dout, const uint16_t* Y, const RouteArgs a, int64_t T, uint16_t* dY,
+                        float* dweights) {
+  pdl_launch_dependents();
+  pdl_wait();
   __shared__ float red[2][kRowThreads / 32][kSlotsAtOnce];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = static_cast<int>(blockDim.x) >> 5;
   int buf = 0;
@@ -335,6 +343,21 @@ int threads_for(int64_t N, int vec) {
   return n < kRowThreads ? static_cast<int>(n) : kRowThreads;
 }
 
+// Launches early beside the previous kernel of the stream; the kernels wait for it themselves.
+template <typename... P, typename... A>
+cudaError_t launch_rows(void (*k)(P...), unsigned grid, int threads, cudaStream_t s, A... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(static_cast<unsigned>(threads));
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, k, P(args)...);
+}
+
 // CTAs that walk over T tokens: as many as are resident, at `full` CTAs of kRowThreads an SM.
 unsigned walkers(int64_t T, int threads, int full) {
   const int64_t most = static_cast<int64_t>(sm_count()) * (full * kRowThreads / threads < 16 ? full * kRowThreads / threads : 16);
@@ -368,13 +391,15 @@ cudaError_t launch_sort(const Id* ids, int64_t R, int32_t E, int32_t* offsets, i
   cfg.blockDim = dim3(kSortThreads);
   cfg.dynamicSmemBytes = static_cast<size_t>(kSortWarps + 2) * E * 4;
   cfg.stream = s;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = static_cast<unsigned>(C);
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = static_cast<unsigned>(C);
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = 2;
   return cudaLaunchKernelEx(&cfg, expert_sort_kernel<Id>, ids, R, static_cast<int>(E), per_warp, offsets, rows, slots);
 }
 
@@ -391,29 +416,21 @@ cudaError_t lbq_launch_expert_dispatch(const uint16_t* X, const int32_t* rows, c
                                        cudaStream_t s) {
   const RouteArgs a = {rows, weights, R, K, topk};
   const unsigned grid = static_cast<unsigned>(T);
-  if (vec8(K, X, out)) {
-    if (weights) dispatch_kernel<8, true><<<grid, threads_for(K, 8), 0, s>>>(X, a, out);
-    else dispatch_kernel<8, false><<<grid, threads_for(K, 8), 0, s>>>(X, a, out);
-  } else {
-    if (weights) dispatch_kernel<1, true><<<grid, threads_for(K, 1), 0, s>>>(X, a, out);
-    else dispatch_kernel<1, false><<<grid, threads_for(K, 1), 0, s>>>(X, a, out);
-  }
-  return cudaGetLastError();
+  const bool v8 = vec8(K, X, out);
+  return launch_rows(v8 ? (weights ? dispatch_kernel<8, true> : dispatch_kernel<8, false>)
+                        : (weights ? dispatch_kernel<1, true> : dispatch_kernel<1, false>),
+                     grid, threads_for(K, v8 ? 8 : 1), s, X, a, out);
 }
 
 cudaError_t lbq_launch_expert_combine(const uint16_t* Y, const int32_t* rows, const float* weights,
                                       int64_t T, int32_t topk, int64_t N, int64_t R, uint16_t* out,
                                       cudaStream_t s) {
   const RouteArgs a = {rows, weights, R, N, topk};
-  const unsigned grid = walkers(T, threads_for(N, vec8(N, Y, out) ? 8 : 1), 4);
-  if (vec8(N, Y, out)) {
-    if (weights) combine_kernel<8, true><<<grid, threads_for(N, 8), 0, s>>>(Y, a, T, out);
-    else combine_kernel<8, false><<<grid, threads_for(N, 8), 0, s>>>(Y, a, T, out);
-  } else {
-    if (weights) combine_kernel<1, true><<<grid, threads_for(N, 1), 0, s>>>(Y, a, T, out);
-    else combine_kernel<1, false><<<grid, threads_for(N, 1), 0, s>>>(Y, a, T, out);
-  }
-  return cudaGetLastError();
+  const bool v8 = vec8(N, Y, out);
+  const int threads = threads_for(N, v8 ? 8 : 1);
+  return launch_rows(v8 ? (weights ? combine_kernel<8, true> : combine_kernel<8, false>)
+                        : (weights ? combine_kernel<1, true> : combine_kernel<1, false>),
+                     walkers(T, threads, 4), threads, s, Y, a, T, out);
 }
 
 cudaError_t lbq_launch_expert_combine_grad(const uint16_t* dout, const uint16_t* Y,
@@ -421,10 +438,8 @@ cudaError_t lbq_launch_expert_combine_grad(const uint16_t* dout, const uint16_t*
                                            int32_t topk, int64_t N, int64_t R, uint16_t* dY,
                                            float* dweights, cudaStream_t s) {
   const RouteArgs a = {rows, weights, R, N, topk};
-  const unsigned grid = walkers(T, threads_for(N, vec8(N, dout, Y, dY) ? 8 : 1), 3);
-  if (vec8(N, dout, Y, dY))
-    combine_grad_kernel<8><<<grid, threads_for(N, 8), 0, s>>>(dout, Y, a, T, dY, dweights);
-  else
-    combine_grad_kernel<1><<<grid, threads_for(N, 1), 0, s>>>(dout, Y, a, T, dY, dweights);
-  return cudaGetLastError();
+  const bool v8 = vec8(N, dout, Y, dY);
+  const int threads = threads_for(N, v8 ? 8 : 1);
+  return launch_rows(v8 ? combine_grad_kernel<8> : combine_grad_kernel<1>, walkers(T, threads, 3), threads, s, dout,
+                     Y, a, T, dY, dweights);
 }

@@ -70,7 +70,7 @@ constexpr uint32_t kOffRed = kOffInfo + kInfos * kInfoBytes;  // [512] floats
 constexpr uint32_t kOffPre = kOffRed + kDec * 4;                   // [E + 1] tiles before expert e
 constexpr uint32_t kOffFirst = kOffPre + (LBQ_MAX_EXPERTS + 2) * 4;  // [E + 1] offsets, clamped
 constexpr uint32_t kOffBar = kOffFirst + (LBQ_MAX_EXPERTS + 2) * 4;
-constexpr uint32_t kBarBytes = 8 * (2 * kStages + 2 * kRawStages + 2 * kInfos + 2) + 8;  // and the TMEM slot
+constexpr uint32_t kBarBytes = 8 * (2 * kStages + 2 * kRawStages + 2 * kInfos + 3) + 8;  // and the TMEM slot
 constexpr uint32_t kSmem = kOffBar + kBarBytes + 1024;
 static_assert(kSmem <= 232448, "over the shared-memory limit");
 constexpr unsigned kFaultX = 14, kFaultMma = 15, kFaultW = 16, kFaultDecode = 17, kFaultEpilogue = 18;
@@ -114,12 +114,13 @@ __device__ __forceinline__ int clamp_row(int v, int R) { return v < 0 ? 0 : (v >
 // blocks). The blocks behind take groups of four weight rows, one a warp: the exponent
 // that brings a row's largest scale to [2^11, 2^12).
 template <int kRow>
-__global__ void __launch_bounds__(256)
+__global__ void __launch_bounds__(256, 8)
     q4_prepare_kernel(const Args a, uint16_t* __restrict__ Xh, int* __restrict__ xexp,
                       int* __restrict__ xflag, int* __restrict__ wexp, int ngroups, int group) {
   pdl_launch_dependents();
+  pdl_wait();
   constexpr int kRows = 256 / kRow;  // rows a block
-  __shared__ float red[8];
+  __shared__ uint2 red[8];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int64_t xblocks = (static_cast<int64_t>(a.M) + kRows - 1) / kRows;
   if (static_cast<int64_t>(blockIdx.x) >= xblocks) {
@@ -165,49 +166,68 @@ __global__ void __launch_bounds__(256)
   const uint4* xr = reinterpret_cast<const uint4*>(a.X + src * a.K);
   auto lo = [](uint32_t w) { return __uint_as_float(w << 16); };
   auto hi = [](uint32_t w) { return __uint_as_float(w & 0xffff0000u); };
-  uint32_t mb = 0;  // largest magnitude, as bf16 bits in both halves
-#pragma unroll 8
-  for (int k = u; k < K8; k += kRow) {
-    const uint4 v = xr[k];
-    mb = __vmaxu2(mb, __vmaxu2(__vmaxu2(v.x & 0x7fff7fffu, v.y & 0x7fff7fffu),
-                               __vmaxu2(v.z & 0x7fff7fffu, v.w & 0x7fff7fffu)));
-  }
-  float mx = fmaxf(lo(mb), hi(mb));
+  // the row's first kKeep x kRow vectors stay in registers, what is behind is read twice
+  constexpr int kKeep = 2;
+  uint4 kept[kKeep];
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+  for (int i = 0; i < kKeep; ++i) kept[i] = u + i * kRow < K8 ? xr[u + i * kRow] : make_uint4(0, 0, 0, 0);
+  // largest and smallest non-zero magnitude, as bf16 bits in both halves (the smallest less
+  // one, so that zeros come last; a zero low half borrows one more from the high half, which
+  // only makes the row's flag more careful)
+  uint32_t mb = 0, sb = 0xffffffffu;
+  auto largest = [&](const uint4& v) {
+    const uint32_t w[4] = {v.x & 0x7fff7fffu, v.y & 0x7fff7fffu, v.z & 0x7fff7fffu, v.w & 0x7fff7fffu};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      mb = __vmaxu2(mb, w[i]);
+      sb = __vminu2(sb, w[i] - 0x00010001u);
+    }
+  };
+#pragma unroll
+  for (int i = 0; i < kKeep; ++i) largest(kept[i]);
+#pragma unroll 4
+  for (int k = u + kKeep * kRow; k < K8; k += kRow) largest(xr[k]);
+  uint32_t mag = max(mb & 0xffffu, mb >> 16), small = min(sb & 0xffffu, sb >> 16);
+  mag = __reduce_max_sync(0xffffffffu, mag);
+  small = __reduce_min_sync(0xffffffffu, small);
   if (kRow == 256) {
-    if (lane == 0) red[warp] = mx;
+    if (lane == 0) red[warp] = make_uint2(mag, small);
     __syncthreads();
-    mx = red[0];
-    for (int i = 1; i < 8; ++i) mx = fmaxf(mx, red[i]);
+    for (int i = 0; i < 8; ++i) {
+      mag = max(mag, red[i].x);
+      small = min(small, red[i].y);
+    }
   }
-  const int e = mx > 0.0f ? ilogbf(mx) - 14 : 0;  // max |x| 2^-e in [2^14, 2^15)
-  bool inexact = false;
-  auto pack = [&inexact](float a0, float a1) {
-    const __half h0 = __float2half_rn(a0), h1 = __float2half_rn(a1);
-    inexact = inexact || __half2float(h0) != a0 || __half2float(h1) != a1;
-    return static_cast<uint32_t>(__half_as_ushort(h0)) | (static_cast<uint32_t>(__half_as_ushort(h1)) << 16);
+  const float mx = __uint_as_float(mag << 16);
+  const int e = mag == 0 ? 0 : ilogbf(mx) - 14;  // max |x| 2^-e in [2^14, 2^15)
+  // fp16 holds a bf16 value of 2^-17 or more exactly (its last bit is then at least fp16's
+  // smallest step, 2^-24): a row is flagged when its smallest value, 31 powers of two below
+  // the largest, may not be (or when it has NaN or Inf)
+  const bool inexact = mag >= 0x7f80u || (small != 0xffffu && ilogbf(__uint_as_float((small + 1u) << 16)) - e < -17);
+  auto pack = [](float a0, float a1) {
+    const __half2 h = __floats2half2_rn(a0, a1);
+    return *reinterpret_cast<const uint32_t*>(&h);
+  };
+  auto convert = [&](auto scale) {
+    auto put = [&](int k, const uint4& v) {
+      hr[k] = make_uint4(pack(scale(lo(v.x)), scale(hi(v.x))), pack(scale(lo(v.y)), scale(hi(v.y))),
+                         pack(scale(lo(v.z)), scale(hi(v.z))), pack(scale(lo(v.w)), scale(hi(v.w))));
+    };
+#pragma unroll
+    for (int i = 0; i < kKeep; ++i)
+      if (u + i * kRow < K8) put(u + i * kRow, kept[i]);
+#pragma unroll 2
+    for (int k = u + kKeep * kRow; k < K8; k += kRow) put(k, xr[k]);
   };
   if (-e >= -126 && -e <= 127) {
     const float f = __int_as_float((127 - e) << 23);
-#pragma unroll 4
-    for (int k = u; k < K8; k += kRow) {
-      const uint4 v = xr[k];
-      hr[k] = make_uint4(pack(lo(v.x) * f, hi(v.x) * f), pack(lo(v.y) * f, hi(v.y) * f),
-                         pack(lo(v.z) * f, hi(v.z) * f), pack(lo(v.w) * f, hi(v.w) * f));
-    }
+    convert([f](float x) { return x * f; });
   } else {
-    for (int k = u; k < K8; k += kRow) {
-      const uint4 v = xr[k];
-      auto sc = [&](float x) { return ldexpf(x, -e); };
-      hr[k] = make_uint4(pack(sc(lo(v.x)), sc(hi(v.x))), pack(sc(lo(v.y)), sc(hi(v.y))),
-                         pack(sc(lo(v.z)), sc(hi(v.z))), pack(sc(lo(v.w)), sc(hi(v.w))));
-    }
+    convert([e](float x) { return ldexpf(x, -e); });
   }
-  const bool any = kRow == 256 ? __syncthreads_or(inexact ? 1 : 0) != 0 : __any_sync(0xffffffffu, inexact);
   if (u == 0) {
     xexp[m] = e;
-    xflag[m] = any ? 1 : 0;
+    xflag[m] = inexact ? 1 : 0;
   }
 }
 
@@ -260,7 +280,9 @@ __device__ __forceinline__ Tile tile_at(const Args& a, const int* pre, const int
 // (an instruction on the previous one's accumulator waits for it; small ones are shorter
 // than that wait).
 __device__ __forceinline__ int mma_n(int cnt) { return cnt <= 16 ? 16 : (cnt + 15) / 16 * 16; }
-__device__ __forceinline__ int accs_for(int n) { return n > 128 ? 1 : (n > 64 ? 2 : (n > 32 ? 4 : 8)); }
+__device__ __forceinline__ int accs_for(int n) {
+  return n > 128 ? 1 : (n > 64 ? 2 : (n > 32 ? 4 : 8));
+}
 
 __device__ __forceinline__ uint64_t sw128_desc(uint32_t saddr) {
   uint64_t d = static_cast<uint64_t>((saddr >> 4) & 0x3FFFu);
@@ -284,19 +306,6 @@ __device__ __forceinline__ uint32_t lds16(uint32_t addr) {
   asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(addr));
   return v;
 }
-__device__ __forceinline__ bool named_bar_or(uint32_t id, uint32_t count, bool v) {
-  uint32_t r;
-  asm volatile(
-      "{\n\t.reg .pred p, q;\n\t"
-      "setp.ne.u32 p, %1, 0;\n\t"
-      "bar.red.or.pred q, %2, %3, p;\n\t"
-      "selp.u32 %0, 1, 0, q;\n\t}"
-      : "=r"(r)
-      : "r"(v ? 1u : 0u), "r"(id), "r"(count)
-      : "memory");
-  return r != 0;
-}
-
 __device__ __forceinline__ uint32_t and_or(uint32_t a, uint32_t b, uint32_t c) {
   uint32_t d;
   asm("lop3.b32 %0, %1, %2, %3, 0xea;" : "=r"(d) : "r"(a), "r"(b), "r"(c));  // (a & b) | c
@@ -324,10 +333,10 @@ __device__ __forceinline__ void decode_word(uint32_t w, __half2 s, uint32_t* out
 
 // fp32 recomputation of a tile's flagged tokens by all decoder threads d (four a weight
 // row, each every fourth block of K); put(token, row, value) on threads d < kTileN. The
-// control flow depends on shared data only, so every thread meets every barrier.
-template <int kG, typename Put>
+// flags are shared, so every warp comes to every meeting (a bounded wait, like all).
+template <int kG, typename Meet, typename Put>
 __device__ __forceinline__ void fixup_flagged(const Args& a, const Tile& t, const int* xf, float* red,
-                                              int d, Put put) {
+                                              int d, Meet meet, Put put) {
   const int row = d & (kTileN - 1), qtr = d / kTileN, n = t.n0 + row;
   const int64_t grow = static_cast<int64_t>(t.e) * a.groups * 4 + n;
   for (int i = 0; i < t.cnt; ++i) {
@@ -354,10 +363,10 @@ __device__ __forceinline__ void fixup_flagged(const Args& a, const Tile& t, cons
       }
     }
     red[qtr * kTileN + row] = acc;
-    named_bar_sync(3, kDec);
+    meet();
     if (d < kTileN && n < a.N)
       put(i, row, ((red[row] + red[kTileN + row]) + red[2 * kTileN + row]) + red[3 * kTileN + row]);
-    named_bar_sync(3, kDec);
+    meet();
   }
 }
 
@@ -378,7 +387,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t bars = base + kOffBar;
   const uint32_t full = bars, empty = full + 8 * kStages, fullR = empty + 8 * kStages,
                  emptyR = fullR + 8 * kRawStages, accum = emptyR + 8 * kRawStages, dfree = accum + 8,
-                 fullI = dfree + 8, emptyI = fullI + 8 * kInfos, tslot = emptyI + 8 * kInfos;
+                 meet = dfree + 8, fullI = meet + 8, emptyI = fullI + 8 * kInfos, tslot = emptyI + 8 * kInfos;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (tid == 0) {
     for (int s = 0; s < kStages; ++s) {
@@ -396,6 +405,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     mbar_init(accum, 1);
     mbar_init(dfree, 2 * kDec / 32);
+    mbar_init(meet, kDec / 32);
     fence_mbar_init();
   }
   if (warp == 1) tmem_alloc_pair(tslot, kTmemCols);
@@ -481,7 +491,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int n = mma_n(t.cnt), nacc = accs_for(n);
         const uint32_t idesc = idesc_f16_m256(n);
         const uint32_t half_k = static_cast<uint32_t>((n / 2 + kBoxStep - 1) / kBoxStep) * (kBoxStep * 128 >> 4);
-        // the accumulators are free once the previous tile's have been read
+        // the accumulators are free once their previous tile's have been read
         ok = mbar_wait(dfree, (nt & 1) ^ 1, a.fault, kFaultMma);
         for (int kb = 0; kb < (t.nkb + 1) / 2 * 2; ++kb, ++blk) {
           const uint32_t s = blk % kStages;
@@ -585,6 +595,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                              2u * (row & 3) + 8u * kScales * (grp & 1);
     bool ok = true;
     uint32_t done_tiles = 0;  // epilogues finished
+    uint32_t meetings = 0;    // of the decoder warps
+    auto meeting = [&]() {
+      __syncwarp();
+      if (lane == 0) mbar_arrive(meet);
+      if (ok) ok = mbar_wait(meet, meetings & 1, a.fault, kFaultEpilogue);
+      __syncwarp();
+      ++meetings;
+    };
 
     auto epilogue = [&](const Tile& t) {
       const int n = mma_n(t.cnt), nacc = accs_for(n);
@@ -596,8 +614,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int* xf = xe + kMaxTileM;
       const float* xs = reinterpret_cast<const float*>(xf + kMaxTileM);
       if (ok) ok = mbar_wait(fullI + 8 * si, (done_tiles / kInfos) & 1, a.fault, kFaultEpilogue);
-      // (one answer for all: the recomputation below has barriers)
-      const bool special = named_bar_or(3, kDec, ok && xe[3 * kMaxTileM] != 0);
+      const bool special = ok && xe[3 * kMaxTileM] != 0;
       if (ok) ok = mbar_wait(accum, done_tiles & 1, a.fault, kFaultEpilogue);
       __syncwarp();
       tc_fence_after_sync();
@@ -667,7 +684,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         release();
         if (special)
-          fixup_flagged<kG>(a, t, xf, red, d, [&](int m, int r, float y) {
+          fixup_flagged<kG>(a, t, xf, red, d, meeting, [&](int m, int r, float y) {
             if (!ok) return;
             const int64_t o = static_cast<int64_t>(t.m0 + m) * a.N + t.n0 + r;
             if (part) part[o] = y;
@@ -782,14 +799,27 @@ struct Plan {
   int tile_m, ntm, splits, kb_split;
 };
 
-// Dense: equal token tiles; K is split when the tiles alone leave SMs idle.
+// Dense: how many token tiles, and whether K is split. Modelled time: rounds of tiles over
+// the pairs of SMs, each a fixed part (start, epilogue: some 4 us) and its blocks; a block
+// of 128 K takes about 0.3 us + 1.4 ns a token (measured: 0.33 us at 32 tokens, 0.42 at
+// 128, 0.66 at 256). K is split only when all tiles leave half of the pairs idle.
 Plan plan_for(const lbq_weights* w, int64_t M) {
-  Plan p;
-  p.ntm = static_cast<int>((M + kMaxTileM - 1) / kMaxTileM);
-  p.tile_m = static_cast<int>((M + p.ntm - 1) / p.ntm + 15) / 16 * 16;
-  p.ntm = static_cast<int>((M + p.tile_m - 1) / p.tile_m);
-  const int64_t tiles = (w->N + 2 * kTileN - 1) / (2 * kTileN) * p.ntm, pairs = sm_count() / 2;
+  Plan p = {};
+  const int64_t ntn = (w->N + 2 * kTileN - 1) / (2 * kTileN), pairs = sm_count() / 2;
   const int nkb = static_cast<int>(w->K / kTileK);
+  const int64_t least = (M + kMaxTileM - 1) / kMaxTileM;
+  double best = 0.0;
+  for (int64_t nt = least; nt <= 4 * least && nt <= (M + 15) / 16; ++nt) {
+    const int64_t rows = ((M + nt - 1) / nt + 15) / 16 * 16, tiles = (M + rows - 1) / rows;
+    const double cost = static_cast<double>((tiles * ntn + pairs - 1) / pairs) *
+                        (4.0 + nkb * (0.3 + 0.0014 * static_cast<double>(rows)));
+    if (nt == least || cost < best) {
+      best = cost;
+      p.tile_m = static_cast<int>(rows);
+      p.ntm = static_cast<int>(tiles);
+    }
+  }
+  const int64_t tiles = ntn * p.ntm;
   int splits = tiles < pairs ? static_cast<int>(pairs / tiles) : 1;
   const int most = (nkb + 3) / 4;  // at least four blocks each
   if (splits > most) splits = most;
@@ -912,23 +942,25 @@ cudaError_t launch(const lbq_weights* w, const Plan& plan, const lbq_expert_rows
   a.kb_split = plan.kb_split;
   const unsigned wblocks = static_cast<unsigned>((static_cast<int64_t>(E) * ng + 7) / 8);
   const int ngroups = static_cast<int>(E * ng);
-  if (rows >= 8 * sm_count())  // enough rows for every SM at eight a block
-    q4_prepare_kernel<32><<<static_cast<unsigned>((rows + 7) / 8) + wblocks, 256, 0, s>>>(a, Xh, xexp, xflag, wexp, ngroups, kG);
-  else
-    q4_prepare_kernel<256><<<static_cast<unsigned>(rows) + wblocks, 256, 0, s>>>(a, Xh, xexp, xflag, wexp, ngroups, kG);
-  e = cudaGetLastError();
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  const bool many = rows >= 8 * sm_count();  // enough rows for every SM at eight a block
+  cfg.gridDim = dim3(static_cast<unsigned>(many ? (rows + 7) / 8 : rows) + wblocks);
+  cfg.blockDim = dim3(256);
+  cfg.stream = s;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  e = cudaLaunchKernelEx(&cfg, many ? q4_prepare_kernel<32> : q4_prepare_kernel<256>, a, Xh, xexp, xflag, wexp, ngroups, kG);
   if (e != cudaSuccess) return e;
   const int64_t ntn = (w->N + 2 * kTileN - 1) / (2 * kTileN), pairs = sm_count() / 2;
   // experts: at most rows / 256 + E token tiles
   const int64_t most = er ? (rows / kMaxTileM + E) * ntn : static_cast<int64_t>(plan.ntm) * ntn * plan.splits;
-  cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(2 * static_cast<unsigned>(most < pairs ? most : pairs));
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = kSmem;
   cfg.stream = s;
-  cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
   attr[1].id = cudaLaunchAttributeClusterDimension;
   attr[1].val.clusterDim.x = 2;
   attr[1].val.clusterDim.y = 1;

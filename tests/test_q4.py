@@ -106,7 +106,15 @@ def test_q4_refusals(L):
     assert gemv(desc(), ctypes.c_void_p(0x20008)) == L.LBQ_ERR_ALIGN
     assert gemv(desc(), x, ctypes.c_void_p(0x30001)) == L.LBQ_ERR_ALIGN
     assert lib.lbq_gemm(desc(), x, 0, None, y, None, 0, None) == L.LBQ_ERR_SHAPE
-    assert lib.lbq_gemv_f32(desc(), x, None, ctypes.c_void_p(0x30002), None, 0, None) == L.LBQ_ERR_ALIGN
+    ws = ctypes.c_void_p(0x40000)
+    assert lib.lbq_gemv_f32(desc(), x, None, ctypes.c_void_p(0x30002), ws, 1 << 24, None) == L.LBQ_ERR_ALIGN
+    need = lib.lbq_workspace_bytes(desc(), 1)
+    assert need >= 65536 and gemv(desc()) == L.LBQ_ERR_WORKSPACE
+    assert lib.lbq_gemv(desc(), x, None, y, ws, need - 1, None) == L.LBQ_ERR_WORKSPACE
+    assert lib.lbq_gemv(desc(), x, None, y, ctypes.c_void_p(0x40008), need, None) == L.LBQ_ERR_ALIGN
+    for M in (2, 16, 17, 300):
+        need = lib.lbq_workspace_bytes(desc(), M)
+        assert lib.lbq_gemm(desc(), x, M, None, y, ws, need - 1, None) == L.LBQ_ERR_WORKSPACE
     assert lib.lbq_gemv_noalloc(desc(scales=None), x, None, y, None) == L.LBQ_ERR_ARG
     W = ctypes.c_void_p(0x70000)
     assert lib.lbq_pack(5, W, 512, 4, ctypes.c_void_p(0x10000), None, None) == L.LBQ_ERR_ARG
