@@ -1,5 +1,6 @@
 // q4_gemv.cu -- 4-bit products of few tokens: y[m][n] = sum_k s[n][k/g] (q[n][k] - 8) x[m][k],
-// for a list of products (one token), one matrix and a few tokens, or a matrix per expert. Bound: the bytes of the packed weights, with the decoding close behind.
+// for a list of products (one token), one matrix and a few tokens, or a matrix per expert.
+// Bound: the bytes of the packed weights, with the decoding close behind.
 //
 // Work. A tile is 32 weight rows (eight groups of four) x up to 8 tokens over all of K;
 // its chunks are 128 of K (2 KB of codes). All tiles' chunks lie in one line, cut into
@@ -550,9 +551,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (threadIdx.x < 32) {  // tiles before each expert: a running sum, 32 experts at a time
     const int lane = threadIdx.x, ntn = (a.N + kRowTile - 1) / kRowTile;
     int run = 0;
+    bool down = false;
     for (int e0 = 0; e0 < E; e0 += 32) {
       const int e = e0 + lane, rows = e < E ? off[e + 1] - off[e] : 0;
       const int c = rows > 0 ? (rows + kTok - 1) / kTok * ntn : 0;
+      down = down || rows < 0;
       int inc = c;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
@@ -562,7 +565,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (e < E) pre[e] = run + inc - c;
       run += __shfl_sync(0xffffffffu, inc, 31);
     }
-    if (lane == 0) pre[E] = run;
+    // Offsets that descend somewhere would name rows twice, and more tiles than are counted
+    // in 32 bits: no row then.
+    down = __any_sync(0xffffffffu, down);
+    if (lane == 0) pre[E] = down ? 0 : run;
   }
   __syncthreads();
   if (pre[E] == 0) return;

@@ -199,7 +199,8 @@ __global__ void __launch_bounds__(256, 8)
     }
   }
   const float mx = __uint_as_float(mag << 16);
-  const int e = mag == 0 ? 0 : ilogbf(mx) - 14;  // max |x| 2^-e in [2^14, 2^15)
+  // max |x| 2^-e in [2^14, 2^15); a row of zeros, or with NaN or Inf (flagged below), as it is
+  const int e = mag == 0 || mag >= 0x7f80u ? 0 : ilogbf(mx) - 14;
   // fp16 holds a bf16 value of 2^-17 or more exactly (its last bit is then at least fp16's
   // smallest step, 2^-24): a row is flagged when its smallest value, 31 powers of two below
   // the largest, may not be (or when it has NaN or Inf)
@@ -416,6 +417,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (a.offsets) {  // tiles before each expert (warp 0: a running sum, 32 experts at a time)
     if (warp == 0) {
       int run = 0;
+      bool down = false;
       for (int e0 = 0; e0 < a.E; e0 += 32) {
         const int e = e0 + lane;
         int c = 0;
@@ -425,6 +427,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           off[e] = r0;
           if (e == a.E - 1) off[a.E] = r1;
           c = rows > 0 ? tiles_for(rows) * ntn : 0;
+          down = down || rows < 0;
         }
         int inc = c;
 #pragma unroll
@@ -435,7 +438,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (e < a.E) pre[e] = run + inc - c;
         run += __shfl_sync(0xffffffffu, inc, 31);
       }
-      if (lane == 0) pre[a.E] = run;
+      // offsets that descend somewhere would name rows twice, and more tiles than are
+      // counted in 32 bits: no row then
+      down = __any_sync(0xffffffffu, down);
+      if (lane == 0) pre[a.E] = down ? 0 : run;
     }
   }
   tc_fence_before_sync();

@@ -488,6 +488,9 @@ def lbq_expert_gemm(ew: ExpertWeights, X: torch.Tensor, offsets: torch.Tensor, s
     _arg(w, offsets, torch.int32, (ew.E + 1,))
     _arg(w, slots, torch.int32, (R,))
     _arg(w, Y, torch.bfloat16, (R, ew.N))
+    dev = X.get_device()
+    if ew.codes.get_device() != dev or (workspace is not None and workspace.get_device() != dev):
+        _check(LBQ_ERR_ARG, w)
     if Y is None:
         Y = torch.empty((R, ew.N), dtype=torch.bfloat16, device=X.device)
     if workspace is None:

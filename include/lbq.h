@@ -359,7 +359,8 @@ size_t lbq_expert_workspace_bytes(const lbq_weights* w, int32_t E, int64_t R);
  * points to expert 0's codes and scales; expert e's lie e * ceil(N/4) * 4 * code_stride
  * bytes of codes and e * ceil(N/4) * 4 * scale_stride scales behind them. offsets and
  * slots are read on the device: the call needs no host copy of the routing, so it can be
- * captured; offsets are clamped to 0 .. R and a slot of no token gives a row of zeros.
+ * captured; offsets are clamped to 0 .. R, offsets that descend anywhere leave all of Y
+ * as it was, and a slot of no token gives a row of zeros.
  * Workspace as lbq_expert_workspace_bytes; calls sharing one must not overlap. Each sum
  * is fp32, rounded to bf16 once.
  * Errors: those of lbq_gemv, LBQ_ERR_SHAPE (E, T, R or topk out of range). */

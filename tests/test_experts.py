@@ -363,3 +363,102 @@ def test_python_refuses_what_the_c_call_cannot_see(L):
                 lambda: L.lbq_expert_combine(X.cpu(), rows), lambda: L.lbq_expert_sort(rows.float(), 4)):
         with pytest.raises(L.LbqError):
             bad()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T", [8, 400])
+def test_descending_offsets_compute_no_row(L, orc, T):
+    """Ranges that would overlap (the rows 0 .. T of two experts) are not computed at all."""
+    E, N, K = 3, 40, 256
+    ew, _ = _experts(L, orc, 6, E, N, K, 91)
+    X = synth.activations(T, K, 3).cuda()
+    Y = torch.full((T, N), 7.0, dtype=torch.bfloat16, device="cuda")
+    for off in ([0, T, 0, T], [0, T, T, T - 1], [T // 2, T // 4, T, T]):
+        L.lbq_expert_gemm(ew, X, torch.tensor(off, dtype=torch.int32, device="cuda"), Y=Y)
+        assert (Y == 7).all(), off
+    L.lbq_expert_gemm(ew, X, torch.tensor([1, 1, T - 1, T - 1], dtype=torch.int32, device="cuda"), Y=Y)
+    assert (Y[0] == 7).all() and (Y[T - 1] == 7).all() and not (Y[1:T - 1] == 7).all(1).any()
+    assert L.lbq_device_fault() == 0
+
+
+@pytest.mark.gpu
+def test_weights_or_workspace_on_the_host_are_refused(L, orc):
+    import dataclasses
+    E, N, K, T = 2, 8, 128, 4
+    ew, _ = _experts(L, orc, 6, E, N, K, 92)
+    X = synth.activations(T, K, 3).cuda()
+    off = torch.tensor([0, 2, 4], dtype=torch.int32, device="cuda")
+    ws = L.workspace_for_experts(ew, T)
+    for e, w in ((dataclasses.replace(ew, codes=ew.codes.cpu()), ws), (ew, ws.cpu())):
+        with pytest.raises(L.LbqError):
+            L.lbq_expert_gemm(e, X, off, workspace=w)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T", [4, 200])
+def test_values_that_are_not_finite_stay_in_their_rows(L, orc, T):
+    """A token with NaN or infinities makes its own rows so, and no other: in the experts'
+    products, and in the sums over rows."""
+    E, topk, N, K = 4, 2, 70, 384
+    ew, dense = _experts(L, orc, 5, E, N, K, 93)
+    X = synth.activations(T, K, 4).cuda()
+    ids = _ids(T, topk, E, 5, 0.0).cuda()
+    offsets, rows, slots = L.lbq_expert_sort(ids, E)
+    good = L.lbq_expert_gemm(ew, X, offsets, slots=slots, topk=topk)
+    X[1, 7], X[2, 100] = float("nan"), float("inf")
+    bad = L.lbq_expert_gemm(ew, X, offsets, slots=slots, topk=topk)
+    hit = torch.zeros(T * topk, dtype=torch.bool, device="cuda")
+    hit[rows[1].long()] = True
+    assert bad[hit].isnan().all()
+    for j in range(topk):  # infinity times a weight of zero is NaN, else infinity
+        w = dense[int(ids[2, j])][:, 100]
+        y = bad[rows[2, j]].float()
+        assert torch.equal(y.isnan(), w == 0) and torch.equal(y[w != 0], torch.sign(w[w != 0]).float() * float("inf"))
+    hit[rows[2].long()] = True
+    assert torch.equal(bad[~hit], good[~hit])
+    out = L.lbq_expert_combine(bad, rows)
+    keep = [t for t in range(T) if t not in (1, 2)]
+    assert out[keep].isfinite().all() and out[1].isnan().all()
+    assert L.lbq_device_fault() == 0
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T", [6, 300])
+def test_two_streams_and_two_graphs_at_once(L, orc, T):
+    """Two layers' products in flight together, each with its own workspace, eager and as
+    graphs captured apart, give what they give alone."""
+    E, topk, N, K = 8, 2, 200, 512
+    ids = _ids(T, topk, E, 6, 0.1).cuda()
+    offsets, rows, slots = L.lbq_expert_sort(ids, E)
+    kept = int(offsets[-1])
+    sets = []
+    for i in range(2):
+        ew, _ = _experts(L, orc, 5 + i, E, N, K, 94 + i)
+        X = synth.activations(T, K, 7 + i).cuda()
+        Y = torch.zeros(T * topk, N, dtype=torch.bfloat16, device="cuda")
+        ws = L.workspace_for_experts(ew, T * topk)
+        sets.append((ew, X, Y, ws, L.lbq_expert_gemm(ew, X, offsets, slots=slots, topk=topk)[:kept].clone()))
+    torch.cuda.synchronize()
+
+    def run(i):
+        ew, X, Y, ws, _ = sets[i]
+        L.lbq_expert_gemm(ew, X, offsets, slots=slots, topk=topk, Y=Y, workspace=ws)
+
+    streams, graphs = [torch.cuda.Stream() for _ in range(2)], []
+    for i in range(2):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            run(i)
+        graphs.append(g)
+    for play in (run, lambda i: graphs[i].replay()):
+        for s in sets:
+            s[2].zero_()
+        torch.cuda.synchronize()
+        for _ in range(5):
+            for i in range(2):
+                with torch.cuda.stream(streams[i]):
+                    play(i)
+        torch.cuda.synchronize()
+        for s in sets:
+            assert torch.equal(s[2][:kept], s[4])
+    assert L.lbq_device_fault() == 0
