@@ -63,8 +63,19 @@ constexpr uint32_t kTmemCols = 512, kTmemA = 256;
 constexpr uint32_t kOffSlab = 0;
 constexpr uint32_t kOffRaw = kOffSlab + kStages * 2 * kSlabBytes;
 constexpr uint32_t kOffScale = kOffRaw + kRawStages * kRawBytes;
-constexpr int kInfos = 2;  // tiles whose tokens' exponents are in shared memory
-constexpr uint32_t kInfoBytes = (3 * kMaxTileM + 4) * 4;  // exponents, flags, 2^exponent; special
+// Tiles that are known in shared memory, found by a warp that walks ahead: (found by every
+// decoder warp itself, a tile of experts cost some 1500 of 23000 cycles twice). Of each, in
+// words: 2^exponent of its tokens; exponent * 2 + flag of its tokens; its weight rows'
+// exponents; then the fields of Info.
+constexpr int kInfos = 4;
+constexpr int kInfoExp = kMaxTileM, kInfoRow = 2 * kMaxTileM, kInfoFields = 2 * kMaxTileM + kTileN;
+struct Info {
+  int m0, cnt, n0;  // as in Tile
+  int row0;         // the CTA's first weight row among all matrices'
+  int nkb, kb0, split;
+  int special;      // some token is flagged, or two powers of two cannot be multiplied into one normal float
+};
+constexpr uint32_t kInfoBytes = kInfoFields * 4 + sizeof(Info);
 constexpr uint32_t kOffInfo = kOffScale + kRawStages * kScaleStage;
 constexpr uint32_t kOffRed = kOffInfo + kInfos * kInfoBytes;  // [512] floats
 constexpr uint32_t kOffPre = kOffRed + kDec * 4;                   // [E + 1] tiles before expert e
@@ -336,12 +347,12 @@ __device__ __forceinline__ void decode_word(uint32_t w, __half2 s, uint32_t* out
 // row, each every fourth block of K); put(token, row, value) on threads d < kTileN. The
 // flags are shared, so every warp comes to every meeting (a bounded wait, like all).
 template <int kG, typename Meet, typename Put>
-__device__ __forceinline__ void fixup_flagged(const Args& a, const Tile& t, const int* xf, float* red,
+__device__ __forceinline__ void fixup_flagged(const Args& a, const Info& t, const int* xe, float* red,
                                               int d, Meet meet, Put put) {
   const int row = d & (kTileN - 1), qtr = d / kTileN, n = t.n0 + row;
-  const int64_t grow = static_cast<int64_t>(t.e) * a.groups * 4 + n;
+  const int64_t grow = t.row0 + row;
   for (int i = 0; i < t.cnt; ++i) {
-    if (!xf[i]) continue;
+    if (!(xe[i] & 1)) continue;
     const int64_t src = a.offsets ? source_row(a.slots, a.topk, a.T, t.m0 + i) : t.m0 + i;
     float acc = 0.0f;
     if (n < a.N && src >= 0) {
@@ -551,39 +562,41 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_wait(fullR + 8 * (q % kRawStages), (q / kRawStages) & 1, a.fault, kFaultW, false);
     }
   } else if (warp == 3) {
-    // ---------------- the tiles' tokens' exponents and flags, ahead of the epilogues
+    // ---------------- what the decoders have to know of the tiles
     uint32_t k = 0;
     for (int i = first; i < total; i += step, ++k) {
       const Tile t = tile_at(a, pre, off, ntn, rank, i);
+      const int row0 = t.e * a.groups * 4 + t.n0;
       const uint32_t s = k % kInfos;
-      int* xe = reinterpret_cast<int*>(sp + kOffInfo + s * kInfoBytes);
-      int e[kMaxTileM / 32], f[kMaxTileM / 32];
+      int* info = reinterpret_cast<int*>(sp + kOffInfo + s * kInfoBytes);
+      int e[kMaxTileM / 32], f[kMaxTileM / 32], we[kTileN / 32];
 #pragma unroll
       for (int x = 0; x < kMaxTileM / 32; ++x) {
         const int m = 32 * x + lane;
         e[x] = m < t.cnt ? __ldg(a.xexp + t.m0 + m) : 0;
         f[x] = m < t.cnt ? __ldg(a.xflag + t.m0 + m) : 0;
       }
+#pragma unroll
+      for (int x = 0; x < kTileN / 32; ++x)
+        we[x] = t.n0 + 32 * x + lane < a.N ? __ldg(a.wexp + row0 + 32 * x + lane) : 0;
       bool ok = mbar_wait(emptyI + 8 * s, ((k / kInfos) & 1) ^ 1, a.fault, kFaultEpilogue);
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
-      // special: some token is flagged, or the two powers of two of an output cannot be
-      // multiplied into one normal float
       bool special = false;
 #pragma unroll
       for (int x = 0; x < kMaxTileM / 32; ++x) {
         const int m = 32 * x + lane;
-        xe[m] = e[x];
-        xe[kMaxTileM + m] = f[x];
-        xe[2 * kMaxTileM + m] = (e[x] + 127) << 23;
+        info[m] = (e[x] + 127) << 23;
+        info[kInfoExp + m] = 2 * e[x] + f[x];
         special = special || f[x] != 0 || e[x] < -85 || e[x] > 115;
       }
+#pragma unroll
+      for (int x = 0; x < kTileN / 32; ++x) info[kInfoRow + 32 * x + lane] = we[x];
       special = __any_sync(0xffffffffu, special);
-      if (lane == 0) {
-        xe[3 * kMaxTileM] = special;
-        mbar_arrive(fullI + 8 * s);
-      }
+      if (lane == 0)
+        *reinterpret_cast<Info*>(info + kInfoFields) = {t.m0, t.cnt, t.n0, row0, t.nkb, t.kb0, t.split, special};
       __syncwarp();
+      if (lane == 0) mbar_arrive(fullI + 8 * s);
     }
   } else if (warp >= 4) {
     // ---------------- decode: weight stage g belongs to warp group g (four warps, one
@@ -600,7 +613,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t myscale = base + kOffScale + static_cast<uint32_t>(row >> 2) * (kChunkBlocks * kScales * 8) +
                              2u * (row & 3) + 8u * kScales * (grp & 1);
     bool ok = true;
-    uint32_t done_tiles = 0;  // epilogues finished
+    uint32_t tiles = 0, done_tiles = 0;  // begun, and epilogues finished
     uint32_t meetings = 0;    // of the decoder warps
     auto meeting = [&]() {
       __syncwarp();
@@ -610,17 +623,18 @@ __global__ void __launch_bounds__(kThreads, 1)
       ++meetings;
     };
 
-    auto epilogue = [&](const Tile& t) {
+    auto info_of = [&](uint32_t k) { return reinterpret_cast<const int*>(sp + kOffInfo + (k % kInfos) * kInfoBytes); };
+    // of the oldest tile without one (its info is there: the warp has decoded for it)
+    auto epilogue = [&]() {
+      const int* const info = info_of(done_tiles);
+      const Info& t = *reinterpret_cast<const Info*>(info + kInfoFields);
+      const float* xs = reinterpret_cast<const float*>(info);
+      const int* xe = info + kInfoExp;
       const int n = mma_n(t.cnt), nacc = accs_for(n);
       const int nr = t.n0 + 32 * q + lane;
-      const int we = nr < a.N ? __ldg(a.wexp + static_cast<int64_t>(t.e) * a.groups * 4 + nr) : 0;
+      const int we = info[kInfoRow + 32 * q + lane];
       const float ws = __int_as_float((127 + we) << 23);  // 2^we (we is in -30 .. 4)
-      const uint32_t si = done_tiles % kInfos;
-      const int* xe = reinterpret_cast<const int*>(sp + kOffInfo + si * kInfoBytes);
-      const int* xf = xe + kMaxTileM;
-      const float* xs = reinterpret_cast<const float*>(xf + kMaxTileM);
-      if (ok) ok = mbar_wait(fullI + 8 * si, (done_tiles / kInfos) & 1, a.fault, kFaultEpilogue);
-      const bool special = ok && xe[3 * kMaxTileM] != 0;
+      const bool special = ok && t.special;
       if (ok) ok = mbar_wait(accum, done_tiles & 1, a.fault, kFaultEpilogue);
       __syncwarp();
       tc_fence_after_sync();
@@ -680,8 +694,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int x = 0; x < 16; ++x) {
             const int m = c0 + x;
-            if (m < t.cnt && !xf[m]) {
-              const float y = special ? scale_pow2(__uint_as_float(v[x]), xe[m] + we) : __uint_as_float(v[x]) * (xs[m] * ws);
+            if (m < t.cnt && !(xe[m] & 1)) {
+              const float y = special ? scale_pow2(__uint_as_float(v[x]), (xe[m] >> 1) + we) : __uint_as_float(v[x]) * (xs[m] * ws);
               const int64_t o = static_cast<int64_t>(t.m0 + m) * a.N + nr;
               if (part) part[o] = y;
               else a.Y[o] = f32_to_bf16_bits(y);
@@ -690,7 +704,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         release();
         if (special)
-          fixup_flagged<kG>(a, t, xf, red, d, meeting, [&](int m, int r, float y) {
+          fixup_flagged<kG>(a, t, xe, red, d, meeting, [&](int m, int r, float y) {
             if (!ok) return;
             const int64_t o = static_cast<int64_t>(t.m0 + m) * a.N + t.n0 + r;
             if (part) part[o] = y;
@@ -698,32 +712,16 @@ __global__ void __launch_bounds__(kThreads, 1)
           });
       }
       __syncwarp();
-      if (lane == 0) mbar_arrive(emptyI + 8 * si);
+      if (lane == 0) mbar_arrive(emptyI + 8 * (done_tiles % kInfos));
       ++done_tiles;
     };
-    int pend = first;  // the tile whose epilogue is next, and its last block
-    Tile pt = {};
-    int64_t pend_last = -1;
-    auto next_pend = [&]() {
-      if (pend >= total) return;
-      pt = tile_at(a, pre, off, ntn, rank, pend);
-      pend_last += (pt.nkb + 1) / 2 * 2;
-    };
-    auto weight_exp = [&](const Tile& t) {
-      return t.n0 + row < a.N ? __ldg(a.wexp + static_cast<int64_t>(t.e) * a.groups * 4 + t.n0 + row) : 0;
-    };
-    next_pend();
-    int64_t blk0 = 0;     // blocks and chunks of the tiles before
-    uint32_t chunk0 = 0;
-    Tile t = pt;
-    int we_next = pend < total ? weight_exp(t) : 0;
-    for (int i = first; i < total; i += step) {
-      const int we = we_next;
-      const int nkb = t.nkb;
-      if (i + step < total) {  // the next tile and its row's exponent, before this one's blocks
-        t = tile_at(a, pre, off, ntn, rank, i + step);
-        we_next = weight_exp(t);
-      }
+    uint32_t chunk0 = 0;  // chunks of the tiles before
+    for (int i = first; i < total; i += step, ++tiles) {
+      if (ok) ok = mbar_wait(fullI + 8 * (tiles % kInfos), (tiles / kInfos) & 1, a.fault, kFaultEpilogue);
+      __syncwarp();
+      const int* const info = info_of(tiles);
+      const int we = ok ? info[kInfoRow + row] : 0;
+      const int nkb = ok ? reinterpret_cast<const Info*>(info + kInfoFields)->nkb : 0;
       // 2^-we as two fp16 factors (we is in -30 .. 4)
       const int we1 = we < -15 ? -15 : we;
       const __half2 f1 = __half2half2(__ushort_as_half(static_cast<uint16_t>((15 - we1) << 10)));
@@ -765,21 +763,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         // blocks, so the tensor cores go on as soon as the accumulators are read. (Each
         // group comes here after its first block behind the tile, which waits only for
         // blocks of that tile or earlier ones: no circle of waits.)
-        const int64_t b = blk0 + 2 * static_cast<int64_t>(c) + (grp & 1);
-        while (pend < total && pend_last < b) {
-          epilogue(pt);
-          pend += step;
-          next_pend();
-        }
+        while (done_tiles < tiles) epilogue();
       }
-      blk0 += 2 * static_cast<int64_t>(nch);
       chunk0 += nch;
     }
-    while (pend < total) {
-      epilogue(pt);
-      pend += step;
-      next_pend();
-    }
+    while (done_tiles < tiles) epilogue();
   }
 
   tc_fence_before_sync();
