@@ -78,10 +78,11 @@ struct Info {
 constexpr uint32_t kInfoBytes = kInfoFields * 4 + sizeof(Info);
 constexpr uint32_t kOffInfo = kOffScale + kRawStages * kScaleStage;
 constexpr uint32_t kOffRed = kOffInfo + kInfos * kInfoBytes;  // [512] floats
-constexpr uint32_t kOffPre = kOffRed + kDec * 4;                   // [E + 1] tiles before expert e
+constexpr uint32_t kOffPre = kOffRed + kDec * 4;                     // [E + 1] tiles before the i-th expert
 constexpr uint32_t kOffFirst = kOffPre + (LBQ_MAX_EXPERTS + 2) * 4;  // [E + 1] offsets, clamped
-constexpr uint32_t kOffBar = kOffFirst + (LBQ_MAX_EXPERTS + 2) * 4;
-constexpr uint32_t kBarBytes = 8 * (2 * kStages + 2 * kRawStages + 2 * kInfos + 3) + 8;  // and the TMEM slot
+constexpr uint32_t kOffOrder = kOffFirst + (LBQ_MAX_EXPERTS + 2) * 4;  // [E] the i-th expert (16 bits)
+constexpr uint32_t kOffBar = kOffOrder + LBQ_MAX_EXPERTS * 2;
+constexpr uint32_t kBarBytes = 8 * (2 * kStages + 2 * kRawStages + 2 * kInfos + 5) + 8;  // and the TMEM slot
 constexpr uint32_t kSmem = kOffBar + kBarBytes + 1024;
 static_assert(kSmem <= 232448, "over the shared-memory limit");
 constexpr unsigned kFaultX = 14, kFaultMma = 15, kFaultW = 16, kFaultDecode = 17, kFaultEpilogue = 18;
@@ -97,6 +98,7 @@ struct Args {
   int64_t T;
   const int* xexp;           // token row m was scaled by 2^-xexp[m]
   const int* xflag;          // 1: row m is recomputed in fp32
+  const int* plan;           // experts: [E + 1] tiles before the i-th expert, [E] the i-th expert
   const int* wexp;           // weight row was scaled by 2^-wexp (rows padded to groups)
   const uint16_t* X;
   const uint8_t* codes;
@@ -118,7 +120,95 @@ __device__ __forceinline__ int64_t source_row(const int32_t* slots, int topk, in
 
 __device__ __forceinline__ int clamp_row(int v, int R) { return v < 0 ? 0 : (v > R ? R : v); }
 
+// Token tiles of `cnt` rows: as few as fit, all alike up to 16 rows (none is empty: all
+// but the last hold at most 256 rows each, and cnt is more than they can hold).
+__device__ __forceinline__ int tiles_for(int cnt) { return (cnt + kMaxTileM - 1) / kMaxTileM; }
+__device__ __forceinline__ int tile_rows(int cnt, int nt) { return ((cnt + nt - 1) / nt + 15) / 16 * 16; }
+
 // ------------------------------------------------------------------- preparation
+// The order of the experts' tiles, by one block: experts whose tiles have the most tokens
+// come first, so that the tiles of a round, one a pair of CTAs, take about the same time
+// and the last round's are the shortest. (2048 tokens x 8
+// of 128 experts 149 us in the experts' order, 140 in this one; 4096 226 and 222. Equal
+// shares of the time, each of tiles in a row, took 257: all activations are then in use at
+// once, more than L2 holds.) A counting sort by sixteenths of a tile, stable.
+__device__ __forceinline__ void plan_tiles(const Args& a, int ntn, int* __restrict__ plan) {
+  constexpr int kClasses = kMaxTileM / 16 + 1, kChunks = LBQ_MAX_EXPERTS / 32;
+  __shared__ int off[LBQ_MAX_EXPERTS + 1], hist[kChunks][kClasses], sum[kClasses];
+  __shared__ short order[LBQ_MAX_EXPERTS];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, E = a.E;
+  for (int e = tid; e <= E; e += 256) off[e] = clamp_row(__ldg(a.offsets + e), a.M);
+  for (int i = tid; i < kChunks * kClasses; i += 256) (&hist[0][0])[i] = 0;
+  __syncthreads();
+  // Offsets that descend somewhere would name rows twice, and more tiles than are counted
+  // in 32 bits: no row then.
+  bool down = false;
+  for (int e = tid; e < E; e += 256) down = down || off[e + 1] < off[e];
+  down = __syncthreads_or(down);
+  auto class_of = [&](int e) {  // 0: the largest tiles; kClasses - 1: none; kClasses: no expert
+    if (e >= E) return kClasses;
+    const int rows = off[e + 1] - off[e];
+    return kClasses - 1 - (rows > 0 ? tile_rows(rows, tiles_for(rows)) / 16 : 0);
+  };
+  auto peers_of = [](int k) {
+    unsigned p = 0xffffffffu;
+#pragma unroll
+    for (int b = 0; b < 5; ++b) {
+      const unsigned m = __ballot_sync(0xffffffffu, (k >> b) & 1);
+      p &= (k >> b) & 1 ? m : ~m;
+    }
+    return p;
+  };
+  static_assert(kClasses < 32, "five bits");
+  if (!down) {
+    for (int e0 = 32 * warp; e0 < E; e0 += 256) {
+      const int k = class_of(e0 + lane);
+      const unsigned p = peers_of(k);
+      if (k < kClasses && lane == __ffs(p) - 1) hist[e0 / 32][k] = __popc(p);
+    }
+    __syncthreads();
+    if (tid < kClasses) {
+      int run = 0;
+      for (int c = 0; c < kChunks; ++c) {
+        const int n = hist[c][tid];
+        hist[c][tid] = run;
+        run += n;
+      }
+      sum[tid] = run;
+    }
+    __syncthreads();
+    for (int e0 = 32 * warp; e0 < E; e0 += 256) {
+      const int k = class_of(e0 + lane);
+      const unsigned p = peers_of(k);
+      if (k < kClasses) {
+        int at = hist[e0 / 32][k] + __popc(p & ((1u << lane) - 1u));
+        for (int j = 0; j < k; ++j) at += sum[j];
+        order[at] = static_cast<short>(e0 + lane);
+      }
+    }
+  }
+  __syncthreads();
+  if (warp != 0) return;
+  int run = 0;  // a running sum, 32 experts at a time
+  for (int i0 = 0; i0 < E; i0 += 32) {
+    const int i = i0 + lane, e = i < E && !down ? order[i] : 0;
+    const int rows = i < E && !down ? off[e + 1] - off[e] : 0;
+    const int c = rows > 0 ? tiles_for(rows) * ntn : 0;
+    int inc = c;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, inc, o);
+      if (lane >= o) inc += v;
+    }
+    if (i < E) {
+      plan[i] = run + inc - c;
+      plan[E + 1 + i] = e;
+    }
+    run += __shfl_sync(0xffffffffu, inc, 31);
+  }
+  if (lane == 0) plan[E] = run;
+}
+
 // The first blocks convert activation rows to fp16, kRow threads a row (exact power-of-two
 // scaling, flag if not exact): a whole block for few long rows, where latency counts, a
 // warp for many (a block a row took 107 us for 32768 rows of 2048, most of it launching
@@ -127,9 +217,14 @@ __device__ __forceinline__ int clamp_row(int v, int R) { return v < 0 ? 0 : (v >
 template <int kRow>
 __global__ void __launch_bounds__(256, 8)
     q4_prepare_kernel(const Args a, uint16_t* __restrict__ Xh, int* __restrict__ xexp,
-                      int* __restrict__ xflag, int* __restrict__ wexp, int ngroups, int group) {
+                      int* __restrict__ xflag, int* __restrict__ wexp, int* __restrict__ plan, int ngroups,
+                      int group) {
   pdl_launch_dependents();
   pdl_wait();
+  if (a.offsets && blockIdx.x == gridDim.x - 1) {
+    plan_tiles(a, (a.N + 2 * kTileN - 1) / (2 * kTileN), plan);
+    return;
+  }
   constexpr int kRows = 256 / kRow;  // rows a block
   __shared__ uint2 red[8];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -250,14 +345,10 @@ struct Tile {
   int split, kb0, nkb;
 };
 
-// Token tiles of `cnt` rows: as few as fit, all alike up to 16 rows (none is empty: all
-// but the last hold at most 256 rows each, and cnt is more than they can hold).
-__device__ __forceinline__ int tiles_for(int cnt) { return (cnt + kMaxTileM - 1) / kMaxTileM; }
-__device__ __forceinline__ int tile_rows(int cnt, int nt) { return ((cnt + nt - 1) / nt + 15) / 16 * 16; }
-
 // Tile `i` of the walk. Token tiles run fastest: the CTAs at work share weight tiles
 // (read from HBM once), and all activations stay in L2.
-__device__ __forceinline__ Tile tile_at(const Args& a, const int* pre, const int* off, int ntn, int rank, int i) {
+__device__ __forceinline__ Tile tile_at(const Args& a, const int* pre, const int* off, const uint16_t* order,
+                                        int ntn, int rank, int i) {
   Tile t;
   const int nkb = static_cast<int>(a.K / kTileK);
   if (!a.offsets) {
@@ -271,14 +362,14 @@ __device__ __forceinline__ Tile tile_at(const Args& a, const int* pre, const int
     t.nkb = nkb - t.kb0 < a.kb_split ? nkb - t.kb0 : a.kb_split;
     return t;
   }
-  int lo = 0, hi = a.E;  // the expert: the last with pre[e] <= i
+  int lo = 0, hi = a.E;  // the expert's place: the last with pre[] <= i
   while (hi - lo > 1) {
     const int mid = (lo + hi) >> 1;
     if (pre[mid] <= i) lo = mid; else hi = mid;
   }
-  const int r0 = off[lo], r1 = off[lo + 1];
+  const int e = order[lo], r0 = off[e], r1 = off[e + 1];
   const int nt = tiles_for(r1 - r0), rows = tile_rows(r1 - r0, nt), l = i - pre[lo];
-  t.e = lo;
+  t.e = e;
   t.n0 = (2 * (l / nt) + rank) * kTileN;
   t.m0 = r0 + (l % nt) * rows;
   t.cnt = r1 - t.m0 < rows ? r1 - t.m0 : rows;
@@ -292,9 +383,10 @@ __device__ __forceinline__ Tile tile_at(const Args& a, const int* pre, const int
 // (an instruction on the previous one's accumulator waits for it; small ones are shorter
 // than that wait).
 __device__ __forceinline__ int mma_n(int cnt) { return cnt <= 16 ? 16 : (cnt + 15) / 16 * 16; }
-__device__ __forceinline__ int accs_for(int n) {
-  return n > 128 ? 1 : (n > 64 ? 2 : (n > 32 ? 4 : 8));
-}
+__device__ __forceinline__ int accs_for(int n) { return n > 64 ? 1 : (n > 32 ? 2 : 4); }
+// Where they lie: a tile of up to 128 tokens takes the half of the accumulators' columns
+// that the tile before it does not, if that is as small, and starts while its sums are read.
+__device__ __forceinline__ uint32_t acc_column(int n, uint32_t tile) { return n <= kMaxTileM / 2 ? (tile & 1) * (kMaxTileM / 2) : 0u; }
 
 __device__ __forceinline__ uint64_t sw128_desc(uint32_t saddr) {
   uint64_t d = static_cast<uint64_t>((saddr >> 4) & 0x3FFFu);
@@ -396,10 +488,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   unsigned char* sp = smem_raw + (base - smem_u32(smem_raw));
   int* pre = reinterpret_cast<int*>(sp + kOffPre);
   int* off = reinterpret_cast<int*>(sp + kOffFirst);
+  uint16_t* order = reinterpret_cast<uint16_t*>(sp + kOffOrder);
   const uint32_t bars = base + kOffBar;
   const uint32_t full = bars, empty = full + 8 * kStages, fullR = empty + 8 * kStages,
-                 emptyR = fullR + 8 * kRawStages, accum = emptyR + 8 * kRawStages, dfree = accum + 8,
-                 meet = dfree + 8, fullI = meet + 8, emptyI = fullI + 8 * kInfos, tslot = emptyI + 8 * kInfos;
+                 emptyR = fullR + 8 * kRawStages, accum = emptyR + 8 * kRawStages, dfree = accum + 16,
+                 meet = dfree + 16, fullI = meet + 8, emptyI = fullI + 8 * kInfos, tslot = emptyI + 8 * kInfos;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (tid == 0) {
     for (int s = 0; s < kStages; ++s) {
@@ -415,8 +508,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(fullI + 8 * s, 1);
       mbar_init(emptyI + 8 * s, kDec / 32);
     }
-    mbar_init(accum, 1);
-    mbar_init(dfree, 2 * kDec / 32);
+    for (int s = 0; s < 2; ++s) {  // of even and odd tiles
+      mbar_init(accum + 8 * s, 1);
+      mbar_init(dfree + 8 * s, 2 * kDec / 32);
+    }
     mbar_init(meet, kDec / 32);
     fence_mbar_init();
   }
@@ -424,42 +519,17 @@ __global__ void __launch_bounds__(kThreads, 1)
   pdl_wait();
   const int rank = static_cast<int>(cluster_rank());
   const int ntn = (a.N + 2 * kTileN - 1) / (2 * kTileN);
-  int total;
-  if (a.offsets) {  // tiles before each expert (warp 0: a running sum, 32 experts at a time)
-    if (warp == 0) {
-      int run = 0;
-      bool down = false;
-      for (int e0 = 0; e0 < a.E; e0 += 32) {
-        const int e = e0 + lane;
-        int c = 0;
-        if (e < a.E) {
-          const int r0 = clamp_row(__ldg(a.offsets + e), a.M), r1 = clamp_row(__ldg(a.offsets + e + 1), a.M);
-          const int rows = r1 - r0;
-          off[e] = r0;
-          if (e == a.E - 1) off[a.E] = r1;
-          c = rows > 0 ? tiles_for(rows) * ntn : 0;
-          down = down || rows < 0;
-        }
-        int inc = c;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-          const int v = __shfl_up_sync(0xffffffffu, inc, o);
-          if (lane >= o) inc += v;
-        }
-        if (e < a.E) pre[e] = run + inc - c;
-        run += __shfl_sync(0xffffffffu, inc, 31);
-      }
-      // offsets that descend somewhere would name rows twice, and more tiles than are
-      // counted in 32 bits: no row then
-      down = __any_sync(0xffffffffu, down);
-      if (lane == 0) pre[a.E] = down ? 0 : run;
+  if (a.offsets)
+    for (int e = tid; e <= a.E; e += kThreads) {
+      off[e] = clamp_row(__ldg(a.offsets + e), a.M);
+      pre[e] = __ldg(a.plan + e);
+      if (e < a.E) order[e] = static_cast<uint16_t>(__ldg(a.plan + a.E + 1 + e));
     }
-  }
   tc_fence_before_sync();
   __syncthreads();
   cluster_sync_all();  // the other CTA's barriers and tensor memory are ready too
   tc_fence_after_sync();
-  total = a.offsets ? pre[a.E] : a.ntm * ntn * a.splits;
+  const int total = a.offsets ? pre[a.E] : a.ntm * ntn * a.splits;
   // All 512 columns are allocated, so the allocation starts at column 0; a constant keeps
   // the MMA loop's addresses in uniform registers.
   constexpr uint32_t tmem = 0;
@@ -473,7 +543,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint32_t blk = 0;  // stages filled
       bool ok = true;
       for (int i = first; i < total && ok; i += step) {
-        const Tile t = tile_at(a, pre, off, ntn, rank, i);
+        const Tile t = tile_at(a, pre, off, order, ntn, rank, i);
         const int half = mma_n(t.cnt) / 2, box = (half + kBoxStep - 1) / kBoxStep;
         const CUtensorMap* map = &tm_x.m[box - 1];
         for (int kb = 0; kb < (t.nkb + 1) / 2 * 2; ++kb, ++blk) {
@@ -502,27 +572,37 @@ __global__ void __launch_bounds__(kThreads, 1)
     // barriers for weights and two activation slabs, a block took 0.74 us at any size).
     if (rank == 0) {
       uint32_t blk = 0, nt = 0;
+      int before = 0;  // tokens of the tile before
       bool ok = true;
       for (int i = first; i < total && ok; i += step) {
-        const Tile t = tile_at(a, pre, off, ntn, rank, i);
-        const int n = mma_n(t.cnt), nacc = accs_for(n);
+        // (the tile's info stays until its epilogues, which come after its last instruction)
+        ok = mbar_wait(fullI + 8 * (nt % kInfos), (nt / kInfos) & 1, a.fault, kFaultMma);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        const Info& t = *reinterpret_cast<const Info*>(sp + kOffInfo + (nt % kInfos) * kInfoBytes + kInfoFields * 4);
+        const int n = mma_n(t.cnt), nacc = accs_for(n), nkb = t.nkb;
+        const uint32_t acc = tmem + acc_column(n, nt);
         const uint32_t idesc = idesc_f16_m256(n);
         const uint32_t half_k = static_cast<uint32_t>((n / 2 + kBoxStep - 1) / kBoxStep) * (kBoxStep * 128 >> 4);
-        // the accumulators are free once their previous tile's have been read
-        ok = mbar_wait(dfree, (nt & 1) ^ 1, a.fault, kFaultMma);
-        for (int kb = 0; kb < (t.nkb + 1) / 2 * 2; ++kb, ++blk) {
+        // the accumulators are free once the tile before the last has been read, and the last
+        // if one of the two is larger than half of them
+        ok = mbar_wait(dfree + 8 * (nt & 1), ((nt >> 1) & 1) ^ 1, a.fault, kFaultMma);
+        if (ok && nt > 0 && (n > kMaxTileM / 2 || before > kMaxTileM / 2))
+          ok = mbar_wait(dfree + 8 * ((nt & 1) ^ 1), ((nt - 1) >> 1) & 1, a.fault, kFaultMma);
+        before = n;
+        for (int kb = 0; kb < (nkb + 1) / 2 * 2; ++kb, ++blk) {
           const uint32_t s = blk % kStages;
           if (ok) ok = mbar_wait(full + 8 * s, (blk / kStages) & 1, a.fault, kFaultMma);
           ok = __all_sync(0xffffffffu, ok);
           if (!ok) break;
           tc_fence_after_sync();
           if (elect_one()) {
-            if (kb < t.nkb) {
+            if (kb < nkb) {
               const uint32_t ta = tmem + kTmemA + 64u * s;
               const uint64_t bdesc = sw128_desc(base + kOffSlab + 2 * s * kSlabBytes);
 #pragma unroll
               for (int ks = 0; ks < 8; ++ks)
-                mma_f16_ts_pair(tmem + static_cast<uint32_t>((ks & (nacc - 1)) * n), ta + 8u * ks,
+                mma_f16_ts_pair(acc + static_cast<uint32_t>((ks & (nacc - 1)) * n), ta + 8u * ks,
                                 bdesc + (ks >> 2) * half_k + 2u * (ks & 3), idesc,
                                 (kb > 0 || ks >= nacc) ? 1u : 0u);
             }
@@ -530,7 +610,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           __syncwarp();
         }
-        if (elect_one()) mma_commit_pair(accum);
+        if (elect_one()) mma_commit_pair(accum + 8 * (nt & 1));
         __syncwarp();
         ++nt;
       }
@@ -544,7 +624,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint32_t c = 0;
       bool ok = true;
       for (int i = first; i < total && ok; i += step) {
-        const Tile t = tile_at(a, pre, off, ntn, rank, i);
+        const Tile t = tile_at(a, pre, off, order, ntn, rank, i);
         const int g0 = t.e * a.groups + t.n0 / 4;
         for (int kb = t.kb0; kb < t.kb0 + t.nkb; kb += kChunkBlocks) {
           const uint32_t r = c % kRawStages;
@@ -565,7 +645,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ---------------- what the decoders have to know of the tiles
     uint32_t k = 0;
     for (int i = first; i < total; i += step, ++k) {
-      const Tile t = tile_at(a, pre, off, ntn, rank, i);
+      const Tile t = tile_at(a, pre, off, order, ntn, rank, i);
       const int row0 = t.e * a.groups * 4 + t.n0;
       const uint32_t s = k % kInfos;
       int* info = reinterpret_cast<int*>(sp + kOffInfo + s * kInfoBytes);
@@ -635,16 +715,17 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int we = info[kInfoRow + 32 * q + lane];
       const float ws = __int_as_float((127 + we) << 23);  // 2^we (we is in -30 .. 4)
       const bool special = ok && t.special;
-      if (ok) ok = mbar_wait(accum, done_tiles & 1, a.fault, kFaultEpilogue);
+      if (ok) ok = mbar_wait(accum + 8 * (done_tiles & 1), (done_tiles >> 1) & 1, a.fault, kFaultEpilogue);
       __syncwarp();
       tc_fence_after_sync();
       // this warp's columns 16 grp + 64 c + (0..15), the accumulators summed in order
+      const uint32_t acc = lane_base + acc_column(n, done_tiles);
       auto read16 = [&](int c0, uint32_t (&v)[16]) {
-        tmem_ld16(lane_base + static_cast<uint32_t>(c0), v);
+        tmem_ld16(acc + static_cast<uint32_t>(c0), v);
         tmem_ld_wait();
         for (int j = 1; j < nacc; ++j) {
           uint32_t u[16];
-          tmem_ld16(lane_base + static_cast<uint32_t>(j * n + c0), u);
+          tmem_ld16(acc + static_cast<uint32_t>(j * n + c0), u);
           tmem_ld_wait();
 #pragma unroll
           for (int x = 0; x < 16; ++x) v[x] = __float_as_uint(__uint_as_float(v[x]) + __uint_as_float(u[x]));
@@ -653,7 +734,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       auto release = [&]() {  // the accumulators may be overwritten
         tc_fence_before_sync();
         __syncwarp();
-        if (lane == 0) mbar_arrive_cluster(dfree0);
+        if (lane == 0) mbar_arrive_cluster(dfree0 + 8 * (done_tiles & 1));
       };
       if (!special && !a.part) {
         // all columns are read, scaled and rounded first, so that the tensor cores wait for
@@ -825,7 +906,7 @@ Plan plan_for(const lbq_weights* w, int64_t M) {
 inline size_t align_up(size_t v, size_t a) { return (v + a - 1) / a * a; }
 
 struct Scratch {
-  size_t xh, xexp, xflag, wexp, part, total;
+  size_t xh, xexp, xflag, wexp, plan, part, total;
 };
 Scratch scratch_for(const lbq_weights* w, int64_t rows, int E, size_t part_floats) {
   Scratch s;
@@ -839,6 +920,7 @@ Scratch scratch_for(const lbq_weights* w, int64_t rows, int E, size_t part_float
   s.xexp = take(static_cast<size_t>(rows) * 4);
   s.xflag = take(static_cast<size_t>(rows) * 4);
   s.wexp = take(static_cast<size_t>(E) * g4_rows(w->N) * 4);
+  s.plan = take((2 * static_cast<size_t>(E) + 1) * 4);
   s.part = take(part_floats * 4);
   s.total = o;
   return s;
@@ -890,6 +972,8 @@ cudaError_t launch(const lbq_weights* w, const Plan& plan, const lbq_expert_rows
   a.xexp = xexp;
   a.xflag = xflag;
   a.wexp = wexp;
+  int* tiles = reinterpret_cast<int*>(ws + sc.plan);
+  a.plan = tiles;
   a.X = X;
   a.codes = static_cast<const uint8_t*>(w->codes);
   a.scales = static_cast<const uint16_t*>(w->scales);
@@ -941,12 +1025,12 @@ cudaError_t launch(const lbq_weights* w, const Plan& plan, const lbq_expert_rows
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
   const bool many = rows >= 8 * sm_count();  // enough rows for every SM at eight a block
-  cfg.gridDim = dim3(static_cast<unsigned>(many ? (rows + 7) / 8 : rows) + wblocks);
+  cfg.gridDim = dim3(static_cast<unsigned>(many ? (rows + 7) / 8 : rows) + wblocks + (er ? 1 : 0));
   cfg.blockDim = dim3(256);
   cfg.stream = s;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  e = cudaLaunchKernelEx(&cfg, many ? q4_prepare_kernel<32> : q4_prepare_kernel<256>, a, Xh, xexp, xflag, wexp, ngroups, kG);
+  e = cudaLaunchKernelEx(&cfg, many ? q4_prepare_kernel<32> : q4_prepare_kernel<256>, a, Xh, xexp, xflag, wexp, tiles, ngroups, kG);
   if (e != cudaSuccess) return e;
   const int64_t ntn = (w->N + 2 * kTileN - 1) / (2 * kTileN), pairs = sm_count() / 2;
   // experts: at most rows / 256 + E token tiles
@@ -970,7 +1054,7 @@ cudaError_t launch(const lbq_weights* w, const Plan& plan, const lbq_expert_rows
 
 }  // namespace
 
-// [64 KB left alone: the counter rule][fp16 X][exponents, flags][weight exponents][partials]
+// [64 KB left alone: the counter rule][fp16 X][exponents, flags][weight exponents][tile order][partials]
 size_t lbq_q4_tc_workspace(const lbq_weights* w, int64_t M) {
   const Plan p = plan_for(w, M);
   return kWsCounterBytes +
