@@ -462,3 +462,31 @@ def test_two_streams_and_two_graphs_at_once(L, orc, T):
         for s in sets:
             assert torch.equal(s[2][:kept], s[4])
     assert L.lbq_device_fault() == 0
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("fmt,T,topk,E,N,K,skew", [(5, 1500, 2, 40, 1200, 384, 3.0), (6, 1500, 2, 40, 1200, 256, 1.0),
+                                                   (5, 4000, 1, 9, 2500, 128, 6.0), (6, 300, 8, 200, 600, 128, 0.0)])
+def test_experts_of_very_different_sizes(L, orc, fmt, T, topk, E, N, K, skew):
+    """Several tiles for every pair of SMs, large and small ones and experts without rows."""
+    ew = L.pack_experts(fmt, (torch.randn(E, N, K, generator=torch.Generator().manual_seed(8)) * 0.02).cuda())
+    X = synth.activations(T, K, 9).cuda()
+    g = torch.Generator().manual_seed(10)
+    score = torch.rand(T, E, generator=g).log() / torch.linspace(1, 8, E).pow(skew)
+    score[:, E // 2] = float("-inf")
+    ids = score.topk(topk, -1).indices.to(torch.int32).cuda()
+    offsets, rows, slots = L.lbq_expert_sort(ids, E)
+    off = offsets.tolist()
+    assert off[E] == T * topk and off[E // 2] == off[E // 2 + 1]
+    Y = L.lbq_expert_gemm(ew, X, offsets, slots=slots, topk=topk)
+    again = L.lbq_expert_gemm(ew, X, offsets, slots=slots, topk=topk)
+    assert torch.equal(Y, again)
+    for e in range(E):
+        if off[e] == off[e + 1]:
+            continue
+        one = L.PackedWeights(fmt, K, N, ew.codes[e], ew.scales[e])
+        q, s = L.lbq_unpack(one)
+        W = q.double() * s.double().repeat_interleave(K // s.shape[1], 1)
+        x = X[(slots[off[e]:off[e + 1]] // topk).long()].double()
+        _check_rows(Y[off[e]:off[e + 1]], x @ W.t(), x.abs() @ W.abs().t(), True)
+    assert L.lbq_device_fault() == 0

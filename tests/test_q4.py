@@ -314,3 +314,27 @@ def test_captured_replayed_and_on_another_stream(L, orc, M):
         both()
     side.synchronize()
     assert torch.equal(y, want)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("fmt", Q4)
+@pytest.mark.parametrize("M,N,K", [(20, 40000, 256), (100, 40000, 384), (300, 30000, 128), (1000, 9000, 256)])
+def test_many_tiles_for_every_pair_of_sms(L, fmt, M, N, K):
+    """Products with several output tiles a pair of SMs, of up to 128 tokens and of more,
+    with a few tokens that span more than fp16 holds (recomputed in fp32)."""
+    W = torch.randn(N, K, generator=torch.Generator().manual_seed(3)).mul_(0.02).cuda()
+    pw = L.lbq_pack(fmt, W)
+    q, s = L.lbq_unpack(pw)
+    dense = q.double() * s.double().repeat_interleave(K // s.shape[1], 1)
+    X = synth.activations(M, K, 4)
+    X[3, 5], X[M - 1, 7] = 2.0 ** 40, 2.0 ** -60
+    X[M // 2] *= 2.0 ** -90
+    X = X.cuda()
+    Y = L.lbq_gemm(pw, X)
+    assert torch.equal(Y, L.lbq_gemm(pw, X))
+    x = X.double()
+    want, S = x @ dense.t(), x.abs() @ dense.abs().t()
+    err = (Y.double() - want).abs()
+    lim = 2.0 ** -8 * want.abs() + (2.0 ** -11 + 2.0 ** -12) * S
+    assert (err <= lim).all(), f"worst {(err / lim).max()}"
+    assert L.lbq_device_fault() == 0
