@@ -44,9 +44,9 @@
 //  * Programmatic dependent launch: the copy warp never waits for the previous
 //    kernel, so its first copies (one slot per warp group) land while it finishes;
 //    the other slots are filled once the table is built (their shared-memory writes
-//    slowed the build down). Only the batch-1 kernels let their successor start
-//    early, and they never write packed weights; any other kernel has completed
-//    before this one starts. x, y and the workspace are touched only after the wait.
+//    slowed the build down). Kernels that let their successor start early (the
+//    batch-1 ones, the 4-bit products and the expert calls) never write packed
+//    weights; any other kernel has completed before this one starts. x, y and the workspace are touched only after the wait.
 #include <type_traits>
 
 #include "lut.cuh"
@@ -175,8 +175,7 @@ __global__ void __maxnreg__(96) gemv_lut_kernel(const __grid_constant__ CUtensor
     // this CTA and goes to slot q % S; one tensor copy of their groups' slice (groups
     // past the last read as zero) and one of their scales; a last, partial slot gets
     // one copy per unit. The packed weights are never written by a kernel that lets
-    // this one start early (only the batch-1 kernels do, and they do not write
-    // weights), so the copies do not wait for the previous kernel: the ring fills
+    // this one start early, so the copies do not wait for the previous kernel: the ring fills
     // while it finishes.
     if (lane == 0) {
       prefetch_tmap(&tm_c);

@@ -49,8 +49,9 @@ extern "C" lbq_status lbq_gemv_noalloc(const lbq_weights* w, const uint16_t* x, 
   void* scratch = nullptr;
   const lbq_status sst = scratch_for_current_device(&scratch);
   if (sst != LBQ_OK) return sst;
-  // Nothing needs clearing: the batch-1 product writes every slice sum before it reads
-  // it, and never touches the arrival counters at the array's start, which are zero
-  // since the library was loaded (static device memory starts zeroed).
+  // Nothing needs clearing: the batch-1 product writes every partial sum before it reads
+  // it, and the arrival counters at the array's start are zero since the library was
+  // loaded (static device memory starts zeroed): 4-bit products leave them zero again,
+  // the others never touch them.
   return lbq_gemv(w, x, D, y, scratch, LBQ_NOALLOC_SCRATCH_BYTES, stream);
 }

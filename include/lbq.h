@@ -164,9 +164,9 @@ lbq_status lbq_pack(int32_t fmt, const float* W, int64_t K, int64_t N, void* cod
                     void* scales, void* stream);
 
 /* Unpack codes to int8 values (t in {-1,0,1} for TERN5, 2b-1 in {-1,1} for SIGN1,
- * q in {0,1,2,3} for Q2RHT, q - 8 in -8..7 for the 4-bit formats) into out [N][K] (device), and the block scales as fp32
- * into scales_out [N][K/blk] (device; blk = 128, or 32 for Q2RHT and Q4G32) when
- * non-NULL.
+ * q in {0,1,2,3} for Q2RHT, q - 8 in -8..7 for the 4-bit formats) into out [N][K]
+ * (device), and the block scales as fp32 into scales_out [N][K/blk] (device; blk = 128,
+ * or 32 for Q2RHT and Q4G32) when non-NULL.
  * A test hook for the bit-exact code check. */
 lbq_status lbq_unpack(const lbq_weights* w, int8_t* out, float* scales_out, void* stream);
 
@@ -202,7 +202,9 @@ size_t lbq_workspace_bytes(const lbq_weights* w, int64_t M);
  * (programmatic dependent launch) and touches x, y and the workspace only once that
  * kernel has finished, but it reads the packed weights at once. Weights written on
  * the same stream are therefore safe as long as the writing kernel does not itself
- * let its successor start early: lbq_pack, copies and ordinary kernels do not.
+ * let its successor start early: lbq_pack, copies and ordinary kernels do not. (The
+ * same holds for 4-bit products of up to 16 rows in lbq_gemm and for 4-bit lists in
+ * lbq_gemv_batch. The expert calls start early too, and read nothing before their turn.)
  * Errors: LBQ_ERR_ARG (nulls, D missing for Q2RHT), LBQ_ERR_SHAPE, LBQ_ERR_ALIGN,
  * LBQ_ERR_FORMAT, LBQ_ERR_WORKSPACE, LBQ_ERR_CUDA. */
 lbq_status lbq_gemv(const lbq_weights* w, const uint16_t* x, const int8_t* D, uint16_t* y,
@@ -294,9 +296,8 @@ lbq_status lbq_gemv_batch(const lbq_product* ps, int32_t n, void* workspace,
  * whose first unit-slice lies in [bound[c], bound[c + 1]) (unit u of piece s of product
  * i starts at c0_i + NU_i * j0 + u * (j1 - j0)), and *total, the list's unit-slices.
  * Errors: LBQ_ERR_ARG (NULL outputs, ctas < 1 or > LBQ_BATCH_MAX_CTAS, n > LBQ_BATCH_MAX,
- * mixed formats), LBQ_ERR_FORMAT (a 4-bit list: its launch cuts products into 32-row
- * tiles of full K, one CTA each, and has no such schedule), and those of
- * lbq_gemv_batch's checks. */
+ * mixed formats), LBQ_ERR_FORMAT (a 4-bit list: its launch cuts one line of 32-row
+ * tiles into equal runs and has no unit-slices), and those of lbq_gemv_batch's checks. */
 lbq_status lbq_gemv_batch_plan(const lbq_product* ps, int32_t n, int32_t ctas, int32_t* pieces,
                                int64_t* bound, int64_t* total);
 
@@ -377,10 +378,9 @@ lbq_status lbq_expert_gemm(const lbq_weights* w, int32_t E, const uint16_t* X, i
  * wait that runs out records a non-zero *code (3: shared-memory layout of the
  * batch-1 product, 4-9: tensor-core product stages, 10: the batch-1 product's
  * weight copies, 11: lbq_selftest_wait, 12: unused (lbq_gemv_batch has no waits),
- * 13: lbq_gemv_batch's shared-memory layout, 14-18: 4-bit tensor-core product stages, 19: a 4-bit product
- * of few tokens waiting for room)
- * and the kernel returns early with
- * incomplete outputs instead of hanging. Synchronises the device.
+ * 13: lbq_gemv_batch's shared-memory layout, 14-18: 4-bit tensor-core product stages)
+ * and the kernel returns early with incomplete outputs instead of hanging. Synchronises
+ * the device.
  * Returns LBQ_OK with *code = 0 when no wait gave up, LBQ_ERR_DEVICE_WAIT with the
  * code otherwise. Errors: LBQ_ERR_ARG (code NULL), LBQ_ERR_CUDA. */
 lbq_status lbq_device_fault(uint32_t* code);
@@ -405,9 +405,9 @@ lbq_status lbq_selftest_wait(void* stream);
  * LBQ_ERR_WORKSPACE and enqueues nothing; use lbq_gemv with your own workspace
  * then. The call allocates nothing: no cudaMalloc, no cudaFree, no allocating
  * library routine. It enqueues the product's kernels only: the product writes every
- * scratch value before reading it, and the array's arrival counters, which it never
- * writes, are zero from the moment the library is loaded, so there is nothing to
- * clear between calls.
+ * scratch value before reading it, and the array's arrival counters are zero from the
+ * moment the library is loaded (a 4-bit product counts in them and leaves them zero,
+ * the others never write them), so there is nothing to clear between calls.
  *
  * The first call on each device looks up the array's device address (with that
  * device current) and caches it; make that first call before any stream capture.

@@ -5,7 +5,8 @@
  * code, header, table or constant generator with the CUDA library.
  *
  * Formats (ids 1 = ternary 5-trits-per-byte, 2 = 1-bit sign, 3 = 2-bit with
- * rotated input, 5 and 6 = 4-bit with scales per 32 and 128) are described where they are implemented, in lbq_oracle.c.
+ * rotated input, 5 and 6 = 4-bit with scales per 32 and 128) are described where they
+ * are implemented, in lbq_oracle.c.
  * Every function returns 0 on success and a negative number on bad arguments.
  */
 #ifndef LBQ_ORACLE_H
