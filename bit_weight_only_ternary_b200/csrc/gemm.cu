@@ -17,9 +17,18 @@ using namespace lbq;
 // lanes' sums are then added across the warp.
 constexpr int kRowsPerWarp = 8;
 
-// 4-bit weights: up to this many tokens the warp-level matrix instructions of q4_gemv.cu,
-// more run on the tensor cores of q4_tc.cu.
-constexpr int64_t kQ4FewTokens = 16;
+// 4-bit weights: few tokens run on the warp-level matrix instructions of q4_gemv.cu, which
+// decode the weights once for every eight tokens, more on the tensor cores of q4_tc.cu,
+// which decode them once but start and prepare some 10 us longer. Measured, K x N:
+//   tokens  2048x1536     5120x5120     5120x7168     5120x10240    5120x34816
+//        8  8.4 / 14.3    14.9 / 20.3                               32.5 / 41.0 us
+//       16  8.4 / 14.4    17.3 / 20.7   20.6 / 22.9   23.6 / 24.7   47.8 / 41.0
+//       24  8.7 / 14.4    20.3 / 24.5   23.6 / 24.6   28.8 / 24.7   66.0 / 41.1
+//       32  12.5 / 14.5   22.6 / 24.3   27.1 / 24.7   33.2 / 24.7   82.4 / 41.1
+// (40 tokens of 2048 x 4096: 16.4 / 14.4.)
+inline bool q4_few(const lbq_weights* w, int64_t M) {
+  return M <= 8 || (M <= 32 && (M + 7) / 8 * w->N <= (int64_t{1} << 27) / w->K);
+}
 
 template <int FMT>
 __global__ void __launch_bounds__(256) gemm_rowwarp(const uint8_t* __restrict__ codes,
@@ -101,7 +110,7 @@ __global__ void __launch_bounds__(256) gemm_rowwarp(const uint8_t* __restrict__ 
 
 size_t lbq_gemm_workspace(const lbq_weights* w, int64_t M) {
   if (w->fmt == LBQ_TERN5) return lbq_gemm_tc_workspace(w, M);
-  if (is_q4(w->fmt)) return M <= kQ4FewTokens ? lbq_q4_few_workspace(M) : lbq_q4_tc_workspace(w, M);
+  if (is_q4(w->fmt)) return q4_few(w, M) ? lbq_q4_few_workspace(M) : lbq_q4_tc_workspace(w, M);
   return w->fmt == LBQ_Q2RHT
              ? kWsCounterBytes + static_cast<size_t>(w->K) * static_cast<size_t>(M) * sizeof(float)
              : 0;
@@ -117,7 +126,7 @@ cudaError_t lbq_launch_gemm(const lbq_weights* w, const uint16_t* X, int64_t M, 
   switch (w->fmt) {
     case LBQ_Q4G32:
     case LBQ_Q4G128:
-      return M <= kQ4FewTokens ? lbq_launch_q4_few(w, X, M, Y, ws, s) : lbq_launch_q4_tc(w, X, M, Y, ws, s);
+      return q4_few(w, M) ? lbq_launch_q4_few(w, X, M, Y, ws, s) : lbq_launch_q4_tc(w, X, M, Y, ws, s);
     case LBQ_TERN5:  // tensor-core path (gemm_tc.cu)
       return lbq_launch_gemm_tc(w, X, M, Y, ws, s);
     case LBQ_SIGN1:

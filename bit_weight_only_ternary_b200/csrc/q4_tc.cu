@@ -860,46 +860,70 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-// Y = bf16(sum over splits of the fp32 partial products), splits in order.
+// Y = bf16(sum over splits of the fp32 partial products), splits in order; four outputs a
+// thread (kVec: their number is a multiple of four and Y is aligned to them).
+template <bool kVec>
 __global__ void __launch_bounds__(256) q4_split_sum_kernel(const float* __restrict__ part, int splits,
                                                            int64_t MN, uint16_t* __restrict__ Y) {
-  const int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x;
+  pdl_launch_dependents();
+  pdl_wait();
+  const int64_t i = 4 * (static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x);
   if (i >= MN) return;
-  float sum = 0.0f;
-  for (int z = 0; z < splits; ++z) sum += __ldcg(part + z * MN + i);
-  Y[i] = f32_to_bf16_bits(sum);
+  if (kVec) {
+    float4 sum = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 4
+    for (int z = 0; z < splits; ++z) {
+      const float4 v = __ldcg(reinterpret_cast<const float4*>(part + z * MN + i));
+      sum.x += v.x;
+      sum.y += v.y;
+      sum.z += v.z;
+      sum.w += v.w;
+    }
+    const uint32_t lo = f32_to_bf16_bits(sum.x) | (static_cast<uint32_t>(f32_to_bf16_bits(sum.y)) << 16);
+    const uint32_t hi = f32_to_bf16_bits(sum.z) | (static_cast<uint32_t>(f32_to_bf16_bits(sum.w)) << 16);
+    *reinterpret_cast<uint2*>(Y + i) = make_uint2(lo, hi);
+  } else {
+    for (int64_t j = i; j < i + 4 && j < MN; ++j) {
+      float sum = 0.0f;
+      for (int z = 0; z < splits; ++z) sum += __ldcg(part + z * MN + j);
+      Y[j] = f32_to_bf16_bits(sum);
+    }
+  }
 }
 
 struct Plan {
   int tile_m, ntm, splits, kb_split;
 };
 
-// Dense: how many token tiles, and whether K is split. Modelled time: rounds of tiles over
-// the pairs of SMs, each a fixed part (start, epilogue: some 4 us) and its blocks; a block
-// of 128 K takes about 0.3 us + 1.4 ns a token (measured: 0.33 us at 32 tokens, 0.42 at
-// 128, 0.66 at 256). K is split only when all tiles leave half of the pairs idle.
+// Dense: how many token tiles, and whether K is split where the tiles leave half of the
+// pairs of SMs idle or more. Modelled time in us: rounds of tiles over the pairs, each 1.5
+// and its blocks; a block of 128 K takes 0.36 up to some 120 tokens, where the decoding and
+// the reading of the weight operand bound it, and 0.085 + 0.0023 a token beyond (measured:
+// 0.42 at 144, 0.57 at 208, 0.68 at 256); a split 3 and 3.3 a million partial sums, for their
+// way to memory and back. Over 84 sizes (40 to 1500 tokens, 512 x 8192 to 5120 x 34816) the
+// plan is within a few percent of the best of all; 256 tokens of 5120 x 7168: one tile of
+// tokens 39.1 us, one with K in two 37.9, two tiles 27.8.
 Plan plan_for(const lbq_weights* w, int64_t M) {
   Plan p = {};
   const int64_t ntn = (w->N + 2 * kTileN - 1) / (2 * kTileN), pairs = sm_count() / 2;
-  const int nkb = static_cast<int>(w->K / kTileK);
+  const int nkb = static_cast<int>(w->K / kTileK), most = (nkb + 3) / 4;  // splits: at least four blocks each
   const int64_t least = (M + kMaxTileM - 1) / kMaxTileM;
   double best = 0.0;
   for (int64_t nt = least; nt <= 4 * least && nt <= (M + 15) / 16; ++nt) {
-    const int64_t rows = ((M + nt - 1) / nt + 15) / 16 * 16, tiles = (M + rows - 1) / rows;
-    const double cost = static_cast<double>((tiles * ntn + pairs - 1) / pairs) *
-                        (4.0 + nkb * (0.3 + 0.0014 * static_cast<double>(rows)));
+    const int64_t rows = ((M + nt - 1) / nt + 15) / 16 * 16, ntm = (M + rows - 1) / rows, tiles = ntm * ntn;
+    int splits = tiles < pairs ? static_cast<int>(pairs / tiles) : 1;
+    if (splits > most) splits = most;
+    const int kb_split = ((nkb + splits - 1) / splits + kChunkBlocks - 1) / kChunkBlocks * kChunkBlocks;
+    splits = (nkb + kb_split - 1) / kb_split;
+    const double r = static_cast<double>(rows), block = 0.35 + 0.0002 * r, large = 0.085 + 0.0023 * r;
+    const double cost = static_cast<double>((tiles * splits + pairs - 1) / pairs) *
+                            (1.5 + kb_split * (block > large ? block : large)) +
+                        (splits > 1 ? 3.0 + 3.3e-6 * splits * static_cast<double>(M) * static_cast<double>(w->N) : 0.0);
     if (nt == least || cost < best) {
       best = cost;
-      p.tile_m = static_cast<int>(rows);
-      p.ntm = static_cast<int>(tiles);
+      p = {static_cast<int>(rows), static_cast<int>(ntm), splits, kb_split};
     }
   }
-  const int64_t tiles = ntn * p.ntm;
-  int splits = tiles < pairs ? static_cast<int>(pairs / tiles) : 1;
-  const int most = (nkb + 3) / 4;  // at least four blocks each
-  if (splits > most) splits = most;
-  p.kb_split = ((nkb + splits - 1) / splits + kChunkBlocks - 1) / kChunkBlocks * kChunkBlocks;
-  p.splits = (nkb + p.kb_split - 1) / p.kb_split;
   return p;
 }
 
@@ -1048,8 +1072,13 @@ cudaError_t launch(const lbq_weights* w, const Plan& plan, const lbq_expert_rows
   e = cudaLaunchKernelEx(&cfg, q4_tc_kernel<kG>, tx, tw, ts, a);
   if (e != cudaSuccess || plan.splits == 1) return e;
   const int64_t MN = rows * w->N;
-  q4_split_sum_kernel<<<static_cast<unsigned>((MN + 255) / 256), 256, 0, s>>>(a.part, plan.splits, MN, Y);
-  return cudaGetLastError();
+  cfg.gridDim = dim3(static_cast<unsigned>((MN + 1023) / 1024));
+  cfg.blockDim = dim3(256);
+  cfg.dynamicSmemBytes = 0;
+  cfg.numAttrs = 1;
+  const bool vec = MN % 4 == 0 && (reinterpret_cast<uintptr_t>(Y) & 7) == 0;
+  return cudaLaunchKernelEx(&cfg, vec ? q4_split_sum_kernel<true> : q4_split_sum_kernel<false>,
+                            static_cast<const float*>(a.part), plan.splits, MN, Y);
 }
 
 }  // namespace

@@ -203,7 +203,7 @@ size_t lbq_workspace_bytes(const lbq_weights* w, int64_t M);
  * kernel has finished, but it reads the packed weights at once. Weights written on
  * the same stream are therefore safe as long as the writing kernel does not itself
  * let its successor start early: lbq_pack, copies and ordinary kernels do not. (The
- * same holds for 4-bit products of up to 16 rows in lbq_gemm and for 4-bit lists in
+ * same holds for 4-bit products of up to 32 rows in lbq_gemm and for 4-bit lists in
  * lbq_gemv_batch. The expert calls start early too, and read nothing before their turn.)
  * Errors: LBQ_ERR_ARG (nulls, D missing for Q2RHT), LBQ_ERR_SHAPE, LBQ_ERR_ALIGN,
  * LBQ_ERR_FORMAT, LBQ_ERR_WORKSPACE, LBQ_ERR_CUDA. */
@@ -226,10 +226,10 @@ lbq_status lbq_gemv_f32(const lbq_weights* w, const uint16_t* x, const int8_t* D
  * span more than about 2^31) is recomputed in fp32 on the CUDA cores, which is
  * slower but keeps the same accuracy. 1-bit and 2-bit weights: a CUDA-core kernel
  * in which each warp decodes a weight row's blocks once for up to 8 activation rows.
- * 4-bit weights: up to 16 rows on warp-level matrix instructions with nothing rounded
- * before the output; more rows as ternary ones on the tensor cores, with the dequantised
- * weights rounded to fp16 (a relative 2^-11 each; a row's scales below 2^-25 of its
- * largest one count as subnormal).
+ * 4-bit weights: few rows (up to 8, or up to 32 of matrices that are not large) on
+ * warp-level matrix instructions with nothing rounded before the output; more rows as
+ * ternary ones on the tensor cores, with the dequantised weights rounded to fp16 (a
+ * relative 2^-11 each; a row's scales below 2^-25 of its largest one count as subnormal).
  * Same formats, D and workspace rules as lbq_gemv (workspace for this M, from
  * lbq_workspace_bytes). */
 lbq_status lbq_gemm(const lbq_weights* w, const uint16_t* X, int64_t M, const int8_t* D,
