@@ -338,3 +338,23 @@ def test_many_tiles_for_every_pair_of_sms(L, fmt, M, N, K):
     lim = 2.0 ** -8 * want.abs() + (2.0 ** -11 + 2.0 ** -12) * S
     assert (err <= lim).all(), f"worst {(err / lim).max()}"
     assert L.lbq_device_fault() == 0
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("fmt", Q4)
+def test_tensor_parallel_shards(L, orc, fmt):
+    """Shards of a matrix over three ranks: output rows beside one another, and input
+    features whose fp32 partial products are summed."""
+    from bit_weight_only_ternary_b200 import tp
+    K, N, world = 1536, 300, 3
+    W, X = synth.weights(N, K, 71), synth.activations(1, K, 72)
+    codes, scales = orc.pack(fmt, W.numpy())
+    Y, S = orc.gemm(fmt, codes, scales, K, synth.bf16_bits(X))
+    x, pack = X[0].cuda(), lambda f, w: L.lbq_pack(f, w.cuda())
+    col = torch.cat([tp.column_forward(tp.make_shard(W, fmt, "column", r, world, pack), x) for r in range(world)])
+    _inside(col, Y[0], S[0], "column")
+    part = torch.zeros(N, device="cuda")
+    for r in range(world):
+        s = tp.make_shard(W, fmt, "row", r, world, pack)
+        part += L.lbq_gemv_f32(s.weights, x[s.lo:s.hi])
+    _inside(part, Y[0], S[0], "row", rounded=False)
