@@ -228,20 +228,27 @@ __global__ void __launch_bounds__(kRowThreads)
 // Slots of a token taken together: their rows' loads are all in flight at once.
 constexpr int kSlotsAtOnce = 8;
 
-// The rows (and weights) of up to eight slots of a token. CTAs walk over the tokens and
-// read the next token's ahead: looked up when they were needed, they put a second memory
-// latency before every token's rows (32768 rows of 2048: 27 us to add up).
+// The rows (and weights) of up to eight slots of a token, lane j's of slot j0 + j. CTAs
+// walk over the tokens and read the next token's ahead: looked up when they were needed,
+// they put a second memory latency before every token's rows (32768 rows of 2048: 27 us to
+// add up); in every lane's registers all eight, they spilled.
 template <bool kWeighted>
 struct Slots {
-  int32_t r[kSlotsAtOnce];
-  float w[kSlotsAtOnce];
+  int32_t r;
+  float w;
   __device__ __forceinline__ void load(const RouteArgs& a, int64_t t, int64_t T, int j0) {
+    const int j = j0 + (threadIdx.x & 31);
+    const bool in = t < T && j < j0 + kSlotsAtOnce && j < a.topk;
+    r = in ? a.rows[t * a.topk + j] : -1;
+    w = kWeighted && in ? a.weights[t * a.topk + j] : 0.0f;
+    if (r >= a.R) r = -1;
+    if (r < 0) w = 0.0f;  // whatever it is: the slot adds nothing
+  }
+  __device__ __forceinline__ void spread(int32_t (&rows)[kSlotsAtOnce], float (&weights)[kSlotsAtOnce]) const {
 #pragma unroll
     for (int j = 0; j < kSlotsAtOnce; ++j) {
-      const bool in = t < T && j0 + j < a.topk;
-      r[j] = in ? a.rows[t * a.topk + j0 + j] : -1;
-      w[j] = kWeighted && in ? a.weights[t * a.topk + j0 + j] : 1.0f;
-      if (r[j] >= a.R) r[j] = -1;
+      rows[j] = __shfl_sync(0xffffffffu, r, j);
+      if (kWeighted) weights[j] = __shfl_sync(0xffffffffu, w, j);
     }
   }
 };
@@ -251,32 +258,40 @@ __global__ void __launch_bounds__(kRowThreads, 4)
     combine_kernel(const uint16_t* Y, const RouteArgs a, int64_t T, uint16_t* out) {
   pdl_launch_dependents();
   pdl_wait();
+  const int N = static_cast<int>(a.N), threads = static_cast<int>(blockDim.x);
+  const int cols = (N + kVec - 1) / kVec, rounds = (cols + threads - 1) / threads;
   Slots<kWeighted> next;
   next.load(a, blockIdx.x, T, 0);
   for (int64_t t = blockIdx.x; t < T; t += gridDim.x) {
     const Slots<kWeighted> first = next;
     next.load(a, t + gridDim.x, T, 0);
-    for (int64_t n = static_cast<int64_t>(threadIdx.x) * kVec; n < a.N; n += static_cast<int64_t>(blockDim.x) * kVec) {
+    for (int k = 0; k < rounds; ++k) {  // (whole warps, for the shuffles)
+      const int c = k * threads + static_cast<int>(threadIdx.x);
+      const uint16_t* const y = Y + kVec * c;
       float acc[kVec] = {};
       for (int j0 = 0; j0 < a.topk; j0 += kSlotsAtOnce) {
         Slots<kWeighted> s = first;
         if (j0) s.load(a, t, T, j0);
+        int32_t r[kSlotsAtOnce];
+        float w[kSlotsAtOnce];
+        s.spread(r, w);
         Vec<kVec> v[kSlotsAtOnce];
 #pragma unroll
-        for (int j = 0; j < kSlotsAtOnce; ++j)
-          if (s.r[j] >= 0) v[j].load(Y + s.r[j] * a.N + n);
-#pragma unroll
         for (int j = 0; j < kSlotsAtOnce; ++j) {
-          if (s.r[j] < 0) continue;
+          v[j] = {};
+          if (r[j] >= 0 && c < cols) v[j].load(y + static_cast<int64_t>(r[j]) * N);
+        }
+#pragma unroll
+        for (int j = 0; j < kSlotsAtOnce; ++j) {  // (a slot left out adds 0 times zeros)
           float f[kVec];
           v[j].get(f);
 #pragma unroll
-          for (int i = 0; i < kVec; ++i) acc[i] += kWeighted ? s.w[j] * f[i] : f[i];
+          for (int i = 0; i < kVec; ++i) acc[i] += kWeighted ? w[j] * f[i] : f[i];
         }
       }
       Vec<kVec> o;
       o.set(acc);
-      o.store(out + t * a.N + n);
+      if (c < cols) o.store(out + t * N + kVec * c);
     }
   }
 }
@@ -289,36 +304,41 @@ __global__ void __launch_bounds__(kRowThreads, 3)
   pdl_wait();
   __shared__ float red[2][kRowThreads / 32][kSlotsAtOnce];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = static_cast<int>(blockDim.x) >> 5;
+  const int N = static_cast<int>(a.N);
   int buf = 0;
   Slots<true> next;
   next.load(a, blockIdx.x, T, 0);
   for (int64_t t = blockIdx.x; t < T; t += gridDim.x) {
     for (int j0 = 0; j0 < a.topk; j0 += kSlotsAtOnce, buf ^= 1) {
-      const Slots<true> s = next;
+      int32_t r[kSlotsAtOnce];
+      float w[kSlotsAtOnce];
+      next.spread(r, w);
       const bool more = j0 + kSlotsAtOnce < a.topk;
       next.load(a, more ? t : t + gridDim.x, T, more ? j0 + kSlotsAtOnce : 0);
       float dot[kSlotsAtOnce] = {};
-      for (int64_t n = static_cast<int64_t>(threadIdx.x) * kVec; n < a.N; n += static_cast<int64_t>(blockDim.x) * kVec) {
+      for (int n = static_cast<int>(threadIdx.x) * kVec; n < N; n += static_cast<int>(blockDim.x) * kVec) {
         Vec<kVec> v, y[kSlotsAtOnce];
-        v.load(dout + t * a.N + n);
+        v.load(dout + t * N + n);
 #pragma unroll
-        for (int j = 0; j < kSlotsAtOnce; ++j)
-          if (s.r[j] >= 0) y[j].load(Y + s.r[j] * a.N + n);
+        for (int j = 0; j < kSlotsAtOnce; ++j) {
+          y[j] = {};
+          if (r[j] >= 0) y[j].load(Y + n + static_cast<int64_t>(r[j]) * N);
+        }
         float g[kVec];
         v.get(g);
 #pragma unroll
         for (int j = 0; j < kSlotsAtOnce; ++j) {
-          if (s.r[j] < 0) continue;
+          if (r[j] < 0) continue;  // (its gradient is 0, whatever dout holds)
           float f[kVec], p[kVec];
           y[j].get(f);
 #pragma unroll
           for (int i = 0; i < kVec; ++i) {
             dot[j] += g[i] * f[i];
-            p[i] = s.w[j] * g[i];
+            p[i] = w[j] * g[i];
           }
           Vec<kVec> d;
           d.set(p);
-          d.store(dY + s.r[j] * a.N + n);
+          d.store(dY + n + static_cast<int64_t>(r[j]) * N);
         }
       }
       // lanes by a fixed tree, then warps in order (two buffers: one barrier a round)

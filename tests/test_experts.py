@@ -490,3 +490,28 @@ def test_experts_of_very_different_sizes(L, orc, fmt, T, topk, E, N, K, skew):
         x = X[(slots[off[e]:off[e + 1]] // topk).long()].double()
         _check_rows(Y[off[e]:off[e + 1]], x @ W.t(), x.abs() @ W.abs().t(), True)
     assert L.lbq_device_fault() == 0
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("topk", [3, 11])
+@pytest.mark.parametrize("N", [64, 77])
+def test_weights_of_slots_left_out_do_not_count(L, topk, N):
+    """A slot without a row adds nothing and has no gradient, whatever its weight is."""
+    T, R = 9, 40
+    g = torch.Generator().manual_seed(11)
+    Y = torch.randn(R, N, generator=g).to(torch.bfloat16).cuda()
+    dout = torch.randn(T, N, generator=g).to(torch.bfloat16).cuda()
+    rows = torch.randperm(T * topk, generator=g).view(T, topk).to(torch.int32)
+    rows[rows >= R] = -1
+    rows[2] = -1
+    rows[3, 0] = R
+    w = torch.rand(T, topk, generator=g)
+    keep = (rows >= 0) & (rows < R)
+    clean = torch.where(keep, w, torch.zeros(()))
+    bad = torch.where(keep, w, torch.tensor([float("nan"), float("inf")])[torch.arange(topk) % 2].expand(T, topk))
+    rows, bad, clean = rows.cuda(), bad.cuda().contiguous(), clean.cuda()
+    out = L.lbq_expert_combine(Y, rows, bad)
+    assert out.isfinite().all() and (out[2] == 0).all()
+    assert torch.equal(out, L.lbq_expert_combine(Y, rows, clean))
+    dY, dw = L.lbq_expert_combine_grad(dout, Y, rows, bad, dY=torch.zeros_like(Y))
+    assert dY.isfinite().all() and dw.isfinite().all() and (dw.cpu()[~keep] == 0).all()
