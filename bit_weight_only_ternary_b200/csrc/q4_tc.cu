@@ -214,14 +214,18 @@ __device__ __forceinline__ void plan_tiles(const Args& a, int ntn, int* __restri
   if (lane == 0) plan[E] = run;
 }
 
+// Lanes that share a weight row group's scales: experts have many groups of few scales (128
+// experts of 2048 x 1536, 512 tokens: 95.5 us with a warp a group, 89.8 with eight lanes).
+__host__ __device__ inline int scale_lanes(int ns) { return ns <= 64 ? 8 : 32; }
+
 // The first blocks convert activation rows to fp16, kRow threads a row (exact power-of-two
 // scaling, flag if not exact): a whole block for few long rows, where latency counts, a
 // warp for many (a block a row took 107 us for 32768 rows of 2048, most of it launching
 // blocks; a warp 45). An expert's rows are written once each, in their order, so that one
 // copy brings a block of a tile: with the tokens converted once and the rows gathered by
 // the product, 4096 tokens x 8 took 334 us by asynchronous copies of 16 bytes and 535 by
-// four-row tensor copies, where this takes 223. The blocks behind take groups of four weight rows, one a warp: the exponent
-// that brings a row's largest scale to [2^11, 2^12).
+// four-row tensor copies, where this takes 222. The blocks behind take groups of four
+// weight rows: the exponent that brings a row's largest scale to [2^11, 2^12).
 template <int kRow>
 __global__ void __launch_bounds__(256, 8)
     q4_prepare_kernel(const Args a, uint16_t* __restrict__ Xh, int* __restrict__ xexp,
@@ -238,26 +242,31 @@ __global__ void __launch_bounds__(256, 8)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int64_t xblocks = (static_cast<int64_t>(a.M) + kRows - 1) / kRows;
   if (static_cast<int64_t>(blockIdx.x) >= xblocks) {
-    const int64_t grp = (static_cast<int64_t>(blockIdx.x) - xblocks) * 8 + warp;
-    if (grp >= ngroups) return;
-    const uint2* s = reinterpret_cast<const uint2*>(a.scales + grp * 4 * a.scale_stride);
-    const int ns = static_cast<int>(a.K / group);
-    uint32_t m01 = 0, m23 = 0;
-#pragma unroll 4
-    for (int e = lane; e < ns; e += 32) {
-      const uint2 v = __ldg(s + e);
-      m01 = __vmaxu2(m01, v.x & 0x7fff7fffu);
-      m23 = __vmaxu2(m23, v.y & 0x7fff7fffu);
+    const int ns = static_cast<int>(a.K / group), width = scale_lanes(ns), l = lane & (width - 1);
+    const int64_t grp = (static_cast<int64_t>(blockIdx.x) - xblocks) * (256 / width) + threadIdx.x / width;
+    bool used = grp < ngroups;
+    if (used && a.offsets) {  // experts without rows need none
+      const int e = static_cast<int>(grp) / a.groups;
+      used = __ldg(a.offsets + e) < __ldg(a.offsets + e + 1);
     }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
+    uint32_t m01 = 0, m23 = 0;
+    if (used) {
+      const uint2* s = reinterpret_cast<const uint2*>(a.scales + grp * 4 * a.scale_stride);
+#pragma unroll 4
+      for (int e = l; e < ns; e += width) {
+        const uint2 v = __ldg(s + e);
+        m01 = __vmaxu2(m01, v.x & 0x7fff7fffu);
+        m23 = __vmaxu2(m23, v.y & 0x7fff7fffu);
+      }
+    }
+    for (int o = width / 2; o > 0; o >>= 1) {
       m01 = __vmaxu2(m01, __shfl_xor_sync(0xffffffffu, m01, o));
       m23 = __vmaxu2(m23, __shfl_xor_sync(0xffffffffu, m23, o));
     }
-    if (lane < 4) {
-      const uint32_t h = (lane & 2 ? m23 : m01) >> (16 * (lane & 1)) & 0xffffu;
+    if (used && l < 4) {
+      const uint32_t h = (l & 2 ? m23 : m01) >> (16 * (l & 1)) & 0xffffu;
       // an infinite or NaN scale makes its row's outputs so whatever the exponent
-      wexp[grp * 4 + lane] = h == 0 ? 0 : (h >= 0x7c00u ? 4 : max(-30, ilogbf(f16_bits_to_f32(static_cast<uint16_t>(h))) - 11));
+      wexp[grp * 4 + l] = h == 0 ? 0 : (h >= 0x7c00u ? 4 : max(-30, ilogbf(f16_bits_to_f32(static_cast<uint16_t>(h))) - 11));
     }
     return;
   }
@@ -1050,7 +1059,8 @@ cudaError_t launch(const lbq_weights* w, const Plan& plan, const lbq_expert_rows
     return cudaErrorInvalidValue;
 
   a.kb_split = plan.kb_split;
-  const unsigned wblocks = static_cast<unsigned>((static_cast<int64_t>(E) * ng + 7) / 8);
+  const int per_block = 256 / scale_lanes(static_cast<int>(w->K / kG));
+  const unsigned wblocks = static_cast<unsigned>((static_cast<int64_t>(E) * ng + per_block - 1) / per_block);
   const int ngroups = static_cast<int>(E * ng);
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
