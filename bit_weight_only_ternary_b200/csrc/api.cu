@@ -146,10 +146,10 @@ lbq_status check_routing(int64_t T, int32_t topk, int32_t E) {
 
 // The experts' products: few rows an expert run on the warp-level matrix instructions,
 // more on the tensor cores. The routing is on the device, so the rule takes the average.
-// Measured: 128 experts of 2048 x 1536, 8 rows each 76.7 / 84.2 us, 9 rows 83.0 / 84.3, 10
-// rows 88.0 / 84.8; 16 of 5120 x 5120, 8 rows 82.1 / 86.6, 10 rows 90.9 / 86.5; 8 of 2048 x
-// 1024, 6 rows 15.1 / 16.5, 12 rows 17.1 / 16.5.
-inline bool expert_few(int32_t E, int64_t R) { return R <= 9 * static_cast<int64_t>(E); }
+// Measured: 128 experts of 2048 x 1536, 7 rows each 70.6 / 77.0 us, 8 rows 77.0 / 78.0, 9
+// rows 83.2 / 78.8; 16 of 5120 x 5120, 8 rows 82.1 / 87.5, 9 rows 85.6 / 87.5; 8 of 2048 x
+// 1024, 6 rows 15.1 / 16.5, 8 rows 16.5 / 16.4.
+inline bool expert_few(int32_t E, int64_t R) { return R <= 8 * static_cast<int64_t>(E); }
 
 // E matrices of one format and shape behind one another (4-bit formats).
 lbq_status check_expert_weights(const lbq_weights* w, int32_t E, Layout* L) {
