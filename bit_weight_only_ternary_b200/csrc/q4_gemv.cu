@@ -88,6 +88,34 @@ __device__ __forceinline__ void mma_bf16_first(float (&d)[4], const uint32_t (&a
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.0f));
 }
 
+// Division by a number the host knows: a product with ceil(2^(31 + l) / d), l = ceil(log2 d),
+// and a shift, exact for 0 <= n < 2^31 (the product's error is below n d / 2^(31 + l) / d <
+// 1 / d). A run's start has half a dozen divisions one after another, and a division by a
+// variable takes some hundred cycles.
+struct Div {
+  uint32_t d, mul;
+  int shift;
+  Div() = default;
+  explicit Div(int64_t v) : d(static_cast<uint32_t>(v)) {
+    int l = 0;
+    while ((int64_t{1} << l) < v) ++l;
+    shift = 31 + l;
+    mul = static_cast<uint32_t>(((uint64_t{1} << shift) + v - 1) / v);
+  }
+  __device__ __forceinline__ int operator()(int n) const {
+    return static_cast<int>((static_cast<uint64_t>(static_cast<uint32_t>(n)) * mul) >> shift);
+  }
+  __device__ __forceinline__ int64_t wide(int64_t n) const {  // any n >= 0
+    return (n >> 31) == 0 ? (*this)(static_cast<int>(n)) : n / d;
+  }
+};
+
+// a / b for a >= 0, b > 0 of any size: in 32 bits where they fit.
+__device__ __forceinline__ int64_t quot(int64_t a, int64_t b) {
+  if (((a | b) >> 32) == 0) return static_cast<uint32_t>(a) / static_cast<uint32_t>(b);
+  return a / b;
+}
+
 // ---------------------------------------------------------------- where the tiles are
 // A source gives the tiles of its products (or experts): tiles and chunks of product p,
 // the lane's pointers into tile i, and where its outputs go.
@@ -110,12 +138,16 @@ struct Q4Prod {
   int64_t q0;          // chunks of the products before
   int64_t gcode;       // code bytes per group of four rows
   int32_t gscale;      // scales per group of four rows
-  int32_t N, nc;       // rows; chunks of a tile
+  int32_t N;           // rows
+  Div nc;              // chunks of a tile
 };
 
 template <int kCap>
 struct Q4List {
   int64_t chunks;
+  int64_t share;       // chunks a CTA; the first `extra` CTAs take one more
+  int32_t extra;
+  Div ntok;            // token tiles
   float* part;         // workspace: parts of tiles cut by a run's end
   unsigned* count;     // arrivals on such a tile (zero before and after)
   int32_t n, M;
@@ -129,8 +161,10 @@ struct ListSource {
   const Q4List<kCap>& a;
   __device__ __forceinline__ int64_t chunks() const { return a.chunks; }
   __device__ __forceinline__ int64_t start(int p) const { return a.p[p].q0; }
-  __device__ __forceinline__ int nc(int p) const { return a.p[p].nc; }
-  __device__ __forceinline__ int ntok() const { return kTok == 1 ? 1 : (a.M + kTok - 1) / kTok; }
+  __device__ __forceinline__ const Div& nc(int p) const { return a.p[p].nc; }
+  __device__ __forceinline__ int64_t share(int) const { return a.share; }
+  __device__ __forceinline__ int extra(int) const { return a.extra; }
+  __device__ __forceinline__ int ntok() const { return kTok == 1 ? 1 : static_cast<int>(a.ntok.d); }
   __device__ __forceinline__ int tiles(int p) const { return (a.p[p].N + kRowTile - 1) / kRowTile * ntok(); }
   __device__ __forceinline__ int next(int p) const { return p + 1; }
   __device__ __forceinline__ int find(int64_t q) const {
@@ -147,20 +181,20 @@ struct ListSource {
   __device__ __forceinline__ void point(int p, int i, int lane, bool, LanePtr& l) const {
     const Q4Prod& P = a.p[p];
     const int g = lane >> 2, t = lane & 3, ng = (P.N + 3) >> 2;
-    const int rt = kTok == 1 ? i : i / ntok(), m = (i - rt * ntok()) * kTok + g;  // token tiles run fastest
+    const int rt = kTok == 1 ? i : a.ntok(i), m = (i - rt * ntok()) * kTok + g;  // token tiles run fastest
     const int64_t grp = rt * (kRowTile / 4);
     l.w = P.codes + grp * P.gcode;
     l.s = P.scales + grp * P.gscale;
     l.gcode = P.gcode;
     l.gscale = P.gscale;
     l.groups = ng - static_cast<int>(grp);
-    const int64_t K = static_cast<int64_t>(P.nc) * kQ4Chunk;
+    const int64_t K = static_cast<int64_t>(P.nc.d) * kQ4Chunk;
     l.x0 = kTok == 1 ? P.x + 8 * lane : (g < kTok && m < a.M ? P.x + m * K + 8 * t : nullptr);
     l.zero = false;
   }
   __device__ __forceinline__ void store(int p, int i, int m, int r, float v) const {
     const Q4Prod& P = a.p[p];
-    const int rt = kTok == 1 ? i : i / ntok(), row = rt * kRowTile + r;
+    const int rt = kTok == 1 ? i : a.ntok(i), row = rt * kRowTile + r;
     m += (i - rt * ntok()) * kTok;
     if (m >= a.M || row >= P.N) return;
     const int64_t o = static_cast<int64_t>(m) * P.N + row;
@@ -173,7 +207,8 @@ struct Q4Experts {
   const uint8_t* codes;
   const uint16_t* scales;
   int64_t gcode, ecode, escale;  // code bytes per group, per expert; scales per expert
-  int32_t gscale, N, nc;
+  int32_t gscale, N;
+  Div nc, ntn, topk;             // chunks of a tile, row tiles
   lbq_expert_rows r;
   float* part;
   unsigned* count;
@@ -188,17 +223,19 @@ struct ExpertSource {
   const Q4Experts& a;
   const int* off;  // [E + 1] first rows, clamped (shared memory)
   const int* pre;  // [E + 1] tiles of the experts before
-  __device__ __forceinline__ int ntn() const { return (a.N + kRowTile - 1) / kRowTile; }
-  __device__ __forceinline__ int64_t chunks() const { return static_cast<int64_t>(pre[a.r.E]) * a.nc; }
-  __device__ __forceinline__ int64_t start(int e) const { return static_cast<int64_t>(pre[e]) * a.nc; }
-  __device__ __forceinline__ int nc(int) const { return a.nc; }
+  __device__ __forceinline__ int ntn() const { return static_cast<int>(a.ntn.d); }
+  __device__ __forceinline__ int64_t chunks() const { return static_cast<int64_t>(pre[a.r.E]) * a.nc.d; }
+  __device__ __forceinline__ int64_t share(int grid) const { return quot(chunks(), grid); }
+  __device__ __forceinline__ int extra(int grid) const { return static_cast<int>(chunks() - share(grid) * grid); }
+  __device__ __forceinline__ int64_t start(int e) const { return static_cast<int64_t>(pre[e]) * a.nc.d; }
+  __device__ __forceinline__ const Div& nc(int) const { return a.nc; }
   __device__ __forceinline__ int tiles(int e) const { return pre[e + 1] - pre[e]; }
   __device__ __forceinline__ int next(int e) const {
     do ++e; while (e < a.r.E && pre[e + 1] == pre[e]);
     return e;
   }
   __device__ __forceinline__ int find(int64_t q) const {
-    const int tile = static_cast<int>(q / a.nc);
+    const int tile = static_cast<int>(a.nc.wide(q));
     int lo = 0, hi = a.r.E;  // the last expert with pre[e] <= tile (the ones before it may be empty)
     while (hi - lo > 1) {
       const int mid = (lo + hi) >> 1;
@@ -208,7 +245,7 @@ struct ExpertSource {
   }
   // (next: the lane stood in the tile before this one, which mostly has the same tokens)
   __device__ __forceinline__ void point(int e, int i, int lane, bool next, LanePtr& l) const {
-    const int g = lane >> 2, t = lane & 3, ng = (a.N + 3) >> 2, nt = i / ntn(), rt = i - nt * ntn();
+    const int g = lane >> 2, t = lane & 3, ng = (a.N + 3) >> 2, nt = a.ntn(i), rt = i - nt * ntn();
     const int64_t grp = rt * (kRowTile / 4);
     l.w = a.codes + e * a.ecode + grp * a.gcode;
     l.s = a.scales + e * a.escale + grp * a.gscale;
@@ -223,14 +260,14 @@ struct ExpertSource {
       int64_t src = row;
       if (a.r.slots) {
         const int slot = __ldcg(a.r.slots + row);
-        src = slot < 0 ? -1 : slot / a.r.topk;
+        src = slot < 0 ? -1 : a.topk(slot);
       }
       l.zero = src < 0 || src >= a.r.T;  // a slot of no token: a row of zeros
-      if (!l.zero) l.x0 = a.r.X + src * (static_cast<int64_t>(a.nc) * kQ4Chunk) + 8 * t;
+      if (!l.zero) l.x0 = a.r.X + src * (static_cast<int64_t>(a.nc.d) * kQ4Chunk) + 8 * t;
     }
   }
   __device__ __forceinline__ void store(int e, int i, int m, int r, float v) const {
-    const int nt = i / ntn(), row = (i - nt * ntn()) * kRowTile + r, y = off[e] + nt * kTok + m;
+    const int nt = a.ntn(i), row = (i - nt * ntn()) * kRowTile + r, y = off[e] + nt * kTok + m;
     if (y < off[e + 1] && row < a.N) a.r.Y[static_cast<int64_t>(y) * a.N + row] = f32_to_bf16_bits(v);
   }
 };
@@ -249,13 +286,6 @@ struct Slot {  // (kDepth a warp)
   static constexpr int kDepth = 2;
 };
 
-// a / b for a >= 0, b > 0: in 32 bits where they fit (a 64-bit division takes some hundred
-// instructions, and a run's start and end have a dozen).
-__device__ __forceinline__ int64_t quot(int64_t a, int64_t b) {
-  if (((a | b) >> 32) == 0) return static_cast<uint32_t>(a) / static_cast<uint32_t>(b);
-  return a / b;
-}
-
 // A place in the line of chunks: chunk c of tile i of product p.
 struct Place {
   int p, i, c;
@@ -265,8 +295,8 @@ __device__ __forceinline__ Place place_of(const Src& src, int64_t q) {
   Place a;
   a.p = src.find(q);
   const int64_t r = q - src.start(a.p);
-  a.i = static_cast<int>(quot(r, src.nc(a.p)));
-  a.c = static_cast<int>(r - static_cast<int64_t>(a.i) * src.nc(a.p));
+  a.i = static_cast<int>(src.nc(a.p).wide(r));
+  a.c = static_cast<int>(r - static_cast<int64_t>(a.i) * src.nc(a.p).d);
   return a;
 }
 
@@ -281,23 +311,24 @@ __device__ __forceinline__ void stream_tiles(const Src& src, float* part, unsign
   float (*ends)[2][kOut] = reinterpret_cast<float (*)[2][kOut]>(slots);
   static_assert(2 * kOut * sizeof(float) <= S::kDepth * S::kBytes, "ends do not fit");
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-  const int64_t W = src.chunks();
   const int b = static_cast<int>(blockIdx.x);
   if (b >= grid) return;
   // The CTA's chunks: an equal share, its ends moved to the nearest start of a tile where
   // tiles are short (then no tile is joined across CTAs, some 2 us at the end: experts with
   // K = 2048, three tokens 20.1 us to 18.6, 64 tokens 54 us to 51; but shares that differ by
   // half a tile of K = 5120 cost as much as they saved).
-  const int64_t share = quot(W, grid);
+  const int64_t share = src.share(grid);
+  const int extra = src.extra(grid);
   auto bound = [&](int i) {
-    const int64_t q = quot(W * i, grid);
+    const int64_t q = i * share + (i < extra ? i : extra);
     if (i == 0 || i == grid) return q;
     const Place a = place_of(src, q);
-    const int nc = src.nc(a.p);
+    const int nc = static_cast<int>(src.nc(a.p).d);
     if (nc > 24 || 6 * static_cast<int64_t>(nc) > share) return q;
     return 2 * a.c < nc ? q - a.c : q + (nc - a.c);
   };
-  const int64_t c0 = bound(b), c1 = bound(b + 1);
+  const int64_t bounds = bound(b + (lane & 1));  // (two lanes' work, side by side)
+  const int64_t c0 = __shfl_sync(0xffffffffu, bounds, 0), c1 = __shfl_sync(0xffffffffu, bounds, 1);
   auto run_start = [&](int w) { return c0 + (c1 - c0) * w / kWarps; };
 
   // --- fetching: chunks 0 .. n - 1 of this warp's run
@@ -320,7 +351,7 @@ __device__ __forceinline__ void stream_tiles(const Src& src, float* part, unsign
     if (kG == 32) l.s += static_cast<int64_t>(f.c) * 16 + (lo >> 1) * static_cast<int64_t>(l.gscale) + 8 * (lo & 1);
     else l.s += static_cast<int64_t>(f.c) * 4 + (lane & 7) * static_cast<int64_t>(l.gscale);
     if (l.x) l.x += static_cast<int64_t>(f.c) * kQ4Chunk;
-    left = src.nc(f.p) - f.c;
+    left = static_cast<int>(src.nc(f.p).d) - f.c;
   };
   if (n > 0) point(false);
   auto fetch_w = [&](uint32_t d) {
@@ -394,7 +425,7 @@ __device__ __forceinline__ void stream_tiles(const Src& src, float* part, unsign
   const int head_c = u.c;
   float acc[2][4], first[2][4];  // first: the sums of place 0
   for (int q = 0; q < n;) {
-    const int nc = src.nc(u.p);
+    const int nc = static_cast<int>(src.nc(u.p).d);
     const int qe = nc - u.c < n - q ? q + (nc - u.c) : n;
 #pragma unroll
     for (int i = 0; i < 8; ++i) acc[i >> 2][i & 3] = 0.0f;
@@ -479,17 +510,27 @@ __device__ __forceinline__ void stream_tiles(const Src& src, float* part, unsign
   // --- tiles that several warps share: joined by the warp in whose run the tile (or the
   // CTA's part of it) begins
   auto join = [&](const Place& at, int64_t qt, int which) {
-    const int nc = src.nc(at.p);
-    const int64_t qn = qt + nc;
-    float v[kTok];  // row `lane` of every token
+    const int64_t qn = qt + src.nc(at.p).d;
+    float v[kTok], next[kTok];  // row `lane` of every token
 #pragma unroll
     for (int m = 0; m < kTok; ++m) v[m] = ends[warp][which][m * kRowTile + lane];
-    for (int w = warp + 1; w < kWarps; ++w) {
-      const int64_t s0 = starts[w];
-      if (s0 >= qn) break;
-      if (s0 == starts[w + 1]) continue;  // an empty run
+    // the later warps whose runs, if not empty, begin inside the tile; a part's loads are
+    // in flight while the one before is added
+    const int64_t s0 = starts[lane < kWarps ? lane : kWarps], s1 = starts[lane < kWarps ? lane + 1 : kWarps];
+    unsigned more = __ballot_sync(0xffffffffu, lane > warp && s0 < qn && s0 < s1);
+    auto fetch_part = [&]() {
 #pragma unroll
-      for (int m = 0; m < kTok; ++m) v[m] += ends[w][0][m * kRowTile + lane];
+      for (int m = 0; m < kTok; ++m) next[m] = ends[__ffs(more) - 1][0][m * kRowTile + lane];
+    };
+    if (more) fetch_part();
+    while (more) {
+      float part[kTok];
+#pragma unroll
+      for (int m = 0; m < kTok; ++m) part[m] = next[m];
+      more &= more - 1;
+      if (more) fetch_part();
+#pragma unroll
+      for (int m = 0; m < kTok; ++m) v[m] += part[m];
     }
     if (which == 1 && qn <= c1) {
 #pragma unroll
@@ -500,8 +541,11 @@ __device__ __forceinline__ void stream_tiles(const Src& src, float* part, unsign
 #pragma unroll
     for (int m = 0; m < kTok; ++m) __stcg(part + static_cast<int64_t>(2 * b + which) * kOut + m * kRowTile + lane, v[m]);
     __syncwarp();
-    auto cta_of = [&](int64_t q) { return static_cast<int>(quot((q + 1) * grid - 1, W)); };
-    const int first = cta_of(qt), parts = cta_of(qn - 1) - first + 1;
+    auto cta_of = [&](int64_t q) {
+      const int64_t r = q - extra * (share + 1);
+      return static_cast<int>(r < 0 ? quot(q, share + 1) : extra + quot(r, share));
+    };
+    const int first = which == 1 ? b : cta_of(qt), parts = cta_of(qn - 1) - first + 1;
     unsigned before = 0;
     // (one atomic that releases this warp's stores and acquires the others')
     if (lane == 0)
@@ -620,6 +664,9 @@ cudaError_t launch_list(Q4List<kCap>& a, void* ws, cudaStream_t s) {
   a.count = static_cast<unsigned*>(ws);
   const int64_t runs = (a.chunks + kWarps - 1) / kWarps;
   const unsigned grid = static_cast<unsigned>(runs < most_runs() ? runs : most_runs());
+  a.share = a.chunks / grid;
+  a.extra = static_cast<int32_t>(a.chunks % grid);
+  a.ntok = Div((a.M + kTok - 1) / kTok);
   const cudaError_t e = allow_smem<q4_list_kernel<kG, kTok, kCap, kF32>>(smem);
   return e != cudaSuccess ? e : launch_pdl(q4_list_kernel<kG, kTok, kCap, kF32>, smem, grid, s, a);
 }
@@ -643,8 +690,8 @@ Q4Prod make_prod(const lbq_weights& w, const uint16_t* x, void* y, int64_t* q0, 
   p.gcode = 4 * w.code_stride;
   p.gscale = static_cast<int32_t>(4 * w.scale_stride);
   p.N = static_cast<int32_t>(w.N);
-  p.nc = static_cast<int32_t>(w.K / kQ4Chunk);
-  *q0 += (w.N + kRowTile - 1) / kRowTile * ntok * p.nc;
+  p.nc = Div(w.K / kQ4Chunk);
+  *q0 += (w.N + kRowTile - 1) / kRowTile * ntok * p.nc.d;
   return p;
 }
 
@@ -697,7 +744,9 @@ cudaError_t lbq_launch_q4_expert_few(const lbq_weights* w, const lbq_expert_rows
   a.ecode = ng * a.gcode;
   a.escale = ng * a.gscale;
   a.N = static_cast<int32_t>(w->N);
-  a.nc = static_cast<int32_t>(w->K / kQ4Chunk);
+  a.nc = Div(w->K / kQ4Chunk);
+  a.ntn = Div((w->N + kRowTile - 1) / kRowTile);
+  a.topk = Div(r.topk);
   a.r = r;
   a.part = part_of(ws);
   a.count = static_cast<unsigned*>(ws);
