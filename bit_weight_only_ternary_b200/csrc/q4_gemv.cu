@@ -157,6 +157,7 @@ struct Q4List {
 template <int kCap, int kTok, bool kF32>
 struct ListSource {
   static constexpr bool kZeros = false;
+  static constexpr bool kWarpFind = false;  // (see ExpertSource)
   static constexpr bool kEarly = true;  // the list and the weights are known before the previous kernel ends
   const Q4List<kCap>& a;
   __device__ __forceinline__ int64_t chunks() const { return a.chunks; }
@@ -219,6 +220,7 @@ struct Q4Experts {
 template <int kTok>
 struct ExpertSource {
   static constexpr bool kZeros = true;  // slots may name no token
+  static constexpr bool kWarpFind = true;  // find() is the whole warp's, for one q
   static constexpr bool kEarly = false;
   const Q4Experts& a;
   const int* off;  // [E + 1] first rows, clamped (shared memory)
@@ -235,13 +237,14 @@ struct ExpertSource {
     return e;
   }
   __device__ __forceinline__ int find(int64_t q) const {
-    const int tile = static_cast<int>(a.nc.wide(q));
-    int lo = 0, hi = a.r.E;  // the last expert with pre[e] <= tile (the ones before it may be empty)
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      if (pre[mid] <= tile) lo = mid; else hi = mid;
-    }
-    return lo;
+    // the last expert with pre[e] <= tile (the ones before it may be empty): one count, 32
+    // experts at a time (a search by halves takes a dependent load a step)
+    const int tile = static_cast<int>(a.nc.wide(q)), lane = threadIdx.x & 31;
+    int n = 0;
+#pragma unroll 4
+    for (int e0 = 0; e0 < a.r.E; e0 += 32)
+      n += __popc(__ballot_sync(0xffffffffu, e0 + lane < a.r.E && pre[e0 + lane] <= tile));
+    return n - 1;
   }
   // (next: the lane stood in the tile before this one, which mostly has the same tokens)
   __device__ __forceinline__ void point(int e, int i, int lane, bool next, LanePtr& l) const {
@@ -327,8 +330,15 @@ __device__ __forceinline__ void stream_tiles(const Src& src, float* part, unsign
     if (nc > 24 || 6 * static_cast<int64_t>(nc) > share) return q;
     return 2 * a.c < nc ? q - a.c : q + (nc - a.c);
   };
-  const int64_t bounds = bound(b + (lane & 1));  // (two lanes' work, side by side)
-  const int64_t c0 = __shfl_sync(0xffffffffu, bounds, 0), c1 = __shfl_sync(0xffffffffu, bounds, 1);
+  int64_t c0, c1;
+  if (Src::kWarpFind) {
+    c0 = bound(b);
+    c1 = bound(b + 1);
+  } else {  // two lanes' work, side by side
+    const int64_t bounds = bound(b + (lane & 1));
+    c0 = __shfl_sync(0xffffffffu, bounds, 0);
+    c1 = __shfl_sync(0xffffffffu, bounds, 1);
+  }
   auto run_start = [&](int w) { return c0 + (c1 - c0) * w / kWarps; };
 
   // --- fetching: chunks 0 .. n - 1 of this warp's run
@@ -586,34 +596,46 @@ __global__ void __launch_bounds__(kThreads, 1)
   int* const pre = off + a.r.E + 1;                                                                           // [E + 1]
   pdl_launch_dependents();
   pdl_wait();
-  const int R = static_cast<int>(a.r.R), E = a.r.E;
-  for (int e = threadIdx.x; e <= E; e += kThreads) {
+  // Tiles before each expert: a running sum over the warp, then over the warps. Offsets that
+  // descend somewhere would name rows twice, and more tiles than are counted in 32 bits: no
+  // row then.
+  __shared__ int wsum[kWarps];
+  const int R = static_cast<int>(a.r.R), E = a.r.E, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  auto clamped = [&](int e) {
     const int v = __ldcg(a.r.offsets + e);
-    off[e] = v < 0 ? 0 : (v > R ? R : v);
-  }
-  __syncthreads();
-  if (threadIdx.x < 32) {  // tiles before each expert: a running sum, 32 experts at a time
-    const int lane = threadIdx.x, ntn = (a.N + kRowTile - 1) / kRowTile;
-    int run = 0;
-    bool down = false;
-    for (int e0 = 0; e0 < E; e0 += 32) {
-      const int e = e0 + lane, rows = e < E ? off[e + 1] - off[e] : 0;
-      const int c = rows > 0 ? (rows + kTok - 1) / kTok * ntn : 0;
-      down = down || rows < 0;
-      int inc = c;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int v = __shfl_up_sync(0xffffffffu, inc, o);
-        if (lane >= o) inc += v;
-      }
-      if (e < E) pre[e] = run + inc - c;
-      run += __shfl_sync(0xffffffffu, inc, 31);
+    return v < 0 ? 0 : (v > R ? R : v);
+  };
+  int run = 0;
+  bool down = false;
+  for (int e0 = 0; e0 < E; e0 += kThreads) {
+    const int e = e0 + threadIdx.x;
+    int c = 0;
+    if (e < E) {
+      const int r0 = clamped(e), r1 = clamped(e + 1);
+      off[e] = r0;
+      if (e == E - 1) off[E] = r1;
+      down = down || r1 < r0;
+      c = r1 > r0 ? (r1 - r0 + kTok - 1) / kTok * static_cast<int>(a.ntn.d) : 0;
     }
-    // Offsets that descend somewhere would name rows twice, and more tiles than are counted
-    // in 32 bits: no row then.
-    down = __any_sync(0xffffffffu, down);
-    if (lane == 0) pre[E] = down ? 0 : run;
+    int inc = c;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, inc, o);
+      if (lane >= o) inc += v;
+    }
+    if (lane == 31) wsum[warp] = inc;
+    down = __syncthreads_or(down);
+    int before = 0, all = 0;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+      if (w < warp) before += wsum[w];
+      all += wsum[w];
+    }
+    if (e < E) pre[e] = run + before + inc - c;
+    run += all;
+    if (e0 + kThreads < E) __syncthreads();  // (wsum is written again)
   }
+  if (threadIdx.x == 0) pre[E] = down ? 0 : run;
   __syncthreads();
   if (pre[E] == 0) return;
   const ExpertSource<kTok> src = {a, off, pre};

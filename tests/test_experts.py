@@ -515,3 +515,25 @@ def test_weights_of_slots_left_out_do_not_count(L, topk, N):
     assert torch.equal(out, L.lbq_expert_combine(Y, rows, clean))
     dY, dw = L.lbq_expert_combine_grad(dout, Y, rows, bad, dY=torch.zeros_like(Y))
     assert dY.isfinite().all() and dw.isfinite().all() and (dw.cpu()[~keep] == 0).all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("fmt", [5, 6])
+@pytest.mark.parametrize("E,T,topk", [(1000, 40, 2), (1024, 1, 5), (513, 600, 3), (700, 3000, 4)])
+def test_as_many_experts_as_there_may_be(L, fmt, E, T, topk):
+    """More experts than threads, most or none of them without rows."""
+    N, K = 9, 128
+    ew = L.pack_experts(fmt, (torch.randn(E, N, K, generator=torch.Generator().manual_seed(12)) * 0.02).cuda())
+    X = synth.activations(T, K, 13).cuda()
+    ids = _ids(T, topk, E, 14, 0.05).cuda()
+    offsets, rows, slots = L.lbq_expert_sort(ids, E)
+    Y = L.lbq_expert_gemm(ew, X, offsets, slots=slots, topk=topk)
+    one = [L.lbq_unpack(L.PackedWeights(fmt, K, N, ew.codes[e], ew.scales[e])) for e in range(E)]
+    W = torch.stack([a.double() * b.double().repeat_interleave(K // b.shape[1], 1) for a, b in one])
+    r, e = rows.flatten().long(), ids.flatten().long()
+    keep = e >= 0
+    x = X.double().repeat_interleave(topk, 0)[keep]
+    want = torch.einsum("rnk,rk->rn", W[e[keep]], x)
+    S = torch.einsum("rnk,rk->rn", W[e[keep]].abs(), x.abs())
+    _check_rows(Y[r[keep]], want, S, True)
+    assert L.lbq_device_fault() == 0
