@@ -340,16 +340,18 @@ def workspace_for_batch(plist: ProductList, device=None) -> torch.Tensor:
     return torch.zeros(((n + 15) // 16) * 16, dtype=torch.uint8, device=dev)
 
 
-def _arg(where: str, t, dtype, shape=None):
+def _args(where: str, *specs):
     """The expert calls take dense tensors of one type on the current device: anything
-    else is refused here (the C call sees pointers only)."""
-    if t is None:
-        return
-    if t.dtype is not dtype or not t.is_cuda or not t.is_contiguous() \
-            or t.get_device() != torch.cuda.current_device():
-        _check(LBQ_ERR_ARG, where)
-    if shape is not None and t.shape != shape:
-        _check(LBQ_ERR_SHAPE, where)
+    else is refused here (the C call sees pointers only). specs: (tensor or None, dtype,
+    shape or None)."""
+    dev = torch.cuda.current_device()
+    for t, dtype, shape in specs:
+        if t is None:
+            continue
+        if t.dtype is not dtype or t.get_device() != dev or not t.is_contiguous():
+            _check(LBQ_ERR_ARG, where)
+        if shape is not None and t.shape != shape:
+            _check(LBQ_ERR_SHAPE, where)
 
 
 @dataclass
@@ -389,11 +391,8 @@ def lbq_expert_sort(expert: torch.Tensor, E: int, offsets=None, rows=None, slots
     """expert int32 or int64 [T][topk] -> (offsets int32 [E+1], rows int32 [T][topk], slots
     int32 [T*topk]): a stable sort of the slots by expert (ids outside 0..E-1 left out)."""
     T, topk = expert.shape
-    w = "lbq_expert_sort"
-    _arg(w, expert, torch.int64 if expert.dtype is torch.int64 else torch.int32)
-    _arg(w, offsets, torch.int32, (E + 1,))
-    _arg(w, rows, torch.int32, (T, topk))
-    _arg(w, slots, torch.int32, (T * topk,))
+    _args("lbq_expert_sort", (expert, torch.int64 if expert.dtype is torch.int64 else torch.int32, None),
+          (offsets, torch.int32, (E + 1,)), (rows, torch.int32, (T, topk)), (slots, torch.int32, (T * topk,)))
     if offsets is None:
         offsets = torch.empty(E + 1, dtype=torch.int32, device=expert.device)
     if rows is None:
@@ -411,13 +410,10 @@ def lbq_expert_dispatch(X: torch.Tensor, rows: torch.Tensor, weights=None, out=N
     R = T * topk (rows behind the last sorted one are then uninitialised)."""
     T, K = X.shape
     topk = rows.shape[1]
-    w = "lbq_expert_dispatch"
-    _arg(w, X, torch.bfloat16)
-    _arg(w, rows, torch.int32, (T, topk))
-    _arg(w, weights, torch.float32, (T, topk))
-    if out is not None:
-        _arg(w, out, torch.bfloat16, (out.shape[0], K))
-    else:
+    _args("lbq_expert_dispatch", (X, torch.bfloat16, None), (rows, torch.int32, (T, topk)),
+          (weights, torch.float32, (T, topk)),
+          (out, torch.bfloat16, None if out is None else (out.shape[0], K)))
+    if out is None:
         out = torch.empty((T * topk, K), dtype=torch.bfloat16, device=X.device)
     _check(_lib.lbq_expert_dispatch(_ptr(X), T, K, _ptr(rows), topk, _ptr(weights), out.shape[0],
                                     _ptr(out), _stream(stream)), "lbq_expert_dispatch")
@@ -429,11 +425,8 @@ def lbq_expert_combine(Y: torch.Tensor, rows: torch.Tensor, weights=None, out=No
     """bf16 out [T][N]: out[t] = sum_j (weights[t][j] *) Y[rows[t][j]] for bf16 Y [R][N]."""
     R, N = Y.shape
     T, topk = rows.shape
-    w = "lbq_expert_combine"
-    _arg(w, Y, torch.bfloat16)
-    _arg(w, rows, torch.int32)
-    _arg(w, weights, torch.float32, (T, topk))
-    _arg(w, out, torch.bfloat16, (T, N))
+    _args("lbq_expert_combine", (Y, torch.bfloat16, None), (rows, torch.int32, None),
+          (weights, torch.float32, (T, topk)), (out, torch.bfloat16, (T, N)))
     if out is None:
         out = torch.empty((T, N), dtype=torch.bfloat16, device=Y.device)
     _check(_lib.lbq_expert_combine(_ptr(Y), R, N, _ptr(rows), T, topk, _ptr(weights), _ptr(out),
@@ -447,13 +440,9 @@ def lbq_expert_combine_grad(dout: torch.Tensor, Y: torch.Tensor, rows: torch.Ten
     of dY that no slot names are left as they were (uninitialised in a new dY)."""
     R, N = Y.shape
     T, topk = rows.shape
-    w = "lbq_expert_combine_grad"
-    _arg(w, Y, torch.bfloat16)
-    _arg(w, dout, torch.bfloat16, (T, N))
-    _arg(w, rows, torch.int32)
-    _arg(w, weights, torch.float32, (T, topk))
-    _arg(w, dY, torch.bfloat16, (R, N))
-    _arg(w, dweights, torch.float32, (T, topk))
+    _args("lbq_expert_combine_grad", (Y, torch.bfloat16, None), (dout, torch.bfloat16, (T, N)),
+          (rows, torch.int32, None), (weights, torch.float32, (T, topk)), (dY, torch.bfloat16, (R, N)),
+          (dweights, torch.float32, (T, topk)))
     if dY is None:
         dY = torch.empty((R, N), dtype=torch.bfloat16, device=Y.device)
     if dweights is None:
@@ -484,10 +473,8 @@ def lbq_expert_gemm(ew: ExpertWeights, X: torch.Tensor, offsets: torch.Tensor, s
     T = X.shape[0]
     w = "lbq_expert_gemm"
     R = Y.shape[0] if Y is not None else (T if slots is None else slots.shape[0])
-    _arg(w, X, torch.bfloat16, (T, ew.K))
-    _arg(w, offsets, torch.int32, (ew.E + 1,))
-    _arg(w, slots, torch.int32, (R,))
-    _arg(w, Y, torch.bfloat16, (R, ew.N))
+    _args(w, (X, torch.bfloat16, (T, ew.K)), (offsets, torch.int32, (ew.E + 1,)), (slots, torch.int32, (R,)),
+          (Y, torch.bfloat16, (R, ew.N)))
     dev = X.get_device()
     if ew.codes.get_device() != dev or (workspace is not None and workspace.get_device() != dev):
         _check(LBQ_ERR_ARG, w)
