@@ -114,10 +114,13 @@ struct Args {
   unsigned* fault;
 };
 
+// What an earlier kernel of the stream may still be writing when this one starts (early) is
+// read after the wait, from L2 or by plain loads: not through the read-only path, which
+// __ldg takes for weights.
 // Source row of sorted row r: its slot's token, or -1.
 __device__ __forceinline__ int64_t source_row(const int32_t* slots, int topk, int64_t T, int64_t r) {
   if (slots) {
-    const int32_t s = __ldg(slots + r);
+    const int32_t s = __ldcg(slots + r);
     r = s < 0 ? -1 : s / topk;
   }
   return r < T ? r : -1;
@@ -142,7 +145,7 @@ __device__ __forceinline__ void plan_tiles(const Args& a, int ntn, int* __restri
   __shared__ int off[LBQ_MAX_EXPERTS + 1], hist[kChunks][kClasses], sum[kClasses];
   __shared__ short order[LBQ_MAX_EXPERTS];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, E = a.E;
-  for (int e = tid; e <= E; e += 256) off[e] = clamp_row(__ldg(a.offsets + e), a.M);
+  for (int e = tid; e <= E; e += 256) off[e] = clamp_row(__ldcg(a.offsets + e), a.M);
   for (int i = tid; i < kChunks * kClasses; i += 256) (&hist[0][0])[i] = 0;
   __syncthreads();
   // Offsets that descend somewhere would name rows twice, and more tiles than are counted
@@ -247,7 +250,7 @@ __global__ void __launch_bounds__(256, 8)
     bool used = grp < ngroups;
     if (used && a.offsets) {  // experts without rows need none
       const int e = static_cast<int>(grp) / a.groups;
-      used = __ldg(a.offsets + e) < __ldg(a.offsets + e + 1);
+      used = a.offsets[e] < a.offsets[e + 1];  // (cached: many blocks read the same)
     }
     uint32_t m01 = 0, m23 = 0;
     if (used) {
@@ -276,7 +279,7 @@ __global__ void __launch_bounds__(256, 8)
   if (m >= a.M) return;
   int64_t src = m;
   if (a.offsets) {
-    if (m >= clamp_row(__ldg(a.offsets + a.E), a.M)) return;
+    if (m >= clamp_row(__ldcg(a.offsets + a.E), a.M)) return;
     src = source_row(a.slots, a.topk, a.T, m);
   }
   uint4* hr = reinterpret_cast<uint4*>(Xh + m * a.K);
@@ -476,7 +479,7 @@ __device__ __forceinline__ void fixup_flagged(const Args& a, const Info& t, cons
 #pragma unroll
             for (int q = 0; q < 8; ++q) {
               const int v = static_cast<int>((c >> (4 * ((q >> 1) + 4 * (q & 1)))) & 15u) - 8;
-              p += static_cast<float>(v) * bf16_bits_to_f32(__ldg(x + 8 * wi + q));
+              p += static_cast<float>(v) * bf16_bits_to_f32(__ldcg(x + 8 * wi + q));
             }
           }
           acc += s * p;
@@ -538,9 +541,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int ntn = (a.N + 2 * kTileN - 1) / (2 * kTileN);
   if (a.offsets)
     for (int e = tid; e <= a.E; e += kThreads) {
-      off[e] = clamp_row(__ldg(a.offsets + e), a.M);
-      pre[e] = __ldg(a.plan + e);
-      if (e < a.E) order[e] = static_cast<uint16_t>(__ldg(a.plan + a.E + 1 + e));
+      off[e] = clamp_row(__ldcg(a.offsets + e), a.M);
+      pre[e] = __ldcg(a.plan + e);
+      if (e < a.E) order[e] = static_cast<uint16_t>(__ldcg(a.plan + a.E + 1 + e));
     }
   tc_fence_before_sync();
   __syncthreads();
@@ -670,12 +673,12 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
       for (int x = 0; x < kMaxTileM / 32; ++x) {
         const int m = 32 * x + lane;
-        e[x] = m < t.cnt ? __ldg(a.xexp + t.m0 + m) : 0;
-        f[x] = m < t.cnt ? __ldg(a.xflag + t.m0 + m) : 0;
+        e[x] = m < t.cnt ? __ldcg(a.xexp + t.m0 + m) : 0;
+        f[x] = m < t.cnt ? __ldcg(a.xflag + t.m0 + m) : 0;
       }
 #pragma unroll
       for (int x = 0; x < kTileN / 32; ++x)
-        we[x] = t.n0 + 32 * x + lane < a.N ? __ldg(a.wexp + row0 + 32 * x + lane) : 0;
+        we[x] = t.n0 + 32 * x + lane < a.N ? __ldcg(a.wexp + row0 + 32 * x + lane) : 0;
       bool ok = mbar_wait(emptyI + 8 * s, ((k / kInfos) & 1) ^ 1, a.fault, kFaultEpilogue);
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
