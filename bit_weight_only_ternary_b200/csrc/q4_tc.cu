@@ -32,7 +32,7 @@
 //            accumulators have been read), the tile's epilogue
 // Every wait is bounded (sm100_async.cuh). Measured: 4096 tokens x 5120 x 34816 in 0.92 to
 // 1.07 ms (1.59 to 1.36 PFLOP/s, by the power that is left), 333 x 5120 x 7001 in 30 us, 4096
-// tokens x 8 of 128 experts of 2048 x 1536 in 261 us (790 TFLOP/s), 45 of them the
+// tokens x 8 of 128 experts of 2048 x 1536 in 260 us (790 TFLOP/s), 45 of them the
 // preparation. A block of 128 K cannot take less than 0.27 us: the tensor cores read its
 // weights, 128 x 128 a CTA, from tensor memory in 8 x 64 cycles.
 #include <cudaTypedefs.h>
