@@ -537,3 +537,53 @@ def test_as_many_experts_as_there_may_be(L, fmt, E, T, topk):
     S = torch.einsum("rnk,rk->rn", W[e[keep]].abs(), x.abs())
     _check_rows(Y[r[keep]], want, S, True)
     assert L.lbq_device_fault() == 0
+
+
+@pytest.mark.gpu
+def test_expert_offsets_past_32_bits(L):
+    """The last expert of matrices of more than 2^32 bytes (random codes)."""
+    fmt, g, E, N, K = 5, 32, 64, 9600, 16384
+    cs, ss, _, _ = L.lbq_packed_layout(fmt, K, N)
+    gen = torch.Generator("cuda").manual_seed(5)
+    c = torch.randint(0, 256, (E, N // 4, 4 * cs), dtype=torch.uint8, device="cuda", generator=gen)
+    assert c.numel() > 2 ** 32
+    s = (torch.rand(E, N // 4, 4 * ss, device="cuda", generator=gen) * 0.01 + 0.001).half().view(torch.int16)
+    ew = L.ExpertWeights(fmt, K, N, E, c, s)
+    q, sc = L.lbq_unpack(L.PackedWeights(fmt, K, N, c[-1], s[-1]))
+    W = q.double() * sc.double().repeat_interleave(g, 1)
+    for T in (8, 700):
+        X = synth.activations(T, K, 6).cuda()
+        ids = _ids(T, 2, E, 7).cuda()
+        ids[0, 0] = ids[T - 1, 1] = E - 1
+        offsets, rows, slots = L.lbq_expert_sort(ids, E)
+        Y = L.lbq_expert_gemm(ew, X, offsets, slots=slots, topk=2)
+        a = int(offsets[E - 1])
+        x = X[(slots[a:] // 2).long()].double()
+        _check_rows(Y[a:], x @ W.t(), x.abs() @ W.abs().t(), True)
+    assert L.lbq_device_fault() == 0
+
+
+@pytest.mark.gpu
+def test_rows_past_32_bits(L):
+    """More than 2^31 values in the rows' buffers."""
+    T, topk, N, E = 33000, 8, 8192, 16
+    part = torch.randn(1000, N, generator=torch.Generator().manual_seed(8)).to(torch.bfloat16).cuda()
+    Y = part.repeat(T * topk // 1000, 1)
+    assert Y.numel() > 2 ** 31
+    ids = torch.randint(0, E, (T, topk), generator=torch.Generator().manual_seed(9)).cuda()
+    offsets, rows, slots = L.lbq_expert_sort(ids, E)
+    assert torch.equal(slots.long(), torch.argsort(ids.flatten(), stable=True))
+    w = torch.rand(T, topk, generator=torch.Generator().manual_seed(10)).cuda()
+    out = L.lbq_expert_combine(Y, rows, w)
+    dY, dw = L.lbq_expert_combine_grad(out, Y, rows, w)
+    last = int(slots[-1]) // topk  # the token of the last row
+    for t in (0, last, T - 1):
+        y, o, c = Y[rows[t].long()].double(), out[t].double(), w[t].double()[:, None]
+        want = (c * y).sum(0)
+        assert ((o - want).abs() <= 2.0 ** -8 * want.abs() + 2.0 ** -20 * (c * y.abs()).sum(0)).all()
+        # fp32 sums of 8192 products in a tree of short sums: far below 2^-16 of their magnitudes
+        assert ((dw[t].double() - y @ o).abs() <= 2.0 ** -16 * (y.abs() @ o.abs())).all()
+        assert ((dY[rows[t].long()].double() - c * o).abs() <= 2.0 ** -8 * (c * o).abs()).all()
+    del dY, Y
+    x = L.lbq_expert_dispatch(out, rows)
+    assert torch.equal(x[-1], out[last]) and torch.equal(x[rows[T - 1].long()], out[T - 1].expand(topk, N))

@@ -358,3 +358,44 @@ def test_tensor_parallel_shards(L, orc, fmt):
         s = tp.make_shard(W, fmt, "row", r, world, pack)
         part += L.lbq_gemv_f32(s.weights, x[s.lo:s.hi])
     _inside(part, Y[0], S[0], "row", rounded=False)
+
+
+@pytest.mark.gpu
+def test_offsets_past_32_bits(L):
+    """Codes of more than 2^32 bytes (random ones, any code is a weight): the last rows."""
+    fmt, g, K, N = 6, 128, 16384, 600_004
+    cs, ss, _, _ = L.lbq_packed_layout(fmt, K, N)
+    gen = torch.Generator("cuda").manual_seed(5)
+    c = torch.randint(0, 256, (N // 4, 4 * cs), dtype=torch.uint8, device="cuda", generator=gen)
+    assert c.numel() > 2 ** 32
+    s = (torch.rand(N // 4, 4 * ss, device="cuda", generator=gen) * 0.01 + 0.001).half().view(torch.int16)
+    pw = L.PackedWeights(fmt, K, N, c, s)
+    q, sc = L.lbq_unpack(L.PackedWeights(fmt, K, 400, c[-100:].contiguous(), s[-100:].contiguous()))
+    W = q.double() * sc.double().repeat_interleave(g, 1)
+    for M in (1, 5, 40):
+        X = synth.activations(M, K, 6).cuda()
+        Y = L.lbq_gemv(pw, X[0])[None] if M == 1 else L.lbq_gemm(pw, X)
+        want, S = X.double() @ W.t(), X.double().abs() @ W.abs().t()
+        assert ((Y[:, -400:].double() - want).abs() <= 2.0 ** -8 * want.abs() + (2.0 ** -12 + 2.0 ** -11) * S).all(), M
+    assert L.lbq_device_fault() == 0
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("fmt", Q4)
+@pytest.mark.parametrize("M", [1, 6, 40, 300])
+@pytest.mark.parametrize("N", [64, 65])
+def test_outputs_at_odd_addresses(L, orc, fmt, M, N):
+    """Y two bytes off every wider boundary (K long enough to be split), nothing around it
+    written."""
+    K = 5120
+    pw, X, Y, S = _make(L, orc, fmt, N, K, M, 81)
+    buf = torch.full((M * N + 18,), 7.0, dtype=torch.bfloat16, device="cuda")
+    y = buf[9:9 + M * N].view(M, N)
+    if M == 1:
+        L.lbq_gemv(pw, X[0], y=y[0])
+    else:
+        L.lbq_gemm(pw, X, Y=y)
+    _inside(y, Y, S, "odd", f16=M > 8)
+    assert (buf[:9] == 7).all() and (buf[9 + M * N:] == 7).all()
+    z = torch.empty(M, N, dtype=torch.bfloat16, device="cuda")
+    assert torch.equal(y, L.lbq_gemm(pw, X, Y=z) if M > 1 else L.lbq_gemv(pw, X[0], y=z[0])[None])
