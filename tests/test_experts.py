@@ -587,3 +587,53 @@ def test_rows_past_32_bits(L):
     del dY, Y
     x = L.lbq_expert_dispatch(out, rows)
     assert torch.equal(x[-1], out[last]) and torch.equal(x[rows[T - 1].long()], out[T - 1].expand(topk, N))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T", [1, 5, 90])
+def test_a_chain_of_every_kind_of_call(L, T):
+    """Ternary, 4-bit and expert calls, each reading what the one before wrote, enqueued
+    without a pause: the bits of the same calls with a wait after each (the kernels start
+    early beside their predecessors)."""
+    H, F, E, topk = 512, 1024, 16, 3
+    g = torch.Generator().manual_seed(15)
+    rnd = lambda *s: (torch.randn(*s, generator=g) * 0.05).cuda()
+    tern, q4a, q4b = L.lbq_pack(1, rnd(H, H)), L.lbq_pack(5, rnd(F, H)), L.lbq_pack(6, rnd(H, F))
+    up, down = L.pack_experts(6, rnd(E, F, H)), L.pack_experts(5, rnd(E, H, F))
+    X0 = synth.activations(T, H, 16).cuda()
+    idss = [_ids(T, topk, E, 17 + i, 0.1).cuda() for i in range(8)]
+    w = torch.rand(T, topk, generator=g).cuda()
+    R = T * topk
+    new = lambda *s, dt=torch.bfloat16: torch.zeros(*s, dtype=dt, device="cuda")
+    ws = {id(p): L.workspace_for(p, T) for p in (tern, q4a, q4b)}
+    wse = {id(p): L.workspace_for_experts(p, R) for p in (up, down)}
+    a, b, c, h, y, x = new(T, H), new(T, F), new(T, H), new(R, F), new(R, H), new(T, H)
+    off, rows, slots = new(E + 1, dt=torch.int32), new(T, topk, dt=torch.int32), new(R, dt=torch.int32)
+
+    def product(p, src, dst):
+        if T == 1:
+            L.lbq_gemv(p, src[0], y=dst[0], workspace=ws[id(p)])
+        else:
+            L.lbq_gemm(p, src, Y=dst, workspace=ws[id(p)])
+
+    def run(wait):
+        x.copy_(X0)
+        for ids in idss:
+            for step in (lambda: product(tern, x, a), lambda: product(q4a, a, b), lambda: product(q4b, b, c),
+                         lambda: L.lbq_expert_sort(ids, E, off, rows, slots),
+                         lambda: L.lbq_expert_gemm(up, c, off, slots=slots, topk=topk, Y=h, workspace=wse[id(up)]),
+                         lambda: L.lbq_expert_gemm(down, h, off, Y=y, workspace=wse[id(down)]),
+                         lambda: L.lbq_expert_combine(y, rows, w, out=x),
+                         lambda: L.lbq_expert_dispatch(x, rows, out=y),
+                         lambda: L.lbq_expert_combine(y, rows, None, out=x)):
+                step()
+                if wait:
+                    torch.cuda.synchronize()
+            x.mul_(0.25 * X0.float().norm() / x.float().norm())
+        return x.clone()
+
+    want = run(True)
+    assert want.isfinite().all() and want.float().norm() > 0
+    for _ in range(10):
+        assert torch.equal(run(False), want)
+    assert L.lbq_device_fault() == 0
