@@ -403,7 +403,9 @@ cudaError_t launch_sort(const Id* ids, int64_t R, int32_t E, int32_t* offsets, i
       },
       &done);
   if (e != cudaSuccess) return e;
-  const int C = R <= 8 * kSortThreads ? 1 : kSortCluster;
+  // one CTA for few slots, a cluster for more (128 experts, one / eight CTAs: 64 slots 3.3 /
+  // 3.7 us, 512 3.9 / 4.3, 1024 4.8 / 4.4, 4096 9.4 / 4.3, 32768 68 / 9.7)
+  const int C = R <= kSortThreads ? 1 : kSortCluster;
   const int64_t warps = static_cast<int64_t>(C) * kSortWarps;
   const int64_t per_warp = ((R + warps - 1) / warps + 31) / 32 * 32;
   cudaLaunchConfig_t cfg = {};

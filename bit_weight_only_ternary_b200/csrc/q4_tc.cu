@@ -221,10 +221,16 @@ __device__ __forceinline__ void plan_tiles(const Args& a, int ntn, int* __restri
 // experts of 2048 x 1536, 512 tokens: 95.5 us with a warp a group, 89.8 with eight lanes).
 __host__ __device__ inline int scale_lanes(int ns) { return ns <= 64 ? 8 : 32; }
 
+// Rows are converted by a block each, or by a warp each where they are many and short (a
+// block's launch, some 3 ns, is then more than a row's share of the time). Measured, whole
+// products, a warp / a block: 512 x 2048, 600 rows 14.6 / 16.5 us, 2000 rows 16.5 / 26.8; 2048 x
+// 1536, 1000 rows 19.9 / 18.5, 2500 rows 27.8 / 28.0; 5120 x 5120, 333 rows 34.9 / 26.8, 8192
+// rows 337 / 333; 17408 x 2048, 2000 rows 146 / 116; the conversion of 32768 rows of 2048 45 /
+// 107.
+inline bool warp_a_row(int64_t K, int64_t rows) { return K <= 4096 && rows >= K; }
+
 // The first blocks convert activation rows to fp16, kRow threads a row (exact power-of-two
-// scaling, flag if not exact): a whole block for few long rows, where latency counts, a
-// warp for many (a block a row took 107 us for 32768 rows of 2048, most of it launching
-// blocks; a warp 45). An expert's rows are written once each, in their order, so that one
+// scaling, flag if not exact). An expert's rows are written once each, in their order, so that one
 // copy brings a block of a tile: with the tokens converted once and the rows gathered by
 // the product, 4096 tokens x 8 took 334 us by asynchronous copies of 16 bytes and 535 by
 // four-row tensor copies, where this takes 222. The blocks behind take groups of four
@@ -1069,7 +1075,7 @@ cudaError_t launch(const lbq_weights* w, const Plan& plan, const lbq_expert_rows
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
-  const bool many = rows >= 8 * sm_count();  // enough rows for every SM at eight a block
+  const bool many = warp_a_row(w->K, rows);
   cfg.gridDim = dim3(static_cast<unsigned>(many ? (rows + 7) / 8 : rows) + wblocks + (er ? 1 : 0));
   cfg.blockDim = dim3(256);
   cfg.stream = s;
