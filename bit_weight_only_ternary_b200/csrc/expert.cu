@@ -17,7 +17,7 @@ using namespace lbq;
 namespace cg = cooperative_groups;
 
 constexpr int kSortThreads = 512, kSortWarps = kSortThreads / 32;
-constexpr int kSortCluster = 8;
+constexpr int kSortCluster = 8, kSortMost = 16;  // CTAs of a cluster
 // Slots of a warp's run that stay in registers, 32 at a time (a run of more is read twice).
 constexpr int kSortKeep = 8;
 
@@ -105,11 +105,11 @@ __global__ void __launch_bounds__(kSortThreads, 1)
     const int e = e0 + tid;
     int32_t all = 0, before = 0;
     if (e < E) {
-      int32_t v[kSortCluster];
+      int32_t v[kSortMost];
 #pragma unroll
-      for (int c = 0; c < kSortCluster; ++c) v[c] = c < C ? *cluster.map_shared_rank(tot + e, c) : 0;
+      for (int c = 0; c < kSortMost; ++c) v[c] = c < C ? *cluster.map_shared_rank(tot + e, c) : 0;
 #pragma unroll
-      for (int c = 0; c < kSortCluster; ++c) {
+      for (int c = 0; c < kSortMost; ++c) {
         all += v[c];
         if (c < rank) before += v[c];
       }
@@ -407,19 +407,27 @@ bool vec8(int64_t N, const void* a, const void* b, const void* c = nullptr, cons
 template <typename Id>
 cudaError_t launch_sort(const Id* ids, int64_t R, int32_t E, int32_t* offsets, int32_t* rows,
                         int32_t* slots, cudaStream_t s) {
-  static PerDevice<bool> configured;
-  bool done = false;
-  cudaError_t e = configured.get(
-      [](int, bool* v) {
-        *v = true;
-        return cudaFuncSetAttribute(expert_sort_kernel<Id>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                    (kSortWarps + 2) * LBQ_MAX_EXPERTS * 4);
+  static PerDevice<int> configured;  // CTAs of the largest cluster this device takes
+  int largest = 0;
+  const cudaError_t e = configured.get(
+      [](int, int* v) {
+        constexpr int smem = (kSortWarps + 2) * LBQ_MAX_EXPERTS * 4;
+        cudaError_t r = cudaFuncSetAttribute(expert_sort_kernel<Id>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+        if (r == cudaSuccess)
+          r = cudaFuncSetAttribute(expert_sort_kernel<Id>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        if (r != cudaSuccess) return r;
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3(kSortMost);
+        cfg.blockDim = dim3(kSortThreads);
+        cfg.dynamicSmemBytes = smem;
+        return cudaOccupancyMaxPotentialClusterSize(v, expert_sort_kernel<Id>, &cfg);
       },
-      &done);
+      &largest);
   if (e != cudaSuccess) return e;
   // one CTA for few slots, a cluster for more (128 experts, one / eight CTAs: 64 slots 3.3 /
-  // 3.7 us, 512 3.9 / 4.3, 1024 4.8 / 4.4, 4096 9.4 / 4.3, 32768 68 / 9.7)
-  const int C = R <= kSortThreads ? 1 : kSortCluster;
+  // 3.7 us, 512 3.9 / 4.3, 1024 4.8 / 4.4, 4096 9.4 / 4.3; eight / sixteen: 16384 slots 6.6 /
+  // 5.4, 32768 9.6 / 6.9, 262144 56 / 30)
+  const int C = R <= kSortThreads ? 1 : (R <= 8192 || largest < kSortMost ? kSortCluster : kSortMost);
   const int64_t warps = static_cast<int64_t>(C) * kSortWarps;
   const int64_t per_warp = ((R + warps - 1) / warps + 31) / 32 * 32;
   cudaLaunchConfig_t cfg = {};
