@@ -304,15 +304,16 @@ __global__ void __launch_bounds__(256, 8)
 #pragma unroll
   for (int i = 0; i < kKeep; ++i) kept[i] = u + i * kRow < K8 ? xr[u + i * kRow] : make_uint4(0, 0, 0, 0);
   // largest and smallest non-zero magnitude, as bf16 bits in both halves (the smallest less
-  // one, so that zeros come last; a zero low half borrows one more from the high half, which
-  // only makes the row's flag more careful)
+  // one, so that zeros, 0xffff, come last; a magnitude's top bit is zero and is set while
+  // the one is taken off, so that no half borrows from the other: borrowed bits hid a 2^-133
+  // above a zero and flagged every row of zeros)
   uint32_t mb = 0, sb = 0xffffffffu;
   auto largest = [&](const uint4& v) {
     const uint32_t w[4] = {v.x & 0x7fff7fffu, v.y & 0x7fff7fffu, v.z & 0x7fff7fffu, v.w & 0x7fff7fffu};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       mb = __vmaxu2(mb, w[i]);
-      sb = __vminu2(sb, w[i] - 0x00010001u);
+      sb = __vminu2(sb, ((w[i] | 0x80008000u) - 0x00010001u) ^ 0x80008000u);
     }
   };
 #pragma unroll
