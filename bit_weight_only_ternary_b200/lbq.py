@@ -357,7 +357,9 @@ def _args(where: str, *specs):
 @dataclass
 class ExpertWeights:
     """E packed K x N matrices of one 4-bit format: codes uint8 [E][ceil(N/4)][4 *
-    code_stride], scales fp16 (as int16) [E][ceil(N/4)][4 * scale_stride]."""
+    code_stride], scales fp16 (as int16) [E][ceil(N/4)][4 * scale_stride]. Both are dense:
+    the matrices lie behind one another (a choice of experts, codes[::2], is copied first:
+    codes[::2].contiguous())."""
     fmt: int
     K: int
     N: int
@@ -366,9 +368,17 @@ class ExpertWeights:
     scales: torch.Tensor
 
     def desc(self) -> lbq_weights:
+        """The C call's descriptor. Raises LbqError unless both tensors are of the shape
+        above, dense, and of one-byte and two-byte values: it takes a pointer to expert 0
+        and finds the others by these sizes."""
+        for t, size in ((self.codes, 1), (self.scales, 2)):
+            if t.dim() != 3 or t.shape[0] != self.E or t.shape[1] != (self.N + 3) // 4 or t.shape[2] % 4:
+                _check(LBQ_ERR_SHAPE, "ExpertWeights")
+            if t.element_size() != size or not t.is_contiguous():
+                _check(LBQ_ERR_ARG, "ExpertWeights")
         return lbq_weights(self.fmt, 0, self.K, self.N, self.codes.data_ptr(),
-                           self.scales.data_ptr(), self.codes.stride(1) // 4,
-                           self.scales.stride(1) // 4)
+                           self.scales.data_ptr(), self.codes.shape[2] // 4,
+                           self.scales.shape[2] // 4)
 
 
 def pack_experts(fmt: int, W: torch.Tensor, stream=None) -> ExpertWeights:
@@ -476,14 +486,16 @@ def lbq_expert_gemm(ew: ExpertWeights, X: torch.Tensor, offsets: torch.Tensor, s
     _args(w, (X, torch.bfloat16, (T, ew.K)), (offsets, torch.int32, (ew.E + 1,)), (slots, torch.int32, (R,)),
           (Y, torch.bfloat16, (R, ew.N)))
     dev = X.get_device()
-    if ew.codes.get_device() != dev or (workspace is not None and workspace.get_device() != dev):
+    if ew.codes.get_device() != dev or ew.scales.get_device() != dev:
         _check(LBQ_ERR_ARG, w)
+    if workspace is not None and (workspace.get_device() != dev or not workspace.is_contiguous()):
+        _check(LBQ_ERR_ARG, w)
+    d = ew.desc()
     if Y is None:
         Y = torch.empty((R, ew.N), dtype=torch.bfloat16, device=X.device)
     if workspace is None:
         workspace = workspace_for_experts(ew, R, X.device)
     wsb = 0 if workspace is None else workspace.numel() * workspace.element_size()
-    d = ew.desc()
     _check(_lib.lbq_expert_gemm(ctypes.byref(d), ew.E, _ptr(X), T, _ptr(offsets), _ptr(slots), topk,
                                 R, _ptr(Y), _ptr(workspace), wsb, _stream(stream)),
            "lbq_expert_gemm")

@@ -85,3 +85,55 @@ def test_rows_of_zeros_take_no_longer(L, experts):
     zeros = _us(run)
     assert (Y[::2] == 0).all() and torch.equal(Y[1::2], full[1::2])
     assert zeros <= 2 * ordinary, f"{zeros:.1f} us, {ordinary:.1f} without rows of zeros"
+
+
+# --------------------------------------------------------------- the experts' weights
+
+def _blank_experts(L, fmt, E, N, K, device="cpu"):
+    cs, ss, _, _ = L.lbq_packed_layout(fmt, K, N)
+    G = (N + 3) // 4
+    return L.ExpertWeights(fmt, K, N, E, torch.zeros(E, G, 4 * cs, dtype=torch.uint8, device=device),
+                           torch.zeros(E, G, 4 * ss, dtype=torch.int16, device=device))
+
+
+@pytest.mark.parametrize("fmt", [5, 6])
+def test_experts_that_do_not_lie_behind_one_another_are_refused(L, fmt):
+    """The C call sees a pointer to expert 0 and sizes: a strided choice of experts, more
+    experts than there are, or tensors of other shapes or types would be read elsewhere."""
+    E, N, K = 6, 10, 256
+    ew = _blank_experts(L, fmt, E, N, K)
+    c, s = ew.codes, ew.scales
+    make = lambda **kw: L.ExpertWeights(**{**dict(fmt=fmt, K=K, N=N, E=E, codes=c, scales=s), **kw})  # noqa: E731
+    assert L.lbq_expert_workspace_bytes(ew, 8) > 0
+    half = make(E=3, codes=c[::2].contiguous(), scales=s[::2].contiguous())
+    assert L.lbq_expert_workspace_bytes(half, 8) > 0
+    assert half.desc().code_stride == ew.desc().code_stride
+    for kw, status in ((dict(E=3, codes=c[::2], scales=s[::2]), L.LBQ_ERR_ARG),
+                       (dict(E=3, codes=c[::2].contiguous(), scales=s[::2]), L.LBQ_ERR_ARG),
+                       (dict(E=7), L.LBQ_ERR_SHAPE), (dict(E=5), L.LBQ_ERR_SHAPE),
+                       (dict(scales=s[:5]), L.LBQ_ERR_SHAPE), (dict(codes=c[:, 1:].contiguous()), L.LBQ_ERR_SHAPE),
+                       (dict(N=14), L.LBQ_ERR_SHAPE), (dict(codes=c[0]), L.LBQ_ERR_SHAPE),
+                       (dict(codes=c.short()), L.LBQ_ERR_ARG), (dict(scales=s.int()), L.LBQ_ERR_ARG),
+                       (dict(codes=c[:, :, 1:].contiguous()), L.LBQ_ERR_SHAPE)):
+        with pytest.raises(L.LbqError) as e:
+            L.lbq_expert_workspace_bytes(make(**kw), 8)
+        assert e.value.status == status, kw.keys()
+    # one row group: whatever stride a dimension of one element claims
+    one = _blank_experts(L, fmt, 1, 4, K)
+    odd = L.ExpertWeights(fmt, K, 4, 1, one.codes.as_strided(one.codes.shape, (7, 5, 1)), one.scales)
+    assert odd.desc().code_stride == one.desc().code_stride == K // 2
+
+
+@pytest.mark.gpu
+def test_scales_on_the_host_are_refused(L):
+    import dataclasses
+    ew = _blank_experts(L, 5, 2, 8, 128, "cuda")
+    X = synth.activations(4, 128, 3).cuda()
+    off = torch.tensor([0, 2, 4], dtype=torch.int32, device="cuda")
+    for bad in (dataclasses.replace(ew, scales=ew.scales.cpu()), dataclasses.replace(ew, codes=ew.codes.cpu()),
+                dataclasses.replace(ew, E=3)):
+        with pytest.raises(L.LbqError):
+            L.lbq_expert_gemm(bad, X, off if bad.E == 2 else torch.zeros(bad.E + 1, dtype=torch.int32, device="cuda"))
+    with pytest.raises(L.LbqError):
+        L.lbq_expert_gemm(ew, X, off, workspace=torch.zeros(1 << 20, 2, dtype=torch.uint8, device="cuda")[:, 0])
+    assert (L.lbq_expert_gemm(ew, X, off) == 0).all()
