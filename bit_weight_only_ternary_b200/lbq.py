@@ -1,12 +1,17 @@
 """Thin ctypes binding of the C ABI in include/lbq.h (argument marshalling only).
 
 Every function keeps the C name and hands torch tensors' device pointers and the
-current CUDA stream to liblbq.so; all arithmetic runs in the library's kernels.
+current CUDA stream to liblbq.so; all arithmetic runs in the library's kernels. With
+`stream=` a call runs on that stream, and the tensors it makes itself (outputs, a
+workspace) are that stream's: order them as any tensor made there before another stream
+reads them. No call records a gradient: outputs are plain tensors, and the calls that
+compute gradients (lbq_expert_combine_grad, lbq_expert_combine) are called as they are.
 Importing this module fails loudly when the library has not been built: there
 is no fallback path.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 from dataclasses import dataclass
@@ -126,6 +131,22 @@ def _stream(stream):
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
+_HERE = contextlib.nullcontext()
+
+
+def _on(stream):
+    """A context for the memory that a call makes itself (outputs, workspaces): taken from
+    and filled in the order of the stream that the call runs on, not of torch's current
+    one, with which nothing orders it."""
+    if stream is None:
+        return _HERE
+    if not isinstance(stream, torch.cuda.Stream):
+        handle = _stream(stream)
+        # (0 and 1 name the default stream, and 0 to ExternalStream a new one)
+        stream = torch.cuda.default_stream() if handle in (0, 1) else torch.cuda.ExternalStream(handle)
+    return torch.cuda.stream(stream)
+
+
 def lbq_packed_layout(fmt: int, K: int, N: int):
     """-> (code_stride bytes, scale_stride elements, code_bytes, scale_bytes)."""
     cs, ss = ctypes.c_int64(), ctypes.c_int64()
@@ -162,8 +183,9 @@ def lbq_pack(fmt: int, W: torch.Tensor, stream=None) -> PackedWeights:
     N, K = W.shape
     cs, ss, cb, sb = lbq_packed_layout(fmt, K, N)
     G = (N + 3) // 4  # rows are stored in groups of four
-    codes = torch.empty((G, 4 * cs), dtype=torch.uint8, device=W.device)
-    scales = torch.empty((G, 4 * ss), dtype=torch.int16, device=W.device) if ss else None
+    with _on(stream):
+        codes = torch.empty((G, 4 * cs), dtype=torch.uint8, device=W.device)
+        scales = torch.empty((G, 4 * ss), dtype=torch.int16, device=W.device) if ss else None
     # (torch's allocations are 256-byte aligned, as the scales' TMA rows require)
     _check(_lib.lbq_pack(fmt, _ptr(W), K, N, _ptr(codes), _ptr(scales), _stream(stream)),
            "lbq_pack")
@@ -173,15 +195,17 @@ def lbq_pack(fmt: int, W: torch.Tensor, stream=None) -> PackedWeights:
 def lbq_unpack(pw: PackedWeights, stream=None):
     """-> (int8 codes [N][K], fp32 block scales [N][K/blk]) on the device."""
     blk = 32 if pw.fmt in (LBQ_Q2RHT, LBQ_Q4G32) else 128
-    out = torch.empty((pw.N, pw.K), dtype=torch.int8, device=pw.codes.device)
-    sc = torch.empty((pw.N, pw.K // blk), dtype=torch.float32, device=pw.codes.device)
+    with _on(stream):
+        out = torch.empty((pw.N, pw.K), dtype=torch.int8, device=pw.codes.device)
+        sc = torch.empty((pw.N, pw.K // blk), dtype=torch.float32, device=pw.codes.device)
     d = pw.desc()
     _check(_lib.lbq_unpack(ctypes.byref(d), _ptr(out), _ptr(sc), _stream(stream)), "lbq_unpack")
     return out, sc
 
 
 def lbq_rht_signs(seed: int, K: int, device="cuda", stream=None) -> torch.Tensor:
-    D = torch.empty(K, dtype=torch.int8, device=device)
+    with _on(stream):
+        D = torch.empty(K, dtype=torch.int8, device=device)
     _check(_lib.lbq_rht_signs(ctypes.c_uint64(seed), K, _ptr(D), _stream(stream)), "lbq_rht_signs")
     return D
 
@@ -191,7 +215,8 @@ def lbq_hadamard(x: torch.Tensor, D: torch.Tensor, out=None, stream=None) -> tor
     x2 = x if x.dim() == 2 else x.view(1, -1)
     M, K = x2.shape
     if out is None:
-        out = torch.empty((M, K), dtype=torch.float32, device=x.device)
+        with _on(stream):
+            out = torch.empty((M, K), dtype=torch.float32, device=x.device)
     _check(_lib.lbq_hadamard(_ptr(x2), _ptr(D), M, K, _ptr(out), _stream(stream)), "lbq_hadamard")
     return out.view(x.shape)
 
@@ -228,9 +253,11 @@ def lbq_gemv(pw: PackedWeights, x: torch.Tensor, D=None, y=None, workspace=None,
              stream=None) -> torch.Tensor:
     """bf16 y [N] = W_hat x for bf16 x [K] (device)."""
     if y is None:
-        y = torch.empty(pw.N, dtype=torch.bfloat16, device=x.device)
+        with _on(stream):
+            y = torch.empty(pw.N, dtype=torch.bfloat16, device=x.device)
     if workspace is None:
-        workspace = workspace_for(pw, 1, x.device)
+        with _on(stream):
+            workspace = workspace_for(pw, 1, x.device)
     d = pw.desc()
     wsb = 0 if workspace is None else workspace.numel() * workspace.element_size()
     _check(_lib.lbq_gemv(ctypes.byref(d), _ptr(x), _ptr(D), _ptr(y), _ptr(workspace), wsb,
@@ -242,9 +269,11 @@ def lbq_gemv_f32(pw: PackedWeights, x: torch.Tensor, D=None, y=None, workspace=N
                  stream=None) -> torch.Tensor:
     """fp32 y [N] = W_hat x for bf16 x [K] (device), without the final bf16 rounding."""
     if y is None:
-        y = torch.empty(pw.N, dtype=torch.float32, device=x.device)
+        with _on(stream):
+            y = torch.empty(pw.N, dtype=torch.float32, device=x.device)
     if workspace is None:
-        workspace = workspace_for(pw, 1, x.device)
+        with _on(stream):
+            workspace = workspace_for(pw, 1, x.device)
     d = pw.desc()
     wsb = 0 if workspace is None else workspace.numel() * workspace.element_size()
     _check(_lib.lbq_gemv_f32(ctypes.byref(d), _ptr(x), _ptr(D), _ptr(y), _ptr(workspace), wsb,
@@ -257,9 +286,11 @@ def lbq_gemm(pw: PackedWeights, X: torch.Tensor, D=None, Y=None, workspace=None,
     """bf16 Y [M][N] = X W_hat^T for bf16 X [M][K] (device)."""
     M = X.shape[0]
     if Y is None:
-        Y = torch.empty((M, pw.N), dtype=torch.bfloat16, device=X.device)
+        with _on(stream):
+            Y = torch.empty((M, pw.N), dtype=torch.bfloat16, device=X.device)
     if workspace is None:
-        workspace = workspace_for(pw, M, X.device)
+        with _on(stream):
+            workspace = workspace_for(pw, M, X.device)
     d = pw.desc()
     wsb = 0 if workspace is None else workspace.numel() * workspace.element_size()
     _check(_lib.lbq_gemm(ctypes.byref(d), _ptr(X), M, _ptr(D), _ptr(Y), _ptr(workspace), wsb,
@@ -273,7 +304,8 @@ def lbq_gemv_noalloc(pw: PackedWeights, x: torch.Tensor, D=None, y=None,
     scratch array replaces the workspace (see include/lbq.h). Only `y` is allocated
     here, and only when the caller passes none."""
     if y is None:
-        y = torch.empty(pw.N, dtype=torch.bfloat16, device=x.device)
+        with _on(stream):
+            y = torch.empty(pw.N, dtype=torch.bfloat16, device=x.device)
     d = pw.desc()
     _check(_lib.lbq_gemv_noalloc(ctypes.byref(d), _ptr(x), _ptr(D), _ptr(y), _stream(stream)),
            "lbq_gemv_noalloc")
@@ -326,7 +358,8 @@ def lbq_gemv_batch(plist: ProductList, workspace=None, stream=None) -> None:
     launch per format present and LBQ_BATCH_MAX products of it. The workspace's first
     64 KB must be zero when it is first used (workspace_for_batch gives such a buffer)."""
     if workspace is None:
-        workspace = workspace_for_batch(plist)
+        with _on(stream):
+            workspace = workspace_for_batch(plist)
     wsb = workspace.numel() * workspace.element_size()
     _check(_lib.lbq_gemv_batch(plist.arr, len(plist), _ptr(workspace), wsb, _stream(stream)),
            "lbq_gemv_batch")
@@ -389,8 +422,9 @@ def pack_experts(fmt: int, W: torch.Tensor, stream=None) -> ExpertWeights:
     if ss == 0:
         _check(LBQ_ERR_FORMAT, "pack_experts")
     G = (N + 3) // 4
-    codes = torch.empty((E, G, 4 * cs), dtype=torch.uint8, device=W.device)
-    scales = torch.empty((E, G, 4 * ss), dtype=torch.int16, device=W.device)
+    with _on(stream):
+        codes = torch.empty((E, G, 4 * cs), dtype=torch.uint8, device=W.device)
+        scales = torch.empty((E, G, 4 * ss), dtype=torch.int16, device=W.device)
     for e in range(E):
         _check(_lib.lbq_pack(fmt, _ptr(W[e]), K, N, _ptr(codes[e]), _ptr(scales[e]),
                              _stream(stream)), "lbq_pack")
@@ -403,12 +437,13 @@ def lbq_expert_sort(expert: torch.Tensor, E: int, offsets=None, rows=None, slots
     T, topk = expert.shape
     _args("lbq_expert_sort", (expert, torch.int64 if expert.dtype is torch.int64 else torch.int32, None),
           (offsets, torch.int32, (E + 1,)), (rows, torch.int32, (T, topk)), (slots, torch.int32, (T * topk,)))
-    if offsets is None:
-        offsets = torch.empty(E + 1, dtype=torch.int32, device=expert.device)
-    if rows is None:
-        rows = torch.empty((T, topk), dtype=torch.int32, device=expert.device)
-    if slots is None:
-        slots = torch.empty(T * topk, dtype=torch.int32, device=expert.device)
+    with _on(stream):
+        if offsets is None:
+            offsets = torch.empty(E + 1, dtype=torch.int32, device=expert.device)
+        if rows is None:
+            rows = torch.empty((T, topk), dtype=torch.int32, device=expert.device)
+        if slots is None:
+            slots = torch.empty(T * topk, dtype=torch.int32, device=expert.device)
     _check(_lib.lbq_expert_sort(_ptr(expert), expert.element_size(), T, topk, E, _ptr(offsets),
                                 _ptr(rows), _ptr(slots), _stream(stream)), "lbq_expert_sort")
     return offsets, rows, slots
@@ -424,7 +459,8 @@ def lbq_expert_dispatch(X: torch.Tensor, rows: torch.Tensor, weights=None, out=N
           (weights, torch.float32, (T, topk)),
           (out, torch.bfloat16, None if out is None else (out.shape[0], K)))
     if out is None:
-        out = torch.empty((T * topk, K), dtype=torch.bfloat16, device=X.device)
+        with _on(stream):
+            out = torch.empty((T * topk, K), dtype=torch.bfloat16, device=X.device)
     _check(_lib.lbq_expert_dispatch(_ptr(X), T, K, _ptr(rows), topk, _ptr(weights), out.shape[0],
                                     _ptr(out), _stream(stream)), "lbq_expert_dispatch")
     return out
@@ -438,7 +474,8 @@ def lbq_expert_combine(Y: torch.Tensor, rows: torch.Tensor, weights=None, out=No
     _args("lbq_expert_combine", (Y, torch.bfloat16, None), (rows, torch.int32, None),
           (weights, torch.float32, (T, topk)), (out, torch.bfloat16, (T, N)))
     if out is None:
-        out = torch.empty((T, N), dtype=torch.bfloat16, device=Y.device)
+        with _on(stream):
+            out = torch.empty((T, N), dtype=torch.bfloat16, device=Y.device)
     _check(_lib.lbq_expert_combine(_ptr(Y), R, N, _ptr(rows), T, topk, _ptr(weights), _ptr(out),
                                    _stream(stream)), "lbq_expert_combine")
     return out
@@ -453,10 +490,11 @@ def lbq_expert_combine_grad(dout: torch.Tensor, Y: torch.Tensor, rows: torch.Ten
     _args("lbq_expert_combine_grad", (Y, torch.bfloat16, None), (dout, torch.bfloat16, (T, N)),
           (rows, torch.int32, None), (weights, torch.float32, (T, topk)), (dY, torch.bfloat16, (R, N)),
           (dweights, torch.float32, (T, topk)))
-    if dY is None:
-        dY = torch.empty((R, N), dtype=torch.bfloat16, device=Y.device)
-    if dweights is None:
-        dweights = torch.empty((T, topk), dtype=torch.float32, device=Y.device)
+    with _on(stream):
+        if dY is None:
+            dY = torch.empty((R, N), dtype=torch.bfloat16, device=Y.device)
+        if dweights is None:
+            dweights = torch.empty((T, topk), dtype=torch.float32, device=Y.device)
     _check(_lib.lbq_expert_combine_grad(_ptr(dout), _ptr(Y), R, N, _ptr(rows), T, topk,
                                         _ptr(weights), _ptr(dY), _ptr(dweights), _stream(stream)),
            "lbq_expert_combine_grad")
@@ -492,9 +530,11 @@ def lbq_expert_gemm(ew: ExpertWeights, X: torch.Tensor, offsets: torch.Tensor, s
         _check(LBQ_ERR_ARG, w)
     d = ew.desc()
     if Y is None:
-        Y = torch.empty((R, ew.N), dtype=torch.bfloat16, device=X.device)
+        with _on(stream):
+            Y = torch.empty((R, ew.N), dtype=torch.bfloat16, device=X.device)
     if workspace is None:
-        workspace = workspace_for_experts(ew, R, X.device)
+        with _on(stream):
+            workspace = workspace_for_experts(ew, R, X.device)
     wsb = 0 if workspace is None else workspace.numel() * workspace.element_size()
     _check(_lib.lbq_expert_gemm(ctypes.byref(d), ew.E, _ptr(X), T, _ptr(offsets), _ptr(slots), topk,
                                 R, _ptr(Y), _ptr(workspace), wsb, _stream(stream)),

@@ -137,3 +137,47 @@ def test_scales_on_the_host_are_refused(L):
     with pytest.raises(L.LbqError):
         L.lbq_expert_gemm(ew, X, off, workspace=torch.zeros(1 << 20, 2, dtype=torch.uint8, device="cuda")[:, 0])
     assert (L.lbq_expert_gemm(ew, X, off) == 0).all()
+
+
+# ----------------------------------------------------------------- streams and memory
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("raw", [False, True])
+def test_calls_on_a_side_stream_make_their_own_memory_there(L, raw):
+    """stream= names another stream than torch's current one, which is busy: a workspace
+    that the call makes is zeroed and used in that stream's order."""
+    K, N, E, R = 5120, 320, 3, 9
+    gen = torch.Generator("cuda").manual_seed(5)
+    W = torch.randn(E, N, K, device="cuda", generator=gen) * 0.02
+    X = torch.randn(R, K, device="cuda", generator=gen).to(torch.bfloat16)
+    pw, ew = L.lbq_pack(5, W[0]), L.pack_experts(5, W)
+    off = torch.tensor([0, 2, 5, R], dtype=torch.int32, device="cuda")
+    ids = torch.tensor([[0, 2], [1, 2], [0, 1]], device="cuda")
+
+    big = X.repeat(8, 1)
+    plist = L.ProductList([(pw, X[i], None, torch.empty(N, dtype=torch.bfloat16, device="cuda")) for i in range(3)])
+
+    def calls(stream):
+        L.lbq_gemv_batch(plist, stream=stream)
+        return [L.lbq_gemv(pw, X[0], stream=stream), L.lbq_gemv_f32(pw, X[1], stream=stream),
+                L.lbq_gemm(pw, X, stream=stream), L.lbq_gemm(pw, big, stream=stream),
+                L.lbq_expert_gemm(ew, X, off, stream=stream), L.lbq_gemv_noalloc(pw, X[2], stream=stream),
+                *L.lbq_expert_sort(ids, E, stream=stream), *[i[3] for i in plist.items]]
+
+    want = [t.clone() for t in calls(None)]
+    side = torch.cuda.Stream()
+    for _ in range(3):
+        # blocks of the workspaces' sizes, full of ones, given back to the current stream's pool
+        dirty = [torch.ones(n, dtype=torch.uint8, device="cuda") for n in (103424, 217088, 368640, 1 << 20) for _ in range(4)]
+        for _, _, _, y in plist.items:
+            y.fill_(7)
+        torch.cuda.synchronize()
+        del dirty
+        torch.cuda._sleep(40_000_000)  # (some 20 ms)
+        got = calls(side.cuda_stream if raw else side)
+        side.synchronize()
+        with torch.cuda.stream(side):
+            assert [torch.equal(g, w) for g, w in zip(got, want)] == [True] * len(want)
+        torch.cuda.synchronize()
+    assert all(torch.equal(g, w) for g, w in zip(calls(0), want))  # the default stream by its handle
+    assert L.lbq_device_fault() == 0
