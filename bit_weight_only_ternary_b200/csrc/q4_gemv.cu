@@ -562,6 +562,7 @@ __device__ __forceinline__ void stream_tiles(const Src& src, float* part, unsign
       asm volatile("atom.acq_rel.gpu.global.add.u32 %0, [%1], 1;" : "=r"(before) : "l"(count + first) : "memory");
     before = __shfl_sync(0xffffffffu, before, 0);
     if (before != static_cast<unsigned>(parts - 1)) return;
+    __syncwarp();  // lane 0's acquire comes before every lane's reads (a shuffle orders no memory)
 #pragma unroll
     for (int m = 0; m < kTok; ++m) {
       float y = __ldcg(part + static_cast<int64_t>(2 * first + 1) * kOut + m * kRowTile + lane);

@@ -33,6 +33,12 @@ def _us(f, n=8):
     return best
 
 
+def _dense(L, pw):
+    """The fp64 weights of a packed matrix."""
+    q, s = L.lbq_unpack(pw)
+    return q.double() * s.double().repeat_interleave(pw.K // s.shape[1], 1)
+
+
 # ------------------------------------------------------- what a row of activations holds
 
 @pytest.mark.gpu
@@ -181,3 +187,26 @@ def test_calls_on_a_side_stream_make_their_own_memory_there(L, raw):
         torch.cuda.synchronize()
     assert all(torch.equal(g, w) for g, w in zip(calls(0), want))  # the default stream by its handle
     assert L.lbq_device_fault() == 0
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("K,N", [(5120, 5120), (17408, 33), (640, 4096)])
+def test_tiles_that_several_ctas_share_join_alike_every_time(L, K, N):
+    """One and five tokens, and the same matrix as an expert: 200 runs give the same bits
+    (the last CTA of a tile reads the others' parts)."""
+    gen = torch.Generator("cuda").manual_seed(6)
+    W = torch.randn(1, N, K, device="cuda", generator=gen) * 0.02
+    X = torch.randn(5, K, device="cuda", generator=gen).to(torch.bfloat16)
+    pw, ew = L.lbq_pack(6, W[0]), L.pack_experts(6, W)
+    off = torch.tensor([0, 5], dtype=torch.int32, device="cuda")
+    w1, w5, we = L.workspace_for(pw, 1), L.workspace_for(pw, 5), L.workspace_for_experts(ew, 5)
+    runs = [lambda: L.lbq_gemv(pw, X[0], workspace=w1), lambda: L.lbq_gemm(pw, X, workspace=w5),
+            lambda: L.lbq_expert_gemm(ew, X, off, workspace=we)]
+    want = [r() for r in runs]
+    dense = X.double() @ _dense(L, pw).t()
+    S = X.double().abs() @ _dense(L, pw).abs().t()
+    for w in (want[0][None], want[1], want[2]):
+        assert ((w.double() - dense[:len(w)]).abs() <= 2.0 ** -8 * dense[:len(w)].abs() + 2.0 ** -12 * S[:len(w)]).all()
+    for _ in range(200):
+        assert all(torch.equal(r(), w) for r, w in zip(runs, want))
+    assert not any(w[:65536].any() for w in (w1, w5, we))
