@@ -258,8 +258,9 @@ typedef struct lbq_product {
 
 /* Bytes of workspace lbq_gemv_batch needs for this list (0 on bad arguments): 64 KB
  * kept under the counter rule of lbq_workspace_bytes (zero when the workspace is first
- * used, zero again after every completed call; this call leaves them untouched), then
- * the piece sums of the products it splits along K (none for lists of many rows). */
+ * used, zero again after every completed call; 4-bit lists count in them, the others
+ * leave them untouched), then the piece sums of the products it splits along K (none
+ * for lists of many rows). */
 size_t lbq_gemv_batch_workspace_bytes(const lbq_product* ps, int32_t n);
 
 /* n independent batch-1 products, each within the bound lbq_gemv meets (the same
@@ -404,16 +405,16 @@ lbq_status lbq_selftest_wait(void* stream);
  * needs more scratch than that (lbq_workspace_bytes(w, 1)) returns
  * LBQ_ERR_WORKSPACE and enqueues nothing; use lbq_gemv with your own workspace
  * then. The call allocates nothing: no cudaMalloc, no cudaFree, no allocating
- * library routine. It enqueues the product's kernels only: the product writes every
- * scratch value before reading it, and the array's arrival counters are zero from the
- * moment the library is loaded (a 4-bit product counts in them and leaves them zero,
- * the others never write them), so there is nothing to clear between calls.
+ * library routine. It enqueues the product's kernels, which write every scratch value
+ * before reading it, and for a 4-bit product, which counts arrivals in the array, one
+ * kernel before that zeroes the counters.
  *
  * The first call on each device looks up the array's device address (with that
  * device current) and caches it; make that first call before any stream capture.
  * All calls on a device share the one array: calls that can overlap on the GPU
  * (different streams without ordering between them) race on it and give wrong
- * results. Order them on one stream, or use lbq_gemv with one workspace each. */
+ * results; calls after them are right again. Order them on one stream, or use lbq_gemv
+ * with one workspace each. */
 lbq_status lbq_gemv_noalloc(const lbq_weights* w, const uint16_t* x, const int8_t* D,
                             uint16_t* y, void* stream);
 

@@ -4,6 +4,8 @@ Bounds as in test_q4.py: one bf16 rounding is 2^-8 of the value; fp32 sums are w
 2^-12 of the sum of magnitudes S; weights rounded to fp16 (many rows, on the tensor cores)
 add 2^-11 S.
 """
+import ctypes
+
 import numpy as np
 import pytest
 import torch
@@ -210,3 +212,57 @@ def test_tiles_that_several_ctas_share_join_alike_every_time(L, K, N):
     for _ in range(200):
         assert all(torch.equal(r(), w) for r, w in zip(runs, want))
     assert not any(w[:65536].any() for w in (w1, w5, we))
+
+
+class _KernelNode(ctypes.Structure):
+    _fields_ = [("func", ctypes.c_void_p), ("grid", ctypes.c_uint * 3), ("block", ctypes.c_uint * 3),
+                ("smem", ctypes.c_uint), ("params", ctypes.POINTER(ctypes.c_void_p)), ("extra", ctypes.c_void_p),
+                ("kern", ctypes.c_void_p), ("ctx", ctypes.c_void_p)]
+
+
+def _noalloc_counters(pw, L, x, y):
+    """The address of the fixed array's arrival counters, from the arguments of a captured
+    lbq_gemv_noalloc: the product's parts lie 64 KB behind them."""
+    g = torch.cuda.CUDAGraph(keep_graph=True)
+    with torch.cuda.graph(g):
+        L.lbq_gemv_noalloc(pw, x, y=y)
+    cu = ctypes.CDLL("libcuda.so.1")
+    graph, n = ctypes.c_void_p(g.raw_cuda_graph()), ctypes.c_size_t()
+    assert cu.cuGraphGetNodes(graph, None, ctypes.byref(n)) == 0
+    nodes = (ctypes.c_void_p * n.value)()
+    assert cu.cuGraphGetNodes(graph, nodes, ctypes.byref(n)) == 0
+    for node in nodes:
+        kind, p = ctypes.c_int(), _KernelNode()
+        assert cu.cuGraphNodeGetType(ctypes.c_void_p(node), ctypes.byref(kind)) == 0
+        if kind.value != 0 or cu.cuGraphKernelNodeGetParams_v2(ctypes.c_void_p(node), ctypes.byref(p)) != 0:
+            continue
+        if p.smem < 65536:  # (not the product)
+            continue
+        words = ctypes.cast(p.params[0], ctypes.POINTER(ctypes.c_uint64))[:8]
+        for a, b in zip(words, words[1:]):
+            if a - b == 65536:
+                return b
+    raise AssertionError("no product among the captured kernels")
+
+
+@pytest.mark.gpu
+def test_noalloc_after_calls_that_overlapped(L):
+    """Calls that overlap on the fixed array are wrong themselves (documented), but may
+    leave counts in it: the calls after them are right all the same."""
+    K, N = 5120, 5120
+    gen = torch.Generator("cuda").manual_seed(7)
+    pw = L.lbq_pack(5, torch.randn(N, K, device="cuda", generator=gen) * 0.02)
+    x = torch.randn(K, device="cuda", generator=gen).to(torch.bfloat16)
+    want = L.lbq_gemv(pw, x)
+    y = torch.empty_like(want)
+    assert torch.equal(L.lbq_gemv_noalloc(pw, x, y=y), want)
+    at = _noalloc_counters(pw, L, x, y)
+    left = torch.ones(1024, dtype=torch.int32)
+    for count in (1, 2, 7):
+        torch.cuda.synchronize()
+        left.fill_(count)
+        assert ctypes.CDLL("libcuda.so.1").cuMemcpyHtoD_v2(ctypes.c_uint64(at), ctypes.c_void_p(left.data_ptr()),
+                                                           ctypes.c_size_t(4 * left.numel())) == 0
+        for _ in range(3):
+            y.fill_(7)
+            assert torch.equal(L.lbq_gemv_noalloc(pw, x, y=y), want)
