@@ -37,6 +37,8 @@
 // weights, 128 x 128 a CTA, from tensor memory in 8 x 64 cycles.
 #include <cudaTypedefs.h>
 
+#include <algorithm>
+
 #include "sm100_async.cuh"
 
 namespace {
@@ -1111,11 +1113,24 @@ cudaError_t launch(const lbq_weights* w, const Plan& plan, const lbq_expert_rows
 
 }  // namespace
 
+// Partial sums of the batches of up to M tokens that plan_for may split: at most pairs /
+// tiles splits, with at least a token tile for every kMaxTileM tokens. (A plan of few tokens
+// may need more of them than one of many: a workspace for M tokens serves all batches up to
+// M.)
+static size_t most_part_floats(const lbq_weights* w, int64_t M) {
+  const int64_t ntn = (w->N + 2 * kTileN - 1) / (2 * kTileN), pairs = sm_count() / 2;
+  const int64_t most = (w->K / kTileK + 3) / 4;
+  int64_t floats = 0;
+  for (int64_t c = 1; c <= (M + kMaxTileM - 1) / kMaxTileM && 2 * c * ntn <= pairs; ++c) {
+    const int64_t splits = std::min(pairs / (c * ntn), most), rows = std::min<int64_t>(M, c * kMaxTileM);
+    if (splits > 1) floats = std::max(floats, splits * rows * w->N);
+  }
+  return static_cast<size_t>(floats);
+}
+
 // [64 KB left alone: the counter rule][fp16 X][exponents, flags][weight exponents][tile order][partials]
 size_t lbq_q4_tc_workspace(const lbq_weights* w, int64_t M) {
-  const Plan p = plan_for(w, M);
-  return kWsCounterBytes +
-         scratch_for(w, M, 1, p.splits > 1 ? static_cast<size_t>(p.splits) * M * w->N : 0).total;
+  return std::max(lbq_q4_few_workspace(8), kWsCounterBytes + scratch_for(w, M, 1, most_part_floats(w, M)).total);
 }
 
 cudaError_t lbq_launch_q4_tc(const lbq_weights* w, const uint16_t* X, int64_t M, uint16_t* Y, void* ws,
@@ -1127,7 +1142,7 @@ cudaError_t lbq_launch_q4_tc(const lbq_weights* w, const uint16_t* X, int64_t M,
 }
 
 size_t lbq_q4_expert_tc_workspace(const lbq_weights* w, int32_t E, int64_t R) {
-  return kWsCounterBytes + scratch_for(w, R, E, 0).total;
+  return std::max(lbq_q4_few_workspace(8), kWsCounterBytes + scratch_for(w, R, E, 0).total);
 }
 
 cudaError_t lbq_launch_q4_expert_tc(const lbq_weights* w, const lbq_expert_rows& r, void* ws, cudaStream_t s) {

@@ -191,7 +191,9 @@ lbq_status lbq_hadamard(const uint16_t* x, const int8_t* D, int64_t M, int64_t K
  * zero when the workspace is first used, and every completed call leaves them zero
  * again, so one zero-fill at allocation serves any sequence of calls on matrices
  * of any shape. The rest is scratch. Calls sharing one workspace must not overlap
- * in time (use one workspace per stream). Returns 0 on bad arguments. */
+ * in time (use one workspace per stream). For 4-bit weights it is never less for more
+ * rows: a workspace for the largest M serves every smaller one. Returns 0 on bad
+ * arguments. */
 size_t lbq_workspace_bytes(const lbq_weights* w, int64_t M);
 
 /* Batch-1 product y = W_hat x (bf16 x [K] -> bf16 y [N]) with W_hat the dequantised
@@ -351,7 +353,7 @@ lbq_status lbq_expert_combine_grad(const uint16_t* dout, const uint16_t* Y, int6
 
 /* Bytes of workspace lbq_expert_gemm needs for R rows (0 on bad arguments), under the
  * counter rule of lbq_workspace_bytes: its first 64 KB are zero when it is first used
- * and zero again after every completed call. */
+ * and zero again after every completed call. It is never less for more rows. */
 size_t lbq_expert_workspace_bytes(const lbq_weights* w, int32_t E, int64_t R);
 
 /* Y[r] = W_hat_e x_r for every row r in [offsets[e], offsets[e+1]), x_r = X[slots[r] /

@@ -266,3 +266,42 @@ def test_noalloc_after_calls_that_overlapped(L):
         for _ in range(3):
             y.fill_(7)
             assert torch.equal(L.lbq_gemv_noalloc(pw, x, y=y), want)
+
+
+# ------------------------------------------------------------------------- workspaces
+
+@pytest.mark.parametrize("fmt", [5, 6])
+@pytest.mark.parametrize("K,N", [(128, 4), (768, 2048), (512, 256), (5120, 7001), (17408, 300), (5120, 34816),
+                                 (5120, 18944), (8192, 9472)])
+def test_a_workspace_for_more_rows_serves_fewer(L, fmt, K, N):
+    """No call of fewer rows needs more bytes than one of more."""
+    lib = L.lib()
+    cs, ss, _, _ = L.lbq_packed_layout(fmt, K, N)
+    w = ctypes.byref(L.lbq_weights(fmt, 0, K, N, 1 << 20, 1 << 20, cs, ss))
+    rows = [*range(1, 700), *range(701, 3000, 37), 4096, 8192, 20000]
+    need = [lib.lbq_workspace_bytes(w, M) for M in rows]
+    assert need[0] >= 65536 and all(a <= b for a, b in zip(need, need[1:]))
+    for E in (1, 8, 128):
+        need = [lib.lbq_expert_workspace_bytes(w, E, R) for R in rows]
+        assert need[0] >= 65536 and all(a <= b for a, b in zip(need, need[1:]))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("fmt", [5, 6])
+def test_one_workspace_for_every_batch(L, fmt):
+    """The largest batch's workspace in calls of every smaller size, K split or not, few rows
+    or many, in turn."""
+    K, N, E = 2048, 768, 8
+    gen = torch.Generator("cuda").manual_seed(8)
+    W = torch.randn(E, N, K, device="cuda", generator=gen) * 0.02
+    X = torch.randn(300, K, device="cuda", generator=gen).to(torch.bfloat16)
+    pw, ew = L.lbq_pack(fmt, W[0]), L.pack_experts(fmt, W)
+    ws, we = L.workspace_for(pw, 300), L.workspace_for_experts(ew, 300)
+    for M in (300, 5, 65, 64, 33, 32, 1, 9, 257, 8, 100):
+        off = torch.linspace(0, M, E + 1).to(torch.int32).cuda()
+        assert torch.equal(L.lbq_expert_gemm(ew, X[:M], off, workspace=we), L.lbq_expert_gemm(ew, X[:M], off))
+        if M == 1:
+            assert torch.equal(L.lbq_gemv(pw, X[0], workspace=ws), L.lbq_gemv(pw, X[0]))
+        else:
+            assert torch.equal(L.lbq_gemm(pw, X[:M], workspace=ws), L.lbq_gemm(pw, X[:M]))
+    assert not ws[:65536].any() and not we[:65536].any()
