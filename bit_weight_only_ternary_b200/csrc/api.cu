@@ -1,5 +1,6 @@
 // api.cu -- the C ABI (include/lbq.h): host-side validation, then one or more launches.
 // Nothing is enqueued unless every argument passes; launch failures map to LBQ_ERR_CUDA.
+#include <initializer_list>
 #include <vector>
 
 #include "lbq_common.cuh"
@@ -27,6 +28,29 @@ inline bool per_token(const lbq_weights* w, int64_t M) {
   if (M == 1) return true;
   return w->fmt == LBQ_TERN5 && M <= kTernPerTokenMaxM &&
          !(lbq_gemv_workspace(w) && w->N > lbq::kMaxSplitRows);
+}
+
+// Byte ranges [lo, hi) overlap.
+inline bool overlap(const void* a, size_t na, const void* b, size_t nb) {
+  const uintptr_t a0 = reinterpret_cast<uintptr_t>(a), b0 = reinterpret_cast<uintptr_t>(b);
+  return a0 < b0 + nb && b0 < a0 + na;
+}
+
+// A call's buffers (null: not given). What it writes may overlap nothing else of the call:
+// its kernels read and write in no order that a caller could count on.
+struct Span {
+  const void* p;
+  size_t bytes;
+};
+bool disjoint(std::initializer_list<Span> written, std::initializer_list<Span> read) {
+  for (const Span* a = written.begin(); a != written.end(); ++a) {
+    if (!a->p) continue;
+    for (const Span* b = written.begin(); b != a; ++b)
+      if (b->p && overlap(a->p, a->bytes, b->p, b->bytes)) return false;
+    for (const Span& b : read)
+      if (b.p && overlap(a->p, a->bytes, b.p, b.bytes)) return false;
+  }
+  return true;
 }
 
 inline bool fmt_known(int32_t fmt) {
@@ -71,8 +95,17 @@ lbq_status check_operands(const lbq_weights* w, const void* x, int64_t M, const 
   return LBQ_OK;
 }
 
+// The packed bytes of E matrices behind one another.
+Span codes_of(const lbq_weights* w, int64_t E = 1) {
+  return {w->codes, static_cast<size_t>(E * lbq::g4_rows(w->N)) * static_cast<size_t>(w->code_stride)};
+}
+Span scales_of(const lbq_weights* w, int64_t E = 1) {
+  return {w->scales, static_cast<size_t>(E * lbq::g4_rows(w->N)) * static_cast<size_t>(w->scale_stride) * 2};
+}
+
+// (y_bytes: of an output)
 lbq_status check_product(const lbq_weights* w, const void* x, int64_t M, const int8_t* D,
-                         const void* y, void* ws, size_t ws_bytes, Layout* L) {
+                         const void* y, void* ws, size_t ws_bytes, Layout* L, size_t y_bytes = 2) {
   lbq_status st = check_operands(w, x, M, D, y, L);
   if (st != LBQ_OK) return st;
   const size_t need = lbq_workspace_bytes(w, M);
@@ -80,6 +113,10 @@ lbq_status check_product(const lbq_weights* w, const void* x, int64_t M, const i
     if (!ws || ws_bytes < need) return LBQ_ERR_WORKSPACE;
     if (!aligned(ws, 16)) return LBQ_ERR_ALIGN;
   }
+  if (lbq::is_q4(w->fmt) &&
+      !disjoint({{y, y_bytes * static_cast<size_t>(M) * w->N}, {need ? ws : nullptr, need}},
+                {{x, 2 * static_cast<size_t>(M) * w->K}, codes_of(w), scales_of(w)}))
+    return LBQ_ERR_ARG;
   return LBQ_OK;
 }
 
@@ -92,12 +129,6 @@ lbq_status lbq_validate_gemv(const lbq_weights* w, const uint16_t* x, const int8
 }
 
 namespace {
-
-// Byte ranges [lo, hi) overlap.
-inline bool overlap(const void* a, size_t na, const void* b, size_t nb) {
-  const uintptr_t a0 = reinterpret_cast<uintptr_t>(a), b0 = reinterpret_cast<uintptr_t>(b);
-  return a0 < b0 + nb && b0 < a0 + na;
-}
 
 // A batch list: every product valid on its own (as for lbq_gemv, without its limit on
 // split rows, which the batch kernel does not have), and no output overlapping an
@@ -298,7 +329,7 @@ lbq_status lbq_gemv(const lbq_weights* w, const uint16_t* x, const int8_t* D, ui
 lbq_status lbq_gemv_f32(const lbq_weights* w, const uint16_t* x, const int8_t* D, float* y,
                         void* workspace, size_t workspace_bytes, void* stream) {
   Layout L;
-  lbq_status st = check_product(w, x, 1, D, y, workspace, workspace_bytes, &L);
+  lbq_status st = check_product(w, x, 1, D, y, workspace, workspace_bytes, &L, 4);
   if (st != LBQ_OK) return st;
   if (!aligned(y, 4)) return LBQ_ERR_ALIGN;
   return from_cuda(lbq_launch_gemv(w, x, D, nullptr, y, workspace, as_stream(stream)));
@@ -373,6 +404,10 @@ lbq_status lbq_expert_sort(const void* expert, int32_t id_bytes, int64_t T, int3
   if (!aligned(expert, static_cast<uintptr_t>(id_bytes)) || !aligned(offsets, 4) || !aligned(rows, 4) ||
       !aligned(slots, 4))
     return LBQ_ERR_ALIGN;
+  const size_t R = static_cast<size_t>(T) * topk;
+  if (!disjoint({{offsets, 4 * (static_cast<size_t>(E) + 1)}, {rows, 4 * R}, {slots, 4 * R}},
+                {{expert, static_cast<size_t>(id_bytes) * R}}))
+    return LBQ_ERR_ARG;
   return from_cuda(lbq_launch_expert_sort(expert, id_bytes, T * topk, E, offsets, rows, slots, as_stream(stream)));
 }
 
@@ -383,7 +418,9 @@ lbq_status lbq_expert_dispatch(const uint16_t* X, int64_t T, int64_t K, const in
   if (st != LBQ_OK) return st;
   if (R < 1 || R > kMaxSlots || K < 1 || K > kMaxWidth) return LBQ_ERR_SHAPE;
   if (!aligned(X, 2) || !aligned(out, 2) || !aligned(rows, 4) || !aligned(weights, 4)) return LBQ_ERR_ALIGN;
-  if (overlap(X, 2 * T * K, out, 2 * R * K)) return LBQ_ERR_ARG;
+  const size_t n = 4 * static_cast<size_t>(T) * topk;
+  if (!disjoint({{out, 2 * static_cast<size_t>(R) * K}}, {{X, 2 * static_cast<size_t>(T) * K}, {rows, n}, {weights, n}}))
+    return LBQ_ERR_ARG;
   return from_cuda(lbq_launch_expert_dispatch(X, rows, weights, T, topk, K, R, out, as_stream(stream)));
 }
 
@@ -394,7 +431,9 @@ lbq_status lbq_expert_combine(const uint16_t* Y, int64_t R, int64_t N, const int
   if (st != LBQ_OK) return st;
   if (R < 1 || R > kMaxSlots || N < 1 || N > kMaxWidth) return LBQ_ERR_SHAPE;
   if (!aligned(Y, 2) || !aligned(out, 2) || !aligned(rows, 4) || !aligned(weights, 4)) return LBQ_ERR_ALIGN;
-  if (overlap(Y, 2 * R * N, out, 2 * T * N)) return LBQ_ERR_ARG;
+  const size_t n = 4 * static_cast<size_t>(T) * topk;
+  if (!disjoint({{out, 2 * static_cast<size_t>(T) * N}}, {{Y, 2 * static_cast<size_t>(R) * N}, {rows, n}, {weights, n}}))
+    return LBQ_ERR_ARG;
   return from_cuda(lbq_launch_expert_combine(Y, rows, weights, T, topk, N, R, out, as_stream(stream)));
 }
 
@@ -410,8 +449,7 @@ lbq_status lbq_expert_combine_grad(const uint16_t* dout, const uint16_t* Y, int6
     return LBQ_ERR_ALIGN;
   const size_t nR = 2 * static_cast<size_t>(R) * N, nT = 2 * static_cast<size_t>(T) * N;
   const size_t nw = 4 * static_cast<size_t>(T) * topk;
-  if (overlap(dY, nR, Y, nR) || overlap(dY, nR, dout, nT) || overlap(dweights, nw, weights, nw))
-    return LBQ_ERR_ARG;
+  if (!disjoint({{dY, nR}, {dweights, nw}}, {{Y, nR}, {dout, nT}, {rows, nw}, {weights, nw}})) return LBQ_ERR_ARG;
   return from_cuda(lbq_launch_expert_combine_grad(dout, Y, rows, weights, T, topk, N, R, dY, dweights,
                                                   as_stream(stream)));
 }
@@ -438,6 +476,10 @@ lbq_status lbq_expert_gemm(const lbq_weights* w, int32_t E, const uint16_t* X, i
     if (!workspace || workspace_bytes < need) return LBQ_ERR_WORKSPACE;
     if (!aligned(workspace, 16)) return LBQ_ERR_ALIGN;
   }
+  if (!disjoint({{Y, 2 * static_cast<size_t>(R) * w->N}, {need ? workspace : nullptr, need}},
+                {{X, 2 * static_cast<size_t>(T) * w->K}, {offsets, 4 * (static_cast<size_t>(E) + 1)},
+                 {slots, 4 * static_cast<size_t>(R)}, codes_of(w, E), scales_of(w, E)}))
+    return LBQ_ERR_ARG;
   const lbq_expert_rows rows = {X, offsets, slots, Y, T, R, topk, E};
   return from_cuda(expert_few(E, R) ? lbq_launch_q4_expert_few(w, rows, workspace, as_stream(stream))
                                     : lbq_launch_q4_expert_tc(w, rows, workspace, as_stream(stream)));

@@ -207,8 +207,9 @@ size_t lbq_workspace_bytes(const lbq_weights* w, int64_t M);
  * let its successor start early: lbq_pack, copies and ordinary kernels do not. (The
  * same holds for 4-bit products of up to 32 rows in lbq_gemm and for 4-bit lists in
  * lbq_gemv_batch. The expert calls start early too, and read nothing before their turn.)
- * Errors: LBQ_ERR_ARG (nulls, D missing for Q2RHT), LBQ_ERR_SHAPE, LBQ_ERR_ALIGN,
- * LBQ_ERR_FORMAT, LBQ_ERR_WORKSPACE, LBQ_ERR_CUDA. */
+ * Errors: LBQ_ERR_ARG (nulls, D missing for Q2RHT, for 4-bit weights y or workspace over
+ * anything else), LBQ_ERR_SHAPE, LBQ_ERR_ALIGN, LBQ_ERR_FORMAT, LBQ_ERR_WORKSPACE,
+ * LBQ_ERR_CUDA. */
 lbq_status lbq_gemv(const lbq_weights* w, const uint16_t* x, const int8_t* D, uint16_t* y,
                     void* workspace, size_t workspace_bytes, void* stream);
 
@@ -311,7 +312,8 @@ lbq_status lbq_gemv_batch_plan(const lbq_product* ps, int32_t n, int32_t ctas, i
  *   out[t] = sum_j weights[t][j] * f_e(x[t]),  e = expert[t][j]
  * is sort, then products and activations on rows, then combine. `rows` (slot -> row)
  * and `slots` (row -> slot) come from lbq_expert_sort; entries outside their range are
- * left out, never followed. */
+ * left out, never followed. What one of these calls writes (its workspace too) may overlap
+ * nothing else that it is given: LBQ_ERR_ARG. */
 #define LBQ_MAX_EXPERTS 1024
 
 /* Stable counting sort of the T * topk slots by expert: expert [T][topk] (device, ids of
@@ -329,7 +331,7 @@ lbq_status lbq_expert_sort(const void* expert, int32_t id_bytes, int64_t T, int3
  * is outside 0 .. R-1 are left out, rows no slot names are left as they were, and rows
  * must be distinct. With weights NULL its gradient with respect to X is
  * lbq_expert_combine(dout, R, K, rows, T, topk, NULL, dX).
- * Errors: LBQ_ERR_ARG (nulls, X and out overlap), LBQ_ERR_SHAPE, LBQ_ERR_ALIGN (bf16 on
+ * Errors: LBQ_ERR_ARG (nulls, overlaps), LBQ_ERR_SHAPE, LBQ_ERR_ALIGN (bf16 on
  * 2 bytes, the rest on 4; 16-byte aligned X and out with K % 8 == 0 are faster),
  * LBQ_ERR_CUDA. */
 lbq_status lbq_expert_dispatch(const uint16_t* X, int64_t T, int64_t K, const int32_t* rows, int32_t topk,
@@ -345,8 +347,7 @@ lbq_status lbq_expert_combine(const uint16_t* Y, int64_t R, int64_t N, const int
 /* Both gradients of lbq_expert_combine in one pass: dY[rows[t][j]] = weights[t][j] *
  * dout[t] (rows no slot names are left as they were; rows must be distinct) and
  * dweights[t][j] = sum_n dout[t][n] Y[rows[t][j]][n] (fp32, a fixed order of sums; 0 for
- * slots left out). Limits and errors as lbq_expert_dispatch; dY may overlap neither Y
- * nor dout, dweights not weights. */
+ * slots left out). Limits and errors as lbq_expert_dispatch. */
 lbq_status lbq_expert_combine_grad(const uint16_t* dout, const uint16_t* Y, int64_t R, int64_t N,
                                    const int32_t* rows, int64_t T, int32_t topk, const float* weights,
                                    uint16_t* dY, float* dweights, void* stream);

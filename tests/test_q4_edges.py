@@ -305,3 +305,53 @@ def test_one_workspace_for_every_batch(L, fmt):
         else:
             assert torch.equal(L.lbq_gemm(pw, X[:M], workspace=ws), L.lbq_gemm(pw, X[:M]))
     assert not ws[:65536].any() and not we[:65536].any()
+
+
+# --------------------------------------------------- buffers that lie over one another
+
+def test_outputs_over_anything_else_are_refused(L):
+    """Addresses only: every call answers before a launch. In each, an output or the
+    workspace reaches one byte into something else, or stands where it does."""
+    lib, A = L.lib(), L.LBQ_ERR_ARG
+    V = ctypes.c_void_p
+    T, k, E, N, K, R = 6, 2, 4, 16, 256, 12
+    G, cs, ss = N // 4, K // 2, 8
+    size = {"ids": 8 * R, "off": 4 * (E + 1), "rows": 4 * R, "slots": 4 * R, "w": 4 * R, "X": 2 * T * K, "Xs": 2 * R * K,
+            "Y": 2 * R * N, "out": 2 * T * N, "dY": 2 * R * N, "dw": 4 * R, "codes": E * G * 4 * cs,
+            "scales": E * G * 4 * ss * 2, "y1": 2 * N, "y32": 4 * N, "x1": 2 * K, "Ym": 2 * T * N}
+    desc = lambda a, e=1: ctypes.byref(L.lbq_weights(5, 0, K, N, a["codes"], a["scales"], cs, ss))  # noqa: E731
+    some = desc({"codes": 1 << 20, "scales": 1 << 20})
+    size["ws1"], size["wsm"] = lib.lbq_workspace_bytes(some, 1), lib.lbq_workspace_bytes(some, T)
+    size["wse"] = lib.lbq_expert_workspace_bytes(some, E, R)
+    size["c1"], size["s1"] = G * 4 * cs, G * 4 * ss * 2
+    place = {n: (i + 1) << 24 for i, n in enumerate(size)}
+    calls = {  # written, read, the call
+        "sort": (("off", "rows", "slots"), ("ids",),
+                 lambda a: lib.lbq_expert_sort(V(a["ids"]), 8, T, k, E, V(a["off"]), V(a["rows"]), V(a["slots"]), None)),
+        "dispatch": (("Xs",), ("X", "rows", "w"),
+                     lambda a: lib.lbq_expert_dispatch(V(a["X"]), T, K, V(a["rows"]), k, V(a["w"]), R, V(a["Xs"]), None)),
+        "combine": (("out",), ("Y", "rows", "w"),
+                    lambda a: lib.lbq_expert_combine(V(a["Y"]), R, N, V(a["rows"]), T, k, V(a["w"]), V(a["out"]), None)),
+        "grad": (("dY", "dw"), ("out", "Y", "rows", "w"),
+                 lambda a: lib.lbq_expert_combine_grad(V(a["out"]), V(a["Y"]), R, N, V(a["rows"]), T, k, V(a["w"]), V(a["dY"]),
+                                                       V(a["dw"]), None)),
+        "experts": (("Y", "wse"), ("X", "off", "slots", "codes", "scales"),
+                    lambda a: lib.lbq_expert_gemm(desc(a), E, V(a["X"]), T, V(a["off"]), V(a["slots"]), k, R, V(a["Y"]),
+                                                  V(a["wse"]), size["wse"], None)),
+        "gemv": (("y1", "ws1"), ("x1", "c1", "s1"),
+                 lambda a: lib.lbq_gemv(desc({"codes": a["c1"], "scales": a["s1"]}), V(a["x1"]), None, V(a["y1"]), V(a["ws1"]),
+                                        size["ws1"], None)),
+        "gemv_f32": (("y32", "ws1"), ("x1", "c1", "s1"),
+                     lambda a: lib.lbq_gemv_f32(desc({"codes": a["c1"], "scales": a["s1"]}), V(a["x1"]), None, V(a["y32"]),
+                                                V(a["ws1"]), size["ws1"], None)),
+        "gemm": (("Ym", "wsm"), ("X", "c1", "s1"),
+                 lambda a: lib.lbq_gemm(desc({"codes": a["c1"], "scales": a["s1"]}), V(a["X"]), T, None, V(a["Ym"]), V(a["wsm"]),
+                                        size["wsm"], None))}
+    for name, (written, read, call) in calls.items():
+        for w in written:
+            for r in (*written, *read):
+                if r != w:
+                    assert call({**place, w: place[r]}) == A, (name, w, r)
+                    # the last 16 bytes of the other, and its first
+                    assert call({**place, w: place[r] + (size[r] - 1) // 16 * 16}) == A, (name, w, r)
+                    assert call({**place, r: place[w] + (size[w] - 1) // 16 * 16}) == A, (name, w, r)
