@@ -57,6 +57,8 @@ inline bool fmt_known(int32_t fmt) {
   return fmt == LBQ_TERN5 || fmt == LBQ_SIGN1 || fmt == LBQ_Q2RHT || lbq::is_q4(fmt);
 }
 
+constexpr int64_t kMaxQ4Rows = int64_t{1} << 30;  // token rows of a 4-bit product: 32-bit counts
+
 // Checks a weight descriptor; fills L on success.
 lbq_status check_weights(const lbq_weights* w, Layout* L) {
   if (!w) return LBQ_ERR_ARG;
@@ -66,8 +68,10 @@ lbq_status check_weights(const lbq_weights* w, Layout* L) {
   if (!w->codes) return LBQ_ERR_ARG;
   if (!aligned(w->codes, 16)) return LBQ_ERR_ALIGN;
   if (w->code_stride < L->code_stride || w->code_stride % 16) return LBQ_ERR_SHAPE;
-  // (4-bit: the kernels index rows and K with 32 bits, offsets with 64)
-  if (lbq::is_q4(w->fmt) && (w->N > (int64_t{1} << 28) || w->K > (int64_t{1} << 28))) return LBQ_ERR_SHAPE;
+  // (4-bit: the kernels index rows, K and a row's scales with 32 bits, offsets with 64)
+  if (lbq::is_q4(w->fmt) && (w->N > (int64_t{1} << 28) || w->K > (int64_t{1} << 28) ||
+                             w->scale_stride > (int64_t{1} << 28)))
+    return LBQ_ERR_SHAPE;
   if (w->fmt == LBQ_TERN5) {
     if (w->scales || w->scale_stride != 0) return LBQ_ERR_ARG;
   } else {
@@ -84,7 +88,7 @@ lbq_status check_operands(const lbq_weights* w, const void* x, int64_t M, const 
   lbq_status st = check_weights(w, L);
   if (st != LBQ_OK) return st;
   if (M < 1) return LBQ_ERR_SHAPE;
-  if (lbq::is_q4(w->fmt) && M > (int64_t{1} << 30)) return LBQ_ERR_SHAPE;
+  if (lbq::is_q4(w->fmt) && M > kMaxQ4Rows) return LBQ_ERR_SHAPE;
   if (!x || !y) return LBQ_ERR_ARG;
   if (!aligned(x, 16) || !aligned(y, 2)) return LBQ_ERR_ALIGN;
   if (w->fmt == LBQ_Q2RHT) {
@@ -314,7 +318,7 @@ lbq_status lbq_selftest_wait(void* stream) { return from_cuda(lbq_launch_wait_se
 
 size_t lbq_workspace_bytes(const lbq_weights* w, int64_t M) {
   Layout L;
-  if (check_weights(w, &L) != LBQ_OK || M < 1) return 0;
+  if (check_weights(w, &L) != LBQ_OK || M < 1 || (lbq::is_q4(w->fmt) && M > kMaxQ4Rows)) return 0;
   return per_token(w, M) ? lbq_gemv_workspace(w) : lbq_gemm_workspace(w, M);
 }
 

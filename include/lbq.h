@@ -86,7 +86,7 @@
  *   of the group. Padding rows and padding words are zero bytes.
  *
  * Shape rules: K % 128 == 0 (LBQ_Q2RHT: K % 512 == 0), K >= 128, N >= 1, M >= 1
- * (4-bit formats: K and N at most 2^28);
+ * (4-bit formats: K, N and scale strides at most 2^28, M at most 2^30);
  * a batch-1 product split over K (K > 512, or > 1024 for LBQ_SIGN1) has N <= 524288.
  * Alignment rules: codes, scales, x/X, W, D, out and workspace 16-byte aligned;
  * y/Y 2-byte aligned. Strides must be at least the packed row size; code strides a

@@ -355,3 +355,23 @@ def test_outputs_over_anything_else_are_refused(L):
                     # the last 16 bytes of the other, and its first
                     assert call({**place, w: place[r] + (size[r] - 1) // 16 * 16}) == A, (name, w, r)
                     assert call({**place, r: place[w] + (size[w] - 1) // 16 * 16}) == A, (name, w, r)
+
+
+@pytest.mark.parametrize("fmt", [5, 6])
+def test_sizes_that_32_bits_do_not_count_are_refused(L, fmt):
+    """A group of four rows has 4 scale_stride scales: 2^29 of them a row would pass 32 bits."""
+    lib, V = L.lib(), ctypes.c_void_p
+    K, N = 256, 8
+
+    def desc(ss=8):
+        return ctypes.byref(L.lbq_weights(fmt, 0, K, N, 1 << 24, 1 << 32, K // 2, ss))
+    for ss in (2 ** 28 + 8, 2 ** 29, 2 ** 30, 2 ** 40):
+        assert lib.lbq_workspace_bytes(desc(ss), 1) == 0
+        assert lib.lbq_gemv(desc(ss), V(1 << 40), None, V(1 << 41), V(1 << 42), 1 << 30, None) == L.LBQ_ERR_SHAPE
+        assert lib.lbq_expert_gemm(desc(ss), 2, V(1 << 40), 4, V(1 << 43), None, 1, 4, V(1 << 41), V(1 << 42), 1 << 30,
+                                   None) == L.LBQ_ERR_SHAPE
+    assert lib.lbq_workspace_bytes(desc(2 ** 28), 1) > 0
+    for M in (2 ** 30 + 1, 2 ** 50, 2 ** 62):
+        assert lib.lbq_workspace_bytes(desc(), M) == 0  # a bad argument
+        assert lib.lbq_gemm(desc(), V(1 << 40), M, None, V(1 << 41), V(1 << 42), 1 << 62, None) == L.LBQ_ERR_SHAPE
+    assert lib.lbq_workspace_bytes(desc(), 2 ** 30) > 2 * K * 2 ** 30
