@@ -177,7 +177,8 @@ __global__ void pack_q4_kernel(const float* __restrict__ W, int64_t K, int64_t N
     if (real) {
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        double t = h ? rint(static_cast<double>(w[8 * q + i]) / s) : 0.0;
+        // (NaN is nearest to no level: 0. Converted as it is, it set a neighbour's bit)
+        double t = h && !isnan(w[8 * q + i]) ? rint(static_cast<double>(w[8 * q + i]) / s) : 0.0;
         t = t < -8.0 ? -8.0 : (t > 7.0 ? 7.0 : t);
         word |= static_cast<uint32_t>(static_cast<int>(t) + 8) << (4 * ((i >> 1) + 4 * (i & 1)));
       }

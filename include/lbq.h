@@ -74,6 +74,7 @@
  *     (codes and scales of another quantiser can be laid out like this and used).
  *     lbq_pack: s16 = fp16_rne(min(max|w| / 7, 65504)) per group (quotient in fp64),
  *     q = clip(round_half_even(w/s16), -8, 7) + 8, q = 8 everywhere when s16 == 0.
+ *     A NaN weight counts as 0, in the maximum and as a code.
  *     Dequantised weight = s16 * (q - 8).
  *
  * Storage order (all formats). The per-row byte strings above are stored with rows

@@ -158,7 +158,8 @@ static uint16_t q2_scale(const float* w) {
 }
 
 /* 4-bit: the outermost level 7 is the largest weight's, s = max|w| / 7; q - 8 is the
- * nearest integer of w / s (ties to even), clipped to -8..7. A zero scale gives 0. */
+ * nearest integer of w / s (ties to even), clipped to -8..7. A zero scale or a NaN weight
+ * gives 0. */
 static uint16_t q4_scale(const float* w, int n) {
   double mx = 0.0;
   for (int k = 0; k < n; ++k) mx = fmax(mx, fabs((double)w[k]));
@@ -167,7 +168,7 @@ static uint16_t q4_scale(const float* w, int n) {
 }
 
 static int quant4(float w, double s) {
-  if (s == 0.0) return 0;
+  if (s == 0.0 || isnan(w)) return 0;
   double r = rint((double)w / s);
   return (int)(r < -8.0 ? -8.0 : (r > 7.0 ? 7.0 : r));
 }

@@ -375,3 +375,28 @@ def test_sizes_that_32_bits_do_not_count_are_refused(L, fmt):
         assert lib.lbq_workspace_bytes(desc(), M) == 0  # a bad argument
         assert lib.lbq_gemm(desc(), V(1 << 40), M, None, V(1 << 41), V(1 << 42), 1 << 62, None) == L.LBQ_ERR_SHAPE
     assert lib.lbq_workspace_bytes(desc(), 2 ** 30) > 2 * K * 2 ** 30
+
+
+# ----------------------------------------------------------- weights that are not finite
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("fmt", [5, 6])
+def test_a_nan_weight_packs_as_zero_and_alone(L, orc, fmt):
+    """At each place of a word: the bytes of the same matrix with a zero there, and the
+    oracle's; infinities saturate."""
+    K, N = 256, 9
+    W = synth.weights(N, K, 95)
+    Z = W.clone()
+    for i in range(8):
+        W[i, 16 + i] = W[i, 200 + i] = float("nan")
+        Z[i, 16 + i] = Z[i, 200 + i] = 0.0
+    W[8], Z[8] = float("nan"), 0.0
+    got, want = L.lbq_pack(fmt, W.cuda()), L.lbq_pack(fmt, Z.cuda())
+    assert torch.equal(got.codes, want.codes) and torch.equal(got.scales, want.scales)
+    W[3, 5], W[4, 6] = float("inf"), float("-inf")
+    got = L.lbq_pack(fmt, W.cuda())
+    codes, scales = orc.pack(fmt, W.numpy())
+    assert np.array_equal(got.codes.cpu().numpy(), orc.group4(codes))
+    assert np.array_equal(got.scales.cpu().numpy().view(np.uint16), orc.group4(scales))
+    q, s = L.lbq_unpack(got)
+    assert (q[3, 5], q[4, 6], s[3, 0], s[4, 0]) == (7, -8, 65504.0, 65504.0)
