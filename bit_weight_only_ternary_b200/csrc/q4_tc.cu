@@ -467,13 +467,18 @@ __device__ __forceinline__ void decode_word(uint32_t w, __half2 s, uint32_t* out
 // fp32 recomputation of a tile's flagged tokens by all decoder threads d (four a weight
 // row, each every fourth block of K); put(token, row, value) on threads d < kTileN. The
 // flags are shared, so every warp comes to every meeting (a bounded wait, like all).
+// All other warps of both CTAs may wait for its end, which takes 5 to 8 ns a token and
+// weight of a row (256 tokens of K = 17408: 24 ms; of K = 2^21: 4.2 s): it beats in both,
+// once a token.
 template <int kG, typename Meet, typename Put>
 __device__ __forceinline__ void fixup_flagged(const Args& a, const Info& t, const int* xe, float* red,
-                                              int d, Meet meet, Put put) {
+                                              int d, uint32_t beat, Meet meet, Put put) {
   const int row = d & (kTileN - 1), qtr = d / kTileN, n = t.n0 + row;
   const int64_t grow = t.row0 + row;
   for (int i = 0; i < t.cnt; ++i) {
     if (!(xe[i] & 1)) continue;
+    if (d < 2)
+      asm volatile("st.volatile.shared::cluster.b32 [%0], %1;" ::"r"(map_to_rank(beat, d)), "r"(beat_now()) : "memory");
     const int64_t src = a.offsets ? source_row(a.slots, a.topk, a.T, t.m0 + i) : t.m0 + i;
     float acc = 0.0f;
     if (n < a.N && src >= 0) {
@@ -521,9 +526,15 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t bars = base + kOffBar;
   const uint32_t full = bars, empty = full + 8 * kStages, fullR = empty + 8 * kStages,
                  emptyR = fullR + 8 * kRawStages, accum = emptyR + 8 * kRawStages, dfree = accum + 16,
-                 meet = dfree + 16, fullI = meet + 8, emptyI = fullI + 8 * kInfos, tslot = emptyI + 8 * kInfos;
+                 meet = dfree + 16, fullI = meet + 8, emptyI = fullI + 8 * kInfos, tslot = emptyI + 8 * kInfos,
+                 beat = tslot + 4;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  auto wait = [&](uint32_t bar, uint32_t parity, unsigned code, bool give_up = true) {
+    // (a token of the largest K, 2^28, is recomputed in some 2 s)
+    return mbar_wait(bar, parity, a.fault, code, give_up, 2 * kWaitLimitNs, beat);
+  };
   if (tid == 0) {
+    asm volatile("st.shared.b32 [%0], %1;" ::"r"(beat), "r"(0u) : "memory");
     for (int s = 0; s < kStages; ++s) {
       // the stage's four decoder warps of both CTAs, and the first CTA's activation lane
       mbar_init(full + 8 * s, 2 * kDec / 32 / kStages + 1);
@@ -577,7 +588,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const CUtensorMap* map = &tm_x.m[box - 1];
         for (int kb = 0; kb < (t.nkb + 1) / 2 * 2; ++kb, ++blk) {
           const uint32_t s = blk % kStages;
-          if (!mbar_wait(empty + 8 * s, ((blk / kStages) & 1) ^ 1, a.fault, kFaultX)) {
+          if (!wait(empty + 8 * s, ((blk / kStages) & 1) ^ 1, kFaultX)) {
             ok = false;
             break;
           }
@@ -592,7 +603,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // every issued copy lands before the CTAs end (both halves complete on the first's barriers)
       if (rank == 0)
         for (uint32_t q = blk > kStages ? blk - kStages : 0; q < blk; ++q)
-          mbar_wait(full + 8 * (q % kStages), (q / kStages) & 1, a.fault, kFaultX, false);
+          wait(full + 8 * (q % kStages), (q / kStages) & 1, kFaultX, false);
     }
   } else if (warp == 1) {
     // ---------------- MMA issue: eight K = 16 steps a stage, one wait and one commit. The
@@ -605,7 +616,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       bool ok = true;
       for (int i = first; i < total && ok; i += step) {
         // (the tile's info stays until its epilogues, which come after its last instruction)
-        ok = mbar_wait(fullI + 8 * (nt % kInfos), (nt / kInfos) & 1, a.fault, kFaultMma);
+        ok = wait(fullI + 8 * (nt % kInfos), (nt / kInfos) & 1, kFaultMma);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         const Info& t = *reinterpret_cast<const Info*>(sp + kOffInfo + (nt % kInfos) * kInfoBytes + kInfoFields * 4);
@@ -615,13 +626,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t half_k = static_cast<uint32_t>((n / 2 + kBoxStep - 1) / kBoxStep) * (kBoxStep * 128 >> 4);
         // the accumulators are free once the tile before the last has been read, and the last
         // if one of the two is larger than half of them
-        ok = mbar_wait(dfree + 8 * (nt & 1), ((nt >> 1) & 1) ^ 1, a.fault, kFaultMma);
+        ok = wait(dfree + 8 * (nt & 1), ((nt >> 1) & 1) ^ 1, kFaultMma);
         if (ok && nt > 0 && (n > kMaxTileM / 2 || before > kMaxTileM / 2))
-          ok = mbar_wait(dfree + 8 * ((nt & 1) ^ 1), ((nt - 1) >> 1) & 1, a.fault, kFaultMma);
+          ok = wait(dfree + 8 * ((nt & 1) ^ 1), ((nt - 1) >> 1) & 1, kFaultMma);
         before = n;
         for (int kb = 0; kb < (nkb + 1) / 2 * 2; ++kb, ++blk) {
           const uint32_t s = blk % kStages;
-          if (ok) ok = mbar_wait(full + 8 * s, (blk / kStages) & 1, a.fault, kFaultMma);
+          if (ok) ok = wait(full + 8 * s, (blk / kStages) & 1, kFaultMma);
           ok = __all_sync(0xffffffffu, ok);
           if (!ok) break;
           tc_fence_after_sync();
@@ -657,7 +668,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int g0 = t.e * a.groups + t.n0 / 4;
         for (int kb = t.kb0; kb < t.kb0 + t.nkb; kb += kChunkBlocks) {
           const uint32_t r = c % kRawStages;
-          if (!mbar_wait(emptyR + 8 * r, ((c / kRawStages) & 1) ^ 1, a.fault, kFaultW)) {
+          if (!wait(emptyR + 8 * r, ((c / kRawStages) & 1) ^ 1, kFaultW)) {
             ok = false;
             break;
           }
@@ -668,7 +679,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       for (uint32_t q = c > kRawStages ? c - kRawStages : 0; q < c; ++q)
-        mbar_wait(fullR + 8 * (q % kRawStages), (q / kRawStages) & 1, a.fault, kFaultW, false);
+        wait(fullR + 8 * (q % kRawStages), (q / kRawStages) & 1, kFaultW, false);
     }
   } else if (warp == 3) {
     // ---------------- what the decoders have to know of the tiles
@@ -688,7 +699,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
       for (int x = 0; x < kTileN / 32; ++x)
         we[x] = t.n0 + 32 * x + lane < a.N ? __ldcg(a.wexp + row0 + 32 * x + lane) : 0;
-      bool ok = mbar_wait(emptyI + 8 * s, ((k / kInfos) & 1) ^ 1, a.fault, kFaultEpilogue);
+      bool ok = wait(emptyI + 8 * s, ((k / kInfos) & 1) ^ 1, kFaultEpilogue);
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
       bool special = false;
@@ -727,7 +738,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     auto meeting = [&]() {
       __syncwarp();
       if (lane == 0) mbar_arrive(meet);
-      if (ok) ok = mbar_wait(meet, meetings & 1, a.fault, kFaultEpilogue);
+      if (ok) ok = wait(meet, meetings & 1, kFaultEpilogue);
       __syncwarp();
       ++meetings;
     };
@@ -744,7 +755,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int we = info[kInfoRow + 32 * q + lane];
       const float ws = __int_as_float((127 + we) << 23);  // 2^we (we is in -30 .. 4)
       const bool special = ok && t.special;
-      if (ok) ok = mbar_wait(accum + 8 * (done_tiles & 1), (done_tiles >> 1) & 1, a.fault, kFaultEpilogue);
+      if (ok) ok = wait(accum + 8 * (done_tiles & 1), (done_tiles >> 1) & 1, kFaultEpilogue);
       __syncwarp();
       tc_fence_after_sync();
       // this warp's columns 16 grp + 64 c + (0..15), the accumulators summed in order
@@ -814,7 +825,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         release();
         if (special)
-          fixup_flagged<kG>(a, t, xe, red, d, meeting, [&](int m, int r, float y) {
+          fixup_flagged<kG>(a, t, xe, red, d, beat, meeting, [&](int m, int r, float y) {
             if (!ok) return;
             const int64_t o = static_cast<int64_t>(t.m0 + m) * a.N + t.n0 + r;
             if (part) part[o] = y;
@@ -827,7 +838,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
     uint32_t chunk0 = 0;  // chunks of the tiles before
     for (int i = first; i < total; i += step, ++tiles) {
-      if (ok) ok = mbar_wait(fullI + 8 * (tiles % kInfos), (tiles / kInfos) & 1, a.fault, kFaultEpilogue);
+      if (ok) ok = wait(fullI + 8 * (tiles % kInfos), (tiles / kInfos) & 1, kFaultEpilogue);
       __syncwarp();
       const int* const info = info_of(tiles);
       const int we = ok ? info[kInfoRow + row] : 0;
@@ -841,7 +852,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t nch = static_cast<uint32_t>(nkb + kChunkBlocks - 1) / kChunkBlocks;
       for (uint32_t c = ((chunk0 & 1) ^ static_cast<uint32_t>(grp >> 1)); c < nch; c += 2) {
         const uint32_t r = (chunk0 + c) % kRawStages;
-        if (ok) ok = mbar_wait(fullR + 8 * r, ((chunk0 + c) / kRawStages) & 1, a.fault, kFaultDecode);
+        if (ok) ok = wait(fullR + 8 * r, ((chunk0 + c) / kRawStages) & 1, kFaultDecode);
         __syncwarp();
         uint32_t w[16];
 #pragma unroll
@@ -853,7 +864,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) mbar_arrive(emptyR + 8 * r);
         // (an odd number of blocks: the last chunk's second one is zeros to its group)
         const uint32_t use = (chunk0 + c) / 2;  // the stage's uses before this one
-        if (ok) ok = mbar_wait(empty + 8 * grp, (use & 1) ^ 1, a.fault, kFaultDecode);
+        if (ok) ok = wait(empty + 8 * grp, (use & 1) ^ 1, kFaultDecode);
         __syncwarp();
         tc_fence_after_sync();
 #pragma unroll

@@ -69,19 +69,29 @@ __device__ __forceinline__ bool mbar_try_wait_sleep(uint32_t bar, uint32_t parit
   return ok != 0;
 }
 
+// Work of unknown length that others wait for leaves the time in a word of shared memory
+// as it goes on (in units of 2^20 ns).
+__device__ __forceinline__ uint32_t beat_now() { return static_cast<uint32_t>(global_ns() >> 20); }
+__device__ __forceinline__ uint32_t since_beat(uint32_t beat) {
+  uint32_t v;
+  asm volatile("ld.volatile.shared.b32 %0, [%1];" : "=r"(v) : "r"(beat));
+  return beat_now() - v;
+}
+
 // Waits for the phase with the given parity to complete. Gives up (returns false)
 // after kWaitLimitNs, recording `code` in *fault, or -- unless give_up_after_fault is
-// false -- as soon as another wait has already given up.
+// false -- as soon as another wait has already given up. With `beat` (such a word's
+// address) only if that is as old.
 __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, unsigned* fault,
                                           unsigned code, bool give_up_after_fault = true,
-                                          uint64_t limit_ns = kWaitLimitNs) {
+                                          uint64_t limit_ns = kWaitLimitNs, uint32_t beat = 0) {
   if (mbar_try_wait(bar, parity)) return true;
   const uint64_t t0 = global_ns();
   for (uint32_t i = 1;; ++i) {
     if (mbar_try_wait_sleep(bar, parity, 1000000u)) return true;
     if ((i & 15) == 0) {
       if (give_up_after_fault && *reinterpret_cast<volatile unsigned*>(fault) != 0) return false;
-      if (global_ns() - t0 > limit_ns) {
+      if (global_ns() - t0 > limit_ns && (!beat || since_beat(beat) > static_cast<uint32_t>(limit_ns >> 20))) {
         atomicExch(fault, code);
         return false;
       }

@@ -383,7 +383,8 @@ lbq_status lbq_expert_gemm(const lbq_weights* w, int32_t E, const uint16_t* X, i
  * wait that runs out records a non-zero *code (3: shared-memory layout of the
  * batch-1 product, 4-9: tensor-core product stages, 10: the batch-1 product's
  * weight copies, 11: lbq_selftest_wait, 12: unused (lbq_gemv_batch has no waits),
- * 13: lbq_gemv_batch's shared-memory layout, 14-18: 4-bit tensor-core product stages)
+ * 13: lbq_gemv_batch's shared-memory layout, 14-18: 4-bit tensor-core product stages,
+ * whose limit is 4 s, and 4 s behind the last row that is recomputed in fp32)
  * and the kernel returns early with incomplete outputs instead of hanging. Synchronises
  * the device.
  * Returns LBQ_OK with *code = 0 when no wait gave up, LBQ_ERR_DEVICE_WAIT with the

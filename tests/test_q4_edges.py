@@ -400,3 +400,28 @@ def test_a_nan_weight_packs_as_zero_and_alone(L, orc, fmt):
     assert np.array_equal(got.scales.cpu().numpy().view(np.uint16), orc.group4(scales))
     q, s = L.lbq_unpack(got)
     assert (q[3, 5], q[4, 6], s[3, 0], s[4, 0]) == (7, -8, 65504.0, 65504.0)
+
+
+# --------------------------------------------------------------- rows recomputed in fp32
+
+@pytest.mark.gpu
+def test_rows_recomputed_for_longer_than_a_wait(L):
+    """A whole tile of tokens that fp16 cannot hold, of more weights than are recomputed in
+    the time that a wait lasts (5 to 8 ns a token and weight of a row, 6 s here).
+
+    Sums: a thread adds K / 512 groups of 128 terms each, then four threads' sums: at most
+    K / 512 + 128 + 3 additions one after another, each off by 2^-24 of S."""
+    K, N, R = 3 << 20, 4, 256
+    gen = torch.Generator("cuda").manual_seed(9)
+    c = torch.randint(0, 256, (1, 1, 2 * K), dtype=torch.uint8, device="cuda", generator=gen)
+    s = (torch.rand(1, 1, 4 * (K // 128), device="cuda", generator=gen) * 0.01 + 0.001).half().view(torch.int16)
+    ew = L.ExpertWeights(6, K, N, 1, c, s)
+    X = torch.randn(R, K, device="cuda", generator=gen, dtype=torch.bfloat16)
+    X[:, 77] = 2.0 ** -60
+    Y = L.lbq_expert_gemm(ew, X, torch.tensor([0, R], dtype=torch.int32, device="cuda"))
+    assert L.lbq_device_fault() == 0
+    W = _dense(L, L.PackedWeights(6, K, N, c[0], s[0]))
+    for r in range(0, R, 16):
+        x = X[r:r + 16].double()
+        want, S = x @ W.t(), x.abs() @ W.abs().t()
+        assert ((Y[r:r + 16].double() - want).abs() <= 2.0 ** -8 * want.abs() + (K / 512 + 131) * 2.0 ** -24 * S).all()
