@@ -425,3 +425,54 @@ def test_rows_recomputed_for_longer_than_a_wait(L):
         x = X[r:r + 16].double()
         want, S = x @ W.t(), x.abs() @ W.abs().t()
         assert ((Y[r:r + 16].double() - want).abs() <= 2.0 ** -8 * want.abs() + (K / 512 + 131) * 2.0 ** -24 * S).all()
+
+
+# ----------------------------------------- few rows and many: what is rounded, and where
+
+def _few(M, N, K):
+    """Whether lbq_gemm takes M rows on the path that rounds nothing before the output."""
+    return M <= 8 or (M <= 32 and (M + 7) // 8 * N <= 2 ** 27 // K)
+
+
+def _held(Y, X, W, f16, what):
+    want, S = X.double() @ W.t(), X.double().abs() @ W.abs().t()
+    err = (Y.double() - want).abs()
+    lim = 2.0 ** -8 * want.abs() + (2.0 ** -12 + (2.0 ** -11 if f16 else 0.0)) * S
+    assert (err <= lim).all(), f"{what}: {(err > lim).sum()} out of bound, worst {(err / lim).max()}"
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("fmt", [5, 6])
+@pytest.mark.parametrize("N,K,first", [(300, 1024, 33), (520, 5120, 33), (40000, 256, 33), (7168, 5120, 25),
+                                       (10240, 5120, 17), (34816, 5120, 9)])
+def test_dense_rows_on_both_sides_of_the_change(L, fmt, N, K, first):
+    """The first number of rows that goes to the tensor cores, the one before, and others."""
+    gen = torch.Generator("cuda").manual_seed(N)
+    pw = L.lbq_pack(fmt, torch.randn(N, K, device="cuda", generator=gen) * 0.02)
+    W = _dense(L, pw)
+    X = torch.randn(64, K, device="cuda", generator=gen).to(torch.bfloat16)
+    assert not _few(first, N, K) and _few(first - 1, N, K)
+    for M in sorted({2, 4, 5, 8, 9, 16, 17, 24, 25, 32, 33, 64}):
+        Y = L.lbq_gemm(pw, X[:M])
+        _held(Y, X[:M], W, not _few(M, N, K), f"{M} rows")
+    assert L.lbq_device_fault() == 0
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("fmt", [5, 6])
+@pytest.mark.parametrize("E,N,K", [(1, 70, 640), (6, 130, 1024), (40, 33, 384)])
+def test_expert_rows_on_both_sides_of_the_change(L, fmt, E, N, K):
+    """Up to eight slots an expert nothing is rounded before the output, however uneven."""
+    gen = torch.Generator("cuda").manual_seed(E)
+    ew = L.pack_experts(fmt, torch.randn(E, N, K, device="cuda", generator=gen) * 0.02)
+    W = [_dense(L, L.PackedWeights(fmt, K, N, ew.codes[e], ew.scales[e])) for e in range(E)]
+    X = torch.randn(8 * E + 1, K, device="cuda", generator=gen).to(torch.bfloat16)
+    for R in (1, E, E + 1, 4 * E, 8 * E, 8 * E + 1):
+        cuts = torch.randint(0, R + 1, (E - 1,), device="cuda", generator=gen).sort().values
+        for inner in (cuts, torch.zeros_like(cuts), torch.full_like(cuts, R)):
+            off = torch.cat([inner.new_zeros(1), inner, inner.new_full((1,), R)]).to(torch.int32)
+            Y, o = L.lbq_expert_gemm(ew, X[:R], off), off.tolist()
+            for e in range(E):
+                if o[e] < o[e + 1]:
+                    _held(Y[o[e]:o[e + 1]], X[o[e]:o[e + 1]], W[e], R > 8 * E, f"{R} rows, expert {e}")
+    assert L.lbq_device_fault() == 0
