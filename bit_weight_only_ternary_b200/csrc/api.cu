@@ -180,7 +180,8 @@ lbq_status check_routing(int64_t T, int32_t topk, int32_t E) {
 }
 
 // The experts' products: few rows an expert run on the warp-level matrix instructions,
-// more on the tensor cores. The routing is on the device, so the rule takes the average.
+// more on the tensor cores. The routing is on the device, so the rule takes the average of
+// the slots, those left out among them.
 // Measured: 128 experts of 2048 x 1536, 7 rows each 70.6 / 77.0 us, 8 rows 77.0 / 78.0, 9
 // rows 83.2 / 78.8; 16 of 5120 x 5120, 8 rows 82.1 / 87.5, 9 rows 85.6 / 87.5; 8 of 2048 x
 // 1024, 6 rows 15.1 / 16.5, 8 rows 16.5 / 16.4.

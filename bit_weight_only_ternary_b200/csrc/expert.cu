@@ -310,6 +310,7 @@ __global__ void __launch_bounds__(kRowThreads, 4)
   }
 }
 
+// (The form for single columns, odd widths and addresses, spills 68 bytes a thread.)
 template <int kVec>
 __global__ void __launch_bounds__(kRowThreads, 3)
     combine_grad_kernel(const uint16_t* dout, const uint16_t* Y, const RouteArgs a, int64_t T, uint16_t* dY,

@@ -46,7 +46,8 @@
 //    the other slots are filled once the table is built (their shared-memory writes
 //    slowed the build down). Kernels that let their successor start early (the
 //    batch-1 ones, the 4-bit products and the expert calls) never write packed
-//    weights; any other kernel has completed before this one starts. x, y and the workspace are touched only after the wait.
+//    weights; any other kernel has completed before this one starts. x, y and the
+//    workspace are touched only after the wait.
 #include <type_traits>
 
 #include "lut.cuh"

@@ -230,10 +230,15 @@ lbq_status lbq_gemv_f32(const lbq_weights* w, const uint16_t* x, const int8_t* D
  * span more than about 2^31) is recomputed in fp32 on the CUDA cores, which is
  * slower but keeps the same accuracy. 1-bit and 2-bit weights: a CUDA-core kernel
  * in which each warp decodes a weight row's blocks once for up to 8 activation rows.
- * 4-bit weights: few rows (up to 8, or up to 32 of matrices that are not large) on
- * warp-level matrix instructions with nothing rounded before the output; more rows as
- * ternary ones on the tensor cores, with the dequantised weights rounded to fp16 (a
- * relative 2^-11 each; a row's scales below 2^-25 of its largest one count as subnormal).
+ * 4-bit weights: few rows (up to 8, or up to 32 while ceil(M / 8) N K <= 2^27) on
+ * warp-level matrix instructions with nothing rounded before the output (a group's sum of
+ * (q - 8) x is formed in fp32, then scaled); more rows as ternary ones on the tensor
+ * cores, with the dequantised weights rounded to fp16 (a relative 2^-11 each; a row's
+ * scales below 2^-25 of its largest one count as subnormal), so that up to one output in
+ * ten rounds to a neighbouring bf16 value. Rows of zeros are ordinary rows; rows that span
+ * more than 2^31 are common behind a squared relu or a wide gelu, and cost far more (21 ms
+ * for 0.16 with 1024 rows behind a squared relu on 17408 x 5120). A scale that is infinite
+ * or NaN makes its row's outputs so, infinite or NaN by the path.
  * Same formats, D and workspace rules as lbq_gemv (workspace for this M, from
  * lbq_workspace_bytes). */
 lbq_status lbq_gemm(const lbq_weights* w, const uint16_t* X, int64_t M, const int8_t* D,
@@ -368,7 +373,9 @@ size_t lbq_expert_workspace_bytes(const lbq_weights* w, int32_t E, int64_t R);
  * captured; offsets are clamped to 0 .. R, offsets that descend anywhere leave all of Y
  * as it was, and a slot of no token gives a row of zeros.
  * Workspace as lbq_expert_workspace_bytes; calls sharing one must not overlap. Each sum
- * is fp32, rounded to bf16 once.
+ * is fp32, rounded to bf16 once. Up to R = 8 E the products are lbq_gemm's of few rows,
+ * with more its products of many (weights rounded to fp16); R counts all slots, those left
+ * out among them. There is no call for the gradient with respect to X.
  * Errors: those of lbq_gemv, LBQ_ERR_SHAPE (E, T, R or topk out of range). */
 lbq_status lbq_expert_gemm(const lbq_weights* w, int32_t E, const uint16_t* X, int64_t T,
                            const int32_t* offsets, const int32_t* slots, int32_t topk, int64_t R,
