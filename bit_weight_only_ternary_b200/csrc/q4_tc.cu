@@ -33,12 +33,13 @@
 // Every wait is bounded (sm100_async.cuh). Measured: 4096 tokens x 5120 x 34816 in 0.92 ms
 // by a cool chip, 1.07 to 1.11 in a row of passes (1.59 to 1.31 PFLOP/s, by the power that
 // is left), 333 x 5120 x 7001 in 30 us, 4096 tokens x 8 of 128 experts of 2048 x 1536 in 250
-// us with other inputs each pass (820 TFLOP/s) and 215 to 226 in a graph of the same one
-// again and again, which finds its weights in L2 (the times beside the choices below are
-// of such graphs); 45 us are the preparation. A row that is recomputed in fp32 costs 5 to 8 ns
-// a weight in every weight tile: 1024 rows of 17408 x 5120 take 0.14 to 0.16 ms, with one
-// in 16 so 3.1, behind a squared relu (two rows in five) 21. A block of 128 K cannot take less than 0.27 us: the tensor cores read its
-// weights, 128 x 128 a CTA, from tensor memory in 8 x 64 cycles.
+// to 260 us with other inputs each pass (820 to 790 TFLOP/s) and 215 to 226 in a graph of
+// the same one again and again, which finds its weights in L2 (the times beside the choices
+// below are of such graphs); 45 us are the preparation. A row that is recomputed in fp32
+// costs 5 to 8 ns a weight in every weight tile: 1024 rows of 17408 x 5120 take 0.14 to 0.16
+// ms, with one in 16 so 3.1, behind a squared relu (two rows in five) 21. A block of 128 K
+// cannot take less than 0.27 us: the tensor cores read its weights, 128 x 128 a CTA, from
+// tensor memory in 8 x 64 cycles.
 #include <cudaTypedefs.h>
 
 #include <algorithm>
