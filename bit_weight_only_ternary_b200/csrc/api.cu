@@ -99,12 +99,15 @@ lbq_status check_operands(const lbq_weights* w, const void* x, int64_t M, const 
   return LBQ_OK;
 }
 
-// The packed bytes of E matrices behind one another.
-Span codes_of(const lbq_weights* w, int64_t E = 1) {
-  return {w->codes, static_cast<size_t>(E * lbq::g4_rows(w->N)) * static_cast<size_t>(w->code_stride)};
+// The packed bytes of E matrices behind one another (L: their layout). What lies behind the
+// last group's own bytes is not theirs: w may be a range of K of a wider matrix.
+Span codes_of(const lbq_weights* w, const Layout& L, int64_t E = 1) {
+  const size_t groups = static_cast<size_t>(E * lbq::g4_rows(w->N) / 4);
+  return {w->codes, 4 * ((groups - 1) * static_cast<size_t>(w->code_stride) + static_cast<size_t>(L.code_stride))};
 }
-Span scales_of(const lbq_weights* w, int64_t E = 1) {
-  return {w->scales, static_cast<size_t>(E * lbq::g4_rows(w->N)) * static_cast<size_t>(w->scale_stride) * 2};
+Span scales_of(const lbq_weights* w, const Layout& L, int64_t E = 1) {
+  const size_t groups = static_cast<size_t>(E * lbq::g4_rows(w->N) / 4);
+  return {w->scales, 8 * ((groups - 1) * static_cast<size_t>(w->scale_stride) + static_cast<size_t>(w->K / L.block))};
 }
 
 // (y_bytes: of an output)
@@ -119,7 +122,7 @@ lbq_status check_product(const lbq_weights* w, const void* x, int64_t M, const i
   }
   if (lbq::is_q4(w->fmt) &&
       !disjoint({{y, y_bytes * static_cast<size_t>(M) * w->N}, {need ? ws : nullptr, need}},
-                {{x, 2 * static_cast<size_t>(M) * w->K}, codes_of(w), scales_of(w)}))
+                {{x, 2 * static_cast<size_t>(M) * w->K}, codes_of(w, *L), scales_of(w, *L)}))
     return LBQ_ERR_ARG;
   return LBQ_OK;
 }
@@ -483,7 +486,7 @@ lbq_status lbq_expert_gemm(const lbq_weights* w, int32_t E, const uint16_t* X, i
   }
   if (!disjoint({{Y, 2 * static_cast<size_t>(R) * w->N}, {need ? workspace : nullptr, need}},
                 {{X, 2 * static_cast<size_t>(T) * w->K}, {offsets, 4 * (static_cast<size_t>(E) + 1)},
-                 {slots, 4 * static_cast<size_t>(R)}, codes_of(w, E), scales_of(w, E)}))
+                 {slots, 4 * static_cast<size_t>(R)}, codes_of(w, L, E), scales_of(w, L, E)}))
     return LBQ_ERR_ARG;
   const lbq_expert_rows rows = {X, offsets, slots, Y, T, R, topk, E};
   return from_cuda(expert_few(E, R) ? lbq_launch_q4_expert_few(w, rows, workspace, as_stream(stream))

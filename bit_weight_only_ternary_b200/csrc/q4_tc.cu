@@ -1064,8 +1064,10 @@ cudaError_t launch(const lbq_weights* w, const Plan& plan, const lbq_expert_rows
     return encode(m, dt, 2, p, dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, sw,
                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
   };
-  const cuuint64_t G = static_cast<cuuint64_t>(E) * ng, cw = static_cast<cuuint64_t>(w->code_stride),
-                   se = static_cast<cuuint64_t>(w->scale_stride) * 4;
+  // (rows of weights end with K: what a chunk holds behind it arrives as zeros, not from the
+  // padding or from behind the last group)
+  const cuuint64_t G = static_cast<cuuint64_t>(E) * ng, cw = static_cast<cuuint64_t>(w->K / 2),
+                   se = static_cast<cuuint64_t>(w->K / kG) * 4;
   // (dense: only the boxes of the full and the last token tile are used)
   const int64_t last = rows - static_cast<int64_t>(plan.ntm - 1) * plan.tile_m;
   auto box_of = [](int64_t cnt) { return static_cast<int>((((cnt + 15) / 16 * 16) / 2 + kBoxStep - 1) / kBoxStep) - 1; };
@@ -1080,9 +1082,11 @@ cudaError_t launch(const lbq_weights* w, const Plan& plan, const lbq_expert_rows
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
       return cudaErrorInvalidValue;
   }
-  if (!map(&tw, CU_TENSOR_MAP_DATA_TYPE_UINT32, const_cast<void*>(w->codes), cw, G, cw * 4, kGroupWords, kTileN / 4,
+  if (!map(&tw, CU_TENSOR_MAP_DATA_TYPE_UINT32, const_cast<void*>(w->codes), cw, G,
+           static_cast<cuuint64_t>(w->code_stride) * 4, kGroupWords, kTileN / 4,
            CU_TENSOR_MAP_SWIZZLE_NONE) ||
-      !map(&ts, CU_TENSOR_MAP_DATA_TYPE_UINT16, const_cast<void*>(w->scales), se, G, se * 2,
+      !map(&ts, CU_TENSOR_MAP_DATA_TYPE_UINT16, const_cast<void*>(w->scales), se, G,
+           static_cast<cuuint64_t>(w->scale_stride) * 8,
            (kChunkBlocks * kTileK / kG) * 4, kTileN / 4, CU_TENSOR_MAP_SWIZZLE_NONE))
     return cudaErrorInvalidValue;
 

@@ -476,3 +476,29 @@ def test_expert_rows_on_both_sides_of_the_change(L, fmt, E, N, K):
                 if o[e] < o[e + 1]:
                     _held(Y[o[e]:o[e + 1]], X[o[e]:o[e + 1]], W[e], R > 8 * E, f"{R} rows, expert {e}")
     assert L.lbq_device_fault() == 0
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("fmt,K,lo,hi", [(5, 2048, 1024, 2048), (5, 2304, 1152, 2304), (6, 2048, 1024, 2048),
+                                         (6, 3328, 1024, 3328), (5, 1536, 256, 1408)])
+def test_a_range_of_k_of_a_wider_matrix(L, fmt, K, lo, hi):
+    """Weights lo .. hi - 1 of every row, as a view; behind the last group's own bytes lies
+    the output, which is neither read nor taken for a part of the matrix."""
+    N, g = 10, {5: 32, 6: 128}[fmt]
+    gen = torch.Generator("cuda").manual_seed(K)
+    pw = L.lbq_pack(fmt, torch.randn(N, K, device="cuda", generator=gen) * 0.02)
+    W = _dense(L, pw)[:, lo:hi]
+    G, row = pw.codes.shape
+    X = torch.randn(60, hi - lo, device="cuda", generator=gen).to(torch.bfloat16)
+    end = (G - 1) * row + 2 * hi  # of the last group's bytes that belong to the range
+    arena = torch.full((end + 2 * 60 * N,), 0xff, dtype=torch.uint8, device="cuda")
+    arena[:end] = pw.codes.view(-1)[:end]
+    codes = arena.as_strided((G, 2 * (hi - lo)), (row, 1), 2 * lo)
+    scales = pw.scales[:, 4 * lo // g:]
+    part = L.PackedWeights(fmt, hi - lo, N, codes, scales)
+    for M in (1, 5, 60):
+        Y = arena[end:end + 2 * M * N].view(torch.bfloat16).view(M, N)
+        L.lbq_gemv(part, X[0], y=Y[0]) if M == 1 else L.lbq_gemm(part, X[:M], Y=Y)
+        _held(Y, X[:M], W, M > 32, f"{M} rows")
+    assert torch.equal(arena[:end], pw.codes.view(-1)[:end])
+    assert L.lbq_device_fault() == 0
